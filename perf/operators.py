@@ -234,11 +234,10 @@ def _logits_inputs(case, seed):
             have = have | (1 << (draft.long() % 32))[..., None]
             words[:, :-1].scatter_(2, at, torch.where(have >= 2 ** 31, have - 2 ** 32, have))
         state["mask"] = words.to(torch.int32)
-    if case["op"] == "verify":
-        state["temperature"] = torch.full((b,), case["temperature"], device="cuda")
-        if case["temperature"]:
-            state["accept_u"] = uniform(b, max(t - 1, 0))
-            state["noise"] = torch.empty((b, v), device="cuda").exponential_(generator=g).clamp_(min=1e-30)
+    if case["op"] == "verify" and case["temperature"]:
+        state.update(temperature=torch.full((b,), case["temperature"], device="cuda"),
+                     accept_u=uniform(b, max(t - 1, 0)),
+                     noise=torch.empty((b, v), device="cuda").exponential_(generator=g).clamp_(min=1e-30))
     return state
 
 
@@ -403,7 +402,7 @@ def run(s):
                                    "presence", "bias_ids", "bias_values", "mask")}
     if op == "process":
         return s["verifier"].process(s["logits"], draft=s["draft"], **rules)
-    tokens, accepted, logprob = s["verifier"].run(s["logits"], s["draft"], temperature=s["temperature"],
+    tokens, accepted, logprob = s["verifier"].run(s["logits"], s["draft"], temperature=s.get("temperature"),
                                                   accept_u=s.get("accept_u"), noise=s.get("noise"),
                                                   return_logprob=True, **rules)
     return {"tokens": tokens, "accepted": accepted, "logprob": logprob}
