@@ -14,7 +14,8 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-CSRC = os.path.join(PKG, "csrc")
+CSRC = os.path.join(PKG, "csrc")                # the rollout
+VERIFY_CSRC = os.path.join(PKG, "csrc_verify")  # the operators of domino_verify.h
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdomino_rollout.so")
 
@@ -33,7 +34,8 @@ def _hipcc():
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+    return sorted(os.path.join(d, f) for d in (CSRC, VERIFY_CSRC) for f in os.listdir(d)
+                  if f.endswith(".hip"))
 
 
 def build(verbose: bool = False) -> str:
@@ -53,7 +55,7 @@ def build(verbose: bool = False) -> str:
             print(out, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(4) as ex:
+    with ThreadPoolExecutor(8) as ex:
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + ".tmp"
     res = subprocess.run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp],

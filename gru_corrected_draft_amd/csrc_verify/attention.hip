@@ -1,0 +1,442 @@
+// Paged attention of new tokens over a key-value cache, and the append that
+// fills it.  See attention.h for rows, key tiles and helpers.
+#include <cmath>
+#include <new>
+
+#include "../../include/domino_verify.h"
+#include "attention.h"
+#include "handle.h"
+
+// ---------------------------------------------------------------- append
+// A copy: one 16-byte piece per thread, keys in the first half of the grid's
+// y, values in the second.  Bound by the launch for a decoding step and by
+// memory for a prompt; rows of a head are contiguous on both sides.
+struct AppendArgs {
+  const void* src[2];
+  void* dst[2];
+  int64_t tok[2], headi[2];
+  int64_t page, head;
+  int32_t row, num_pages, pieces;  // pieces: 16-byte pieces of a row
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t page_shift, elem;
+  const int32_t* kv_len;
+  const int32_t* q_start;
+  int32_t tokens, max_new, max_kv, kv_heads;
+};
+
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+  const int which = blockIdx.y & 1, b = blockIdx.y >> 1;
+  const Request r = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  if (r.bad) return;
+  const int per_token = a.kv_heads * a.pieces;
+  const int64_t total = (int64_t)r.n * per_token;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int t = (int)(i / per_token), rest = (int)(i - (int64_t)t * per_token);
+    const int h = rest / a.pieces, piece = rest - h * a.pieces;
+    const int pos = r.kv - r.n + t;
+    if (pos < 0) continue;
+    const int page = a.table[b * a.table_stride + (pos >> a.page_shift)];
+    if (page < 0 || page >= a.num_pages) continue;
+    const int row = pos & ((1 << a.page_shift) - 1);
+    const char* s = (const char*)a.src[which] +
+                    ((r.q0 + t) * a.tok[which] + h * a.headi[which]) * a.elem + piece * 16;
+    char* d = (char*)a.dst[which] +
+              (page * a.page + h * a.head + (int64_t)row * a.row) * a.elem + piece * 16;
+    *(u32x4*)d = *(const u32x4*)s;
+  }
+}
+
+// ---------------------------------------------------------------- attention, 32-bit products
+// Four waves share a tile of 16 rows and take 16-key tiles in turn, each with
+// its own running maximum and sum; the four are joined in LDS at the end.
+// The scores are computed transposed (keys x rows), so the row's maximum and
+// sum stay in the row's lanes and the accumulator registers of the scores are
+// the second product's operand as they are: lane (n = l % 16, q = l / 16)
+// holds the scores of row n and keys 4 q .. 4 q + 3, and the product over keys
+// takes key 4 q + i in its i-th step.  The head dimension is dealt to the
+// lanes so that every load is 16 bytes: step i of the first product takes
+// element 16 c + 4 q + i, and output row m of accumulator (blk, j) is element
+// 64 blk + 4 m + j.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<bf16_t>(const bf16_t* p) {
+  const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+  return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                     __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u));
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
+  constexpr int KT = 16, ROWS = 16, C = D / 16, NB = D / 64;
+  __shared__ float s_o[4][ROWS][D + 4];
+  __shared__ float s_m[4][ROWS], s_l[4][ROWS];
+  __shared__ int s_bad[4];
+  const int b = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * ROWS;
+  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  const int rows = req.n * a.group;
+  if (r0 >= rows) return;
+  const int lane = threadIdx.x & 63, w = wave_index(), n = lane & 15, q4 = lane >> 4;
+  const int last = min(r0 + ROWS, rows) - 1;
+  const KeySpan span = key_span<KT>(req, r0 / a.group, last / a.group, a.window, a.sinks);
+  const int row = min(r0 + n, last);
+  const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+  const int pos = req.kv - req.n + tok;
+  const T* qp = (const T*)a.q + (req.q0 + tok) * a.q_tok + hq * a.q_head + 4 * q4;
+  float4 Q[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) Q[c] = load4<T>(qp + 16 * c);
+  v4f O[NB][4];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) O[i][j] = zero4();
+  float m = -INFINITY, l = 0.f;
+  bool bad = req.bad;
+  for (int i = w; i < span.count; i += 4) {
+    const int k0 = tile_of(span, i) * KT;
+    int page = a.table[b * a.table_stride + (k0 >> a.page_shift)];
+    if (page < 0 || page >= a.num_pages) {
+      bad = true;
+      break;
+    }
+    const int64_t base = page * a.page + h * a.head + (int64_t)(k0 & ((1 << a.page_shift) - 1)) * a.row;
+    const T* kp = (const T*)a.k + base + (int64_t)n * a.row + 4 * q4;
+    v4f s = zero4();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float4 k = load4<T>(kp + 16 * c);
+      s = mfma_f32(k.x, Q[c].x, s);
+      s = mfma_f32(k.y, Q[c].y, s);
+      s = mfma_f32(k.z, Q[c].z, s);
+      s = mfma_f32(k.w, Q[c].w, s);
+    }
+    const bool edge = !all_visible(span, k0, KT, a.window, a.sinks);
+    if (edge) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!visible(k0 + 4 * q4 + j, pos, a.window, a.sinks)) s[j] = -INFINITY;
+    }
+    float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float mn = fmaxf(m, top);
+    const float ref = mn == -INFINITY ? 0.f : mn * a.scale_log2;
+    const float alpha = exp2f(m * a.scale_log2 - ref);
+    float p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = exp2f(__builtin_fmaf(s[j], a.scale_log2, -ref));
+    l = l * alpha + ((p[0] + p[1]) + (p[2] + p[3]));
+    m = mn;
+#pragma unroll
+    for (int x = 0; x < NB; ++x)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) O[x][j] *= alpha;
+    const T* vp = (const T*)a.v + base + (int64_t)(4 * q4) * a.row + 4 * n;
+    float4 V[4][NB];
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        V[j][x] = load4<T>(vp + (int64_t)j * a.row + 64 * x);
+        odd |= nonfinite(V[j][x].x) || nonfinite(V[j][x].y) || nonfinite(V[j][x].z) ||
+               nonfinite(V[j][x].w);
+      }
+    if (edge && __any(odd)) {
+      // a product would multiply a row's zero weight by an infinity or NaN
+      // that the row does not see: add key by key, to the rows that see it
+      for (int kk = 0; kk < KT; ++kk) {
+        const float mine = (kk & 2) ? ((kk & 1) ? p[3] : p[2]) : ((kk & 1) ? p[1] : p[0]);
+        const float pk = __shfl(mine, (kk >> 2) * 16 + n, 64);
+        if (!visible(k0 + kk, pos, a.window, a.sinks)) continue;
+        const T* vk = (const T*)a.v + base + (int64_t)kk * a.row;
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = load4<T>(vk + 64 * x + 16 * q4 + 4 * e);
+            O[x][0][e] += pk * v.x;
+            O[x][1][e] += pk * v.y;
+            O[x][2][e] += pk * v.z;
+            O[x][3][e] += pk * v.w;
+          }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          O[x][0] = mfma_f32(V[j][x].x, p[j], O[x][0]);
+          O[x][1] = mfma_f32(V[j][x].y, p[j], O[x][1]);
+          O[x][2] = mfma_f32(V[j][x].z, p[j], O[x][2]);
+          O[x][3] = mfma_f32(V[j][x].w, p[j], O[x][3]);
+        }
+    }
+  }
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (lane < 16) {
+    s_m[w][n] = m;
+    s_l[w][n] = l;
+  }
+  if (lane == 0) s_bad[w] = bad;
+#pragma unroll
+  for (int x = 0; x < NB; ++x)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(&s_o[w][n][64 * x + 16 * q4 + 4 * e]) =
+          make_float4(O[x][0][e], O[x][1][e], O[x][2][e], O[x][3][e]);
+  __syncthreads();
+  const bool spoilt = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+  for (int i = threadIdx.x; i < ROWS * D; i += 256) {
+    const int rr = i / D, d = i - rr * D;
+    if (r0 + rr > last) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) top = fmaxf(top, s_m[x][rr]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float num = 0.f, den = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float f = exp2f((s_m[x][rr] - ref) * a.scale_log2);
+      den += f * s_l[x][rr];
+      // a wave that saw no key of this row holds only zeros
+      if (s_m[x][rr] != -INFINITY) num += f * s_o[x][rr][d];
+    }
+    float o = den == 0.f && top == -INFINITY ? 0.f : num / den;
+    if (spoilt) o = NAN;
+    const int tk = (r0 + rr) / a.group, hd = h * a.group + (r0 + rr) - tk * a.group;
+    store_elem((T*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + d, o);
+    if (d == 0 && a.lse)
+      a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] =
+          spoilt ? NAN : (den == 0.f && top == -INFINITY ? -INFINITY : top * a.scale + logf(den));
+  }
+}
+
+// ---------------------------------------------------------------- handle
+struct domino_attention : HandleBase {
+  domino_attention_config_t cfg;
+};
+
+static thread_local char t_err[256] = "";
+
+extern "C" domino_status_t domino_attention_create(const domino_attention_config_t* cfg,
+                                                   domino_attention_t** out) {
+  if (!out) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: out is NULL");
+  *out = nullptr;
+  if (!cfg) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: cfg is NULL");
+  if (cfg->q_heads < 1 || cfg->kv_heads < 1 || cfg->q_heads % cfg->kv_heads)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG,
+               "create: q_heads must be a positive multiple of kv_heads (got %d and %d)",
+               cfg->q_heads, cfg->kv_heads);
+  if (cfg->max_requests < 1 || cfg->max_requests > 1024)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG, "create: max_requests must be in [1, 1024]");
+  if (cfg->dtype != DOMINO_DTYPE_BF16 && cfg->dtype != DOMINO_DTYPE_FP32)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG,
+               "create: dtype must be DOMINO_DTYPE_BF16 or DOMINO_DTYPE_FP32");
+  if (cfg->head_dim != 64 && cfg->head_dim != 128 && cfg->head_dim != 256)
+    return say(t_err, DOMINO_ERR_UNSUPPORTED, "create: head_dim must be 64, 128 or 256 (got %d)",
+               cfg->head_dim);
+  if (cfg->page_size < 16 || cfg->page_size > 4096 || (cfg->page_size & (cfg->page_size - 1)))
+    return say(t_err, DOMINO_ERR_UNSUPPORTED,
+               "create: page_size must be a power of two in [16, 4096] (got %d)", cfg->page_size);
+  if (cfg->q_heads > 1024)
+    return say(t_err, DOMINO_ERR_UNSUPPORTED, "create: at most 1024 query heads");
+  int dev = 0;
+  domino_status_t st = check_device(t_err, &dev);
+  if (st != DOMINO_OK) return st;
+  domino_attention* h = new (std::nothrow) domino_attention();
+  if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
+  h->cfg = *cfg;
+  h->device = dev;
+  *out = h;
+  return DOMINO_OK;
+}
+
+extern "C" void domino_attention_destroy(domino_attention_t* h) {
+  if (!h) return;
+  h->release();
+  delete h;
+}
+
+extern "C" const char* domino_attention_last_error(const domino_attention_t* h) {
+  return h ? h->err : t_err;
+}
+
+static domino_status_t check_cache(domino_attention_t* h, const char* who, const domino_cache_t* c) {
+  const domino_attention_config_t& f = h->cfg;
+  const int elem = f.dtype == DOMINO_DTYPE_BF16 ? 2 : 4, unit = 16 / elem;
+  if (!c) return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: cache is NULL", who);
+  if (!c->k_cache || !c->v_cache || !c->page_table || !c->kv_len || !c->q_start)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: a pointer of the cache is NULL", who);
+  if (((uintptr_t)c->k_cache | (uintptr_t)c->v_cache) & 15)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: caches must be 16-byte aligned", who);
+  if (((uintptr_t)c->page_table | (uintptr_t)c->kv_len | (uintptr_t)c->q_start) & 3)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: page_table, kv_len and q_start must be 4-byte aligned", who);
+  if (c->requests < 1 || c->requests > f.max_requests)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: requests %d outside [1, %d]", who, c->requests,
+               f.max_requests);
+  if (c->tokens < 0 || c->max_new < 0 || c->max_kv < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: tokens, max_new and max_kv must be >= 0", who);
+  if (c->num_pages < 1 || c->table_width < 1 || c->table_stride < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG,
+               "%s: num_pages and table_width must be positive, table_stride >= 0", who);
+  if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < f.head_dim ||
+      c->page_stride % unit || c->head_stride % unit || c->row_stride % unit)
+    return say(h->err, DOMINO_ERR_INVALID_ARG,
+               "%s: cache strides must be multiples of 16 bytes, row_stride at least head_dim", who);
+  if (((double)(f.kv_heads - 1) * c->head_stride + (double)f.page_size * c->row_stride) * elem >=
+      2147483648.0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: a page must span less than 2^31 bytes", who);
+  return DOMINO_OK;
+}
+
+// token arrays: 16-byte aligned base and strides
+static bool rows_ok(const void* p, int64_t tok, int64_t head, int unit) {
+  return !((uintptr_t)p & 15) && tok >= 0 && head >= 0 && tok % unit == 0 && head % unit == 0;
+}
+
+static int32_t clip_kv(const domino_cache_t* c, int page_size) {
+  const int64_t most = (int64_t)c->table_width * page_size;
+  return (int32_t)(c->max_kv < most ? c->max_kv : most);
+}
+
+static domino_status_t launched(domino_attention_t* h, const char* who) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess)
+    return say(h->err, DOMINO_ERR_HIP, "%s: kernel launch failed: %s", who, hipGetErrorString(e));
+  h->err[0] = 0;
+  return DOMINO_OK;
+}
+
+extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const domino_cache_t* c,
+                                                   const void* k, int64_t k_token_stride,
+                                                   int64_t k_head_stride, const void* v,
+                                                   int64_t v_token_stride, int64_t v_head_stride,
+                                                   void* stream) {
+  if (!h) return DOMINO_ERR_INVALID_ARG;
+  domino_status_t st = check_cache(h, "append", c);
+  if (st != DOMINO_OK) return st;
+  const domino_attention_config_t& f = h->cfg;
+  const int elem = f.dtype == DOMINO_DTYPE_BF16 ? 2 : 4, unit = 16 / elem;
+  if (c->tokens == 0 || c->max_new == 0) return DOMINO_OK;
+  if (!k || !v) return say(h->err, DOMINO_ERR_INVALID_ARG, "append: k and v must be non-NULL");
+  if (!rows_ok(k, k_token_stride, k_head_stride, unit) || !rows_ok(v, v_token_stride, v_head_stride, unit))
+    return say(h->err, DOMINO_ERR_INVALID_ARG,
+               "append: k and v must be 16-byte aligned, their strides multiples of 16 bytes");
+  AppendArgs a;
+  a.src[0] = k;
+  a.src[1] = v;
+  a.dst[0] = c->k_cache;
+  a.dst[1] = c->v_cache;
+  a.tok[0] = k_token_stride;
+  a.tok[1] = v_token_stride;
+  a.headi[0] = k_head_stride;
+  a.headi[1] = v_head_stride;
+  a.page = c->page_stride;
+  a.head = c->head_stride;
+  a.row = (int32_t)c->row_stride;
+  a.num_pages = c->num_pages;
+  a.pieces = f.head_dim / unit;
+  a.table = c->page_table;
+  a.table_stride = c->table_stride;
+  a.page_shift = __builtin_ctz(f.page_size);
+  a.elem = elem;
+  a.kv_len = c->kv_len;
+  a.q_start = c->q_start;
+  a.tokens = c->tokens;
+  a.max_new = c->max_new;
+  a.max_kv = clip_kv(c, f.page_size);
+  a.kv_heads = f.kv_heads;
+  const int most = c->max_new < c->tokens ? c->max_new : c->tokens;
+  const int64_t blocks = ((int64_t)most * f.kv_heads * a.pieces + 255) / 256;
+  DeviceGuard dg(h->device);
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(append_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), 2 * c->requests),
+                     dim3(256), 0, (hipStream_t)stream, a);
+  return launched(h, "append");
+}
+
+template <typename T>
+static void launch_attend_f32(int D, const AttendArgs& a, hipStream_t st) {
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  const dim3 grid((unsigned)((rows + 15) / 16), a.kv_heads, a.requests);
+  if (D == 64)
+    hipLaunchKernelGGL((attend_f32_kernel<T, 64>), grid, dim3(256), 0, st, a);
+  else if (D == 128)
+    hipLaunchKernelGGL((attend_f32_kernel<T, 128>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((attend_f32_kernel<T, 256>), grid, dim3(256), 0, st, a);
+}
+
+extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t* c,
+                                                const void* q, int64_t q_token_stride,
+                                                int64_t q_head_stride, int32_t window,
+                                                int32_t sinks, float scale, void* out,
+                                                int64_t out_token_stride, int64_t out_head_stride,
+                                                float* lse, void* stream) {
+  if (!h) return DOMINO_ERR_INVALID_ARG;
+  domino_status_t st = check_cache(h, "run", c);
+  if (st != DOMINO_OK) return st;
+  const domino_attention_config_t& f = h->cfg;
+  const int unit = f.dtype == DOMINO_DTYPE_BF16 ? 8 : 4;
+  if (window < 0 || sinks < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: window and sinks must be >= 0");
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: scale must be finite and > 0");
+  if (c->tokens == 0 || c->max_new == 0) return DOMINO_OK;
+  if (!q || !out) return say(h->err, DOMINO_ERR_INVALID_ARG, "run: q and out must be non-NULL");
+  if (!rows_ok(q, q_token_stride, q_head_stride, unit) || !rows_ok(out, out_token_stride, out_head_stride, unit))
+    return say(h->err, DOMINO_ERR_INVALID_ARG,
+               "run: q and out must be 16-byte aligned, their strides multiples of 16 bytes");
+  if ((uintptr_t)lse & 3) return say(h->err, DOMINO_ERR_INVALID_ARG, "run: lse must be 4-byte aligned");
+  const int32_t max_new = c->max_new < c->tokens ? c->max_new : c->tokens;
+  if ((int64_t)max_new * (f.q_heads / f.kv_heads) > (1 << 30))
+    return say(h->err, DOMINO_ERR_UNSUPPORTED, "run: too many rows for a request");
+  AttendArgs a{};
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.k = c->k_cache;
+  a.v = c->v_cache;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.o_tok = out_token_stride;
+  a.o_head = out_head_stride;
+  a.page = c->page_stride;
+  a.head = c->head_stride;
+  a.row = (int32_t)c->row_stride;
+  a.num_pages = c->num_pages;
+  a.table = c->page_table;
+  a.table_stride = c->table_stride;
+  a.page_shift = __builtin_ctz(f.page_size);
+  a.kv_len = c->kv_len;
+  a.q_start = c->q_start;
+  a.requests = c->requests;
+  a.tokens = c->tokens;
+  // a request can have no more tokens than there are, nor more keys than its
+  // table holds
+  a.max_new = max_new;
+  a.max_kv = clip_kv(c, f.page_size);
+  a.q_heads = f.q_heads;
+  a.kv_heads = f.kv_heads;
+  a.group = f.q_heads / f.kv_heads;
+  // a window that no position reaches past hides nothing
+  a.window = window >= a.max_kv ? 0 : window;
+  a.sinks = sinks < a.max_kv ? sinks : a.max_kv;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  DeviceGuard dg(h->device);
+  (void)hipGetLastError();
+  if (f.dtype == DOMINO_DTYPE_BF16)
+    launch_attend_f32<bf16_t>(f.head_dim, a, (hipStream_t)stream);
+  else
+    launch_attend_f32<float>(f.head_dim, a, (hipStream_t)stream);
+  return launched(h, "run");
+}

@@ -1,0 +1,795 @@
+// Rules on the target's logits (penalties, biases, grammar masks), alone and
+// fused with the acceptance of a draft block.
+//
+// The vocabulary is cut into ranges; a workgroup takes one range of one
+// request for all of the request's rows, so that what the rows share (the
+// history's counts, the biases, the noise) is put into LDS once.
+//
+// Few ids of a range are touched by a penalty or a bias.  The pass over the
+// logits therefore leaves those out by a bit of a bitmap, next to the grammar
+// mask's bit, and the touched ids are taken from a list afterwards, where the
+// division of the repetition penalty and the look-ups are paid for them alone.
+// Counting uses integer atomics in LDS and the list is in the order of the
+// ids, so nothing depends on the order of arrival.
+#include <cmath>
+#include <new>
+
+#include "../../include/domino_verify.h"
+#include "common.h"
+#include "handle.h"
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxRows = 64;
+constexpr uint32_t kPrompt = 0x80000000u;  // id stands in the prompt
+constexpr uint32_t kDrafted = 0x40000000u;  // id is one of the proposals
+constexpr uint32_t kCount = 0x3FFFFFFFu;
+
+struct LogitsArgs {
+  const void* logits;
+  int64_t req_stride, row_stride;
+  int32_t requests, rows, vocab;
+  const int32_t* draft;
+  int64_t draft_stride;
+  const int32_t* draft_len;
+  const int32_t* history;
+  int64_t history_stride;
+  int32_t history_width;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  int64_t bias_stride;
+  int32_t bias_width;
+  const int32_t* bias_len;
+  const uint32_t* mask;
+  int64_t mask_req, mask_row;
+  int32_t range;     // ids of a range, a multiple of 64
+  int32_t row_slots, parts;  // rows taken at once, waves to a row
+  // process
+  void* out;
+  int64_t out_req, out_row;
+  // verify
+  const float* temperature;
+  const float* accept_u;
+  int64_t accept_stride;
+  const float* noise;
+  int64_t noise_stride;
+  struct RowPart* partial;  // [requests][rows][ranges * parts]
+  float* drafted;           // [requests][rows] processed logit of the row's proposal
+  int32_t* out_tokens;
+  int32_t* out_accepted;
+  float* out_logprob;
+};
+
+// What one wave knows of a row: the largest logit, sum of e^((x - m) / T), and
+// the best candidate with its id (kNone: no candidate).
+struct RowPart {
+  float m, s, best;
+  int32_t id;
+};
+constexpr int32_t kNone = 0x7FFFFFFF;
+
+__device__ __forceinline__ int clip_len(const int32_t* len, int b, int width) {
+  if (!len) return width;
+  const int n = len[b];
+  return n < 0 ? 0 : (n > width ? width : n);
+}
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kVec = 4;
+};
+template <>
+struct Elem<bf16_t> {
+  static constexpr int kVec = 8;
+};
+
+// kVec consecutive logits.  Rows of an odd vocabulary are aligned to the
+// element only; the copy still compiles to one 16-byte load, which the memory
+// path takes at any alignment.
+template <typename T>
+struct Vec {
+  T e[Elem<T>::kVec];
+};
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, int n, float* x) {
+  constexpr int V = Elem<T>::kVec;
+  if (n >= V) {
+    Vec<T> v;
+    __builtin_memcpy(&v, p, 16);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (sizeof(T) == 2)
+        x[j] = bf16_to_f32(v.e[j]);
+      else
+        x[j] = v.e[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      x[j] = -INFINITY;
+      if (j < n) {
+        if constexpr (sizeof(T) == 2)
+          x[j] = bf16_to_f32(p[j]);
+        else
+          x[j] = p[j];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bf16_t to_bf16(float x) {
+  return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// the largest fp32 number for +inf, -inf for NaN
+__device__ __forceinline__ float tame(float x) {
+  return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);
+}
+
+__device__ __forceinline__ float temperature_of(const LogitsArgs& a, int b) {
+  const float t = a.temperature ? a.temperature[b] : 0.f;
+  return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;
+}
+
+// LDS of a workgroup: counts, last bias entry, list and bitmap of touched ids
+struct Touched {
+  uint32_t* count;   // [range]
+  uint32_t* bias;    // [range] entry + 1
+  uint32_t* bits;    // [range / 32]
+  uint16_t* list;    // [range] offsets, ascending
+  int n;
+};
+
+__device__ __forceinline__ void build_touched(const LogitsArgs& a, int b, int lo, int ids,
+                                              bool counts, bool biases, int n_draft,
+                                              const int* s_draft, int* s_wave, Touched& t) {
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_index();
+  for (int i = tid; i < a.range; i += kThreads) {
+    t.count[i] = 0;
+    if (biases) t.bias[i] = 0;
+  }
+  __syncthreads();
+  if (counts && a.history) {
+    const int len = clip_len(a.history_len, b, a.history_width);
+    const int prompt = a.prompt_len ? clip_len(a.prompt_len, b, a.history_width) : 0;
+    const int32_t* h = a.history + b * a.history_stride;
+    for (int i = tid; i < len; i += kThreads) {
+      const uint32_t off = (uint32_t)h[i] - (uint32_t)lo;
+      if (off < (uint32_t)ids) {
+        if (i < prompt)
+          atomicOr(&t.count[off], kPrompt);
+        else
+          atomicAdd(&t.count[off], 1u);
+      }
+    }
+  }
+  if (counts && tid < n_draft) {
+    const uint32_t off = (uint32_t)s_draft[tid] - (uint32_t)lo;
+    if (off < (uint32_t)ids) atomicOr(&t.count[off], kDrafted);
+  }
+  if (biases) {
+    const int len = clip_len(a.bias_len, b, a.bias_width);
+    const int32_t* h = a.bias_ids + b * a.bias_stride;
+    for (int i = tid; i < len; i += kThreads) {
+      const uint32_t off = (uint32_t)h[i] - (uint32_t)lo;
+      if (off < (uint32_t)ids) atomicMax(&t.bias[off], (uint32_t)i + 1);
+    }
+  }
+  __syncthreads();
+  // each wave compacts a run of 64-id groups; the runs follow one another
+  const int groups = a.range / 64, per = (groups + kWaves - 1) / kWaves;
+  const int g0 = w * per, g1 = min(g0 + per, groups);
+  int total = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int i = g * 64 + lane;
+    const uint64_t hit = __ballot(t.count[i] != 0 || (biases && t.bias[i] != 0));
+    if (lane < 2) t.bits[2 * g + lane] = (uint32_t)(hit >> (32 * lane));
+    total += __popcll(hit);
+  }
+  if (lane == 0) s_wave[w] = total;
+  __syncthreads();
+  int at = 0, all = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < w) at += s_wave[i];
+    all += s_wave[i];
+  }
+  for (int g = g0; g < g1; ++g) {
+    const int i = g * 64 + lane;
+    const bool hit = t.count[i] != 0 || (biases && t.bias[i] != 0);
+    const uint64_t m = __ballot(hit);
+    if (hit) t.list[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)i;
+    at += __popcll(m);
+  }
+  t.n = all;
+  __syncthreads();
+}
+
+// the rules of one touched id on row t
+struct Rules {
+  float repetition, frequency, presence;
+  bool has_repetition;
+  const float* bias;
+  const int* draft;
+  int n_draft;
+};
+
+__device__ __forceinline__ float touched_logit(float x, uint32_t c, uint32_t entry, int id, int t,
+                                               const Rules& r) {
+  uint32_t n = c & kCount;
+  if (c & kDrafted) {
+    const int before = min(t, r.n_draft);
+    for (int i = 0; i < before; ++i) n += r.draft[i] == id;
+  }
+  if (r.has_repetition && (n > 0 || (c & kPrompt))) x = x > 0.f ? x / r.repetition : __fmul_rn(x, r.repetition);
+  x = __fsub_rn(x, __fmul_rn(r.frequency, (float)n));
+  x = __fsub_rn(x, n > 0 ? r.presence : 0.f);
+  if (entry) x = __fadd_rn(x, r.bias[entry - 1]);
+  return x;
+}
+
+// Reads logits once; writes them (process) or keeps each row's statistics
+// (verify).  Bound by memory at the larger sizes.
+template <typename T, bool VERIFY, bool TOUCH>
+__global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
+  constexpr int V = Elem<T>::kVec;
+  extern __shared__ uint32_t dyn[];
+  __shared__ int s_draft[kMaxRows];
+  __shared__ int s_wave[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_index();
+  const int b = blockIdx.y, lo = blockIdx.x * a.range;
+  const int ids = min(a.range, a.vocab - lo);
+  const bool counts = TOUCH && (a.repetition || a.frequency || a.presence);
+  const bool biases = TOUCH && a.bias_ids;
+  const int n_draft = a.draft ? clip_len(a.draft_len, b, a.rows - 1) : 0;
+  if (tid < kMaxRows) s_draft[tid] = tid < n_draft ? a.draft[b * a.draft_stride + tid] : -1;
+  const float temp = VERIFY ? temperature_of(a, b) : 0.f;
+
+  Touched t;
+  uint32_t* at = dyn;
+  float* noise = nullptr;
+  if (VERIFY && a.noise) {
+    noise = (float*)at;
+    at += a.range;
+  }
+  if (TOUCH) {
+    t.count = at;
+    at += a.range;
+    t.bias = at;
+    if (biases) at += a.range;
+    t.bits = at;
+    at += a.range / 32;
+    t.list = (uint16_t*)at;
+  }
+  t.n = 0;
+  if (VERIFY && temp > 0.f) {
+    const float* e = a.noise + b * a.noise_stride + lo;
+    for (int i = tid; i < ids; i += kThreads) noise[i] = temp * logf(e[i]);
+  }
+  __syncthreads();
+  if (TOUCH) build_touched(a, b, lo, ids, counts, biases, n_draft, s_draft, s_wave, t);
+
+  Rules rules;
+  rules.has_repetition = a.repetition != nullptr;
+  rules.repetition = a.repetition ? a.repetition[b] : 1.f;
+  rules.frequency = a.frequency ? a.frequency[b] : 0.f;
+  rules.presence = a.presence ? a.presence[b] : 0.f;
+  rules.bias = biases ? a.bias_values + b * a.bias_stride : nullptr;
+  rules.draft = s_draft;
+  rules.n_draft = n_draft;
+
+  const int slot = w / a.parts, part = w - slot * a.parts;
+  const int rows = VERIFY ? n_draft + 1 : a.rows;
+  const float c = VERIFY ? 1.44269504088896340736f / (temp > 0.f ? temp : 1.f) : 0.f;
+  const int first = part * 64 + lane, step = a.parts * 64;
+  const int row0 = slot < a.row_slots ? slot : rows;  // waves beyond the slots have no row
+  for (int row = row0; row < rows; row += a.row_slots) {
+    const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
+    const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
+    T* dst = VERIFY ? nullptr : (T*)a.out + b * a.out_req + row * a.out_row + lo;
+    const int proposal = VERIFY && row < n_draft ? s_draft[row] : -1;
+    const int own = proposal >= lo && proposal < lo + ids ? proposal - lo : -1;
+    float m = -INFINITY, s = 0.f, best = -INFINITY;
+    int where = -1;  // vector of the best candidate
+    for (int i = first * V; i < ids; i += step * V) {
+      float x[V];
+      load_vec<T>(src + i, ids - i, x);
+      uint32_t allow = mask ? mask[i / 32] >> (i % 32) : ~0u;
+      if constexpr (!VERIFY) {
+        // touched ids keep their logit here and are written again below
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (!((allow >> j) & 1)) x[j] = -INFINITY;
+        if (i + V <= ids) {
+          Vec<T> v;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            if constexpr (sizeof(T) == 2)
+              v.e[j] = to_bf16(x[j]);
+            else
+              v.e[j] = x[j];
+          }
+          __builtin_memcpy(dst + i, &v, 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (i + j < ids) {
+              if constexpr (sizeof(T) == 2)
+                dst[i + j] = to_bf16(x[j]);
+              else
+                dst[i + j] = x[j];
+            }
+        }
+      } else {
+        if (TOUCH) allow &= ~(t.bits[i / 32] >> (i % 32));
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          x[j] = ((allow >> j) & 1) ? tame(x[j]) : -INFINITY;
+          top = fmaxf(top, x[j]);
+        }
+        if (top > -INFINITY) {
+          const float mn = fmaxf(m, top);
+          s *= exp2f((m - mn) * c);
+#pragma unroll
+          for (int j = 0; j < V; ++j) s += exp2f((x[j] - mn) * c);
+          m = mn;
+        }
+        if ((uint32_t)(own - i) < (uint32_t)V) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (own - i == j) {
+              // a touched proposal is written from the list below
+              if (!TOUCH || !((t.bits[own / 32] >> (own % 32)) & 1)) a.drafted[b * a.rows + row] = x[j];
+              x[j] = -INFINITY;
+            }
+        }
+        if (temp > 0.f) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (x[j] > -INFINITY) x[j] -= noise[i + j];
+        }
+        top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
+        if (top > best) {
+          best = top;
+          where = i;
+        }
+      }
+    }
+    if constexpr (VERIFY) {
+      // exact id of this lane's best candidate: the first of its vector
+      int id = kNone;
+      if (where >= 0) {
+        float x[V];
+        load_vec<T>(src + where, ids - where, x);
+        uint32_t allow = mask ? mask[where / 32] >> (where % 32) : ~0u;
+        if (TOUCH) allow &= ~(t.bits[where / 32] >> (where % 32));
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) {
+          float y = tame(x[j]);
+          if (!((allow >> j) & 1) || where + j == own || y == -INFINITY) continue;
+          if (temp > 0.f) y -= noise[where + j];
+          if (y == best) id = lo + where + j;
+        }
+      }
+      if (TOUCH) {
+        for (int e = first; e < t.n; e += step) {
+          const int off = t.list[e];
+          if (mask && !((mask[off / 32] >> (off % 32)) & 1)) {
+            if (off == own) a.drafted[b * a.rows + row] = -INFINITY;
+            continue;
+          }
+          float x;
+          if constexpr (sizeof(T) == 2)
+            x = bf16_to_f32(src[off]);
+          else
+            x = src[off];
+          x = tame(touched_logit(x, t.count[off], biases ? t.bias[off] : 0u, lo + off, row, rules));
+          if (off == own) a.drafted[b * a.rows + row] = x;
+          if (x == -INFINITY) continue;
+          const float mn = fmaxf(m, x);
+          s = s * exp2f((m - mn) * c) + exp2f((x - mn) * c);
+          m = mn;
+          if (off == own) continue;
+          if (temp > 0.f) x -= noise[off];
+          if (x > best || (x == best && lo + off < id)) {
+            best = x;
+            id = lo + off;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) {
+        const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
+        const float ob = __shfl_xor(best, d, 64);
+        const int oi = __shfl_xor(id, d, 64);
+        const float mn = fmaxf(m, om);
+        if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + os * exp2f((om - mn) * c);
+        m = mn;
+        if (ob > best || (ob == best && oi < id)) {
+          best = ob;
+          id = oi;
+        }
+      }
+      if (lane == 0)
+        a.partial[((int64_t)b * a.rows + row) * ((int64_t)gridDim.x * a.parts) +
+                  (int64_t)blockIdx.x * a.parts + part] = RowPart{m, s, best, id};
+    }
+  }
+  if constexpr (!VERIFY && TOUCH) {
+    __syncthreads();
+    for (int row = row0; row < rows; row += a.row_slots) {
+      const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
+      const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
+      T* dst = (T*)a.out + b * a.out_req + row * a.out_row + lo;
+      for (int e = first; e < t.n; e += step) {
+        const int off = t.list[e];
+        if (mask && !((mask[off / 32] >> (off % 32)) & 1)) continue;
+        float x;
+        if constexpr (sizeof(T) == 2)
+          x = bf16_to_f32(src[off]);
+        else
+          x = src[off];
+        x = touched_logit(x, t.count[off], biases ? t.bias[off] : 0u, lo + off, row, rules);
+        if constexpr (sizeof(T) == 2)
+          dst[off] = to_bf16(x);
+        else
+          dst[off] = x;
+      }
+    }
+  }
+}
+
+// One workgroup per request joins the parts of its rows, walks the proposals
+// and writes the outputs.
+__global__ __launch_bounds__(256) void accept_kernel(LogitsArgs a, int parts) {
+  __shared__ float s_lse[kMaxRows], s_m[kMaxRows], s_best[kMaxRows];
+  __shared__ int s_id[kMaxRows], s_stands[kMaxRows];
+  const int b = blockIdx.x, lane = threadIdx.x & 63, w = wave_index();
+  const int n = a.draft ? clip_len(a.draft_len, b, a.rows - 1) : 0;
+  const float temp = temperature_of(a, b);
+  const float scale = temp > 0.f ? temp : 1.f, c = 1.44269504088896340736f / scale;
+  for (int row = w; row <= n; row += 4) {
+    const RowPart* p = a.partial + ((int64_t)b * a.rows + row) * parts;
+    float m = -INFINITY, s = 0.f, best = -INFINITY;
+    int id = kNone;
+    for (int i = lane; i < parts; i += 64) {
+      const RowPart o = p[i];
+      const float mn = fmaxf(m, o.m);
+      if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + o.s * exp2f((o.m - mn) * c);
+      m = mn;
+      if (o.best > best || (o.best == best && o.id < id)) {
+        best = o.best;
+        id = o.id;
+      }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
+      const float ob = __shfl_xor(best, d, 64);
+      const int oi = __shfl_xor(id, d, 64);
+      const float mn = fmaxf(m, om);
+      if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + os * exp2f((om - mn) * c);
+      m = mn;
+      if (ob > best || (ob == best && oi < id)) {
+        best = ob;
+        id = oi;
+      }
+    }
+    if (lane == 0) {
+      int stands = 0;
+      float lp = -INFINITY;
+      if (row < n) {
+        const int d = a.draft[b * a.draft_stride + row];
+        if (d >= 0 && d < a.vocab) {
+          const float x = a.drafted[b * a.rows + row];
+          if (x > -INFINITY) {
+            lp = (x - m) / scale - logf(s);
+            stands = id == kNone || (temp > 0.f ? a.accept_u[b * a.accept_stride + row] < expf(lp)
+                                                : x > best || (x == best && d < id));
+          }
+        }
+      }
+      s_stands[row] = stands;
+      s_id[row] = id;
+      s_m[row] = m;
+      s_best[row] = best;
+      // log-probability of the proposal where it stands; of the chosen id below
+      s_lse[row] = stands ? lp : logf(s);
+    }
+  }
+  __syncthreads();
+  if (w == 0) {
+    const bool ok = lane < n && s_stands[lane];
+    const uint64_t stood = __ballot(ok);
+    const int taken = min(n, stood == ~0ull ? 64 : __builtin_ctzll(~stood));
+    if (lane == 0) a.out_accepted[b] = taken;
+    if (lane < a.rows) {
+      int tok = -1;
+      float lp = 0.f;
+      if (lane < taken) {
+        tok = a.draft[b * a.draft_stride + lane];
+        lp = s_lse[lane];
+      } else if (lane == taken) {
+        const int id = s_id[lane];
+        if (id == kNone) {
+          lp = -INFINITY;
+        } else {
+          tok = id;
+          // the best score is x - T ln E: the logit itself is that plus T ln E
+          const float x = temp > 0.f ? s_best[lane] + temp * logf(a.noise[b * a.noise_stride + id]) : s_best[lane];
+          lp = (x - s_m[lane]) / scale - s_lse[lane];
+        }
+      }
+      a.out_tokens[b * a.rows + lane] = tok;
+      if (a.out_logprob) a.out_logprob[b * a.rows + lane] = lp;
+    }
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- handle
+struct domino_verify : HandleBase {
+  domino_verify_config_t cfg;
+  RowPart* partial = nullptr;
+  float* drafted = nullptr;
+  int cus = 256;
+};
+
+static thread_local char t_err[256] = "";
+
+constexpr int kMinRange = 512;
+constexpr size_t kLdsBytes = 78 * 1024;  // two workgroups to a CU
+
+struct Cut {
+  int range, ranges, row_slots, parts;
+  size_t lds;
+};
+
+static size_t lds_per_id(bool noise, bool touch, bool biases) {
+  return (noise ? 4 : 0) + (touch ? 6 : 0) + (biases ? 4 : 0);
+}
+
+// longest range: what LDS for two workgroups to a CU holds (its bitmap is
+// counted as a byte per id, an overestimate)
+static int longest_range(size_t per_id) {
+  const int fit = per_id ? (int)((kLdsBytes - 1024) / (per_id + 1)) / 64 * 64 : 16384;
+  return fit < 16384 ? fit : 16384;
+}
+
+// Ranges of a launch.  Workgroups run in rounds of two to a CU, and a range
+// costs its ids plus what its start takes (about the time of 512 ids), so of
+// the cuts that fill one to four rounds more than the longest ranges need,
+// the one with the least rounds x (range + 512) is taken.  requests * ranges
+// is at most requests * (ranges of the longest) + 4 rounds.
+static Cut cut_vocab(int vocab, int cus, int requests, int rows, size_t per_id, bool touch) {
+  Cut k;
+  const int most = longest_range(per_id), slots = 2 * cus;
+  const int least = (vocab + most - 1) / most;
+  int64_t best = -1;
+  const int64_t from = ((int64_t)least * requests + slots - 1) / slots;
+  k.range = most;
+  for (int64_t rounds = from; rounds < from + 4; ++rounds) {
+    int64_t r = rounds * slots / requests;
+    if (r < least) r = least;
+    int range = (int)(((vocab + r - 1) / r + 63) / 64 * 64);
+    if (range < kMinRange) range = kMinRange;
+    if (range > most) range = most;
+    const int64_t ranges = (vocab + range - 1) / range;
+    const int64_t cost = ((requests * ranges + slots - 1) / slots) * (range + 512);
+    if (best < 0 || cost < best) {
+      best = cost;
+      k.range = range;
+    }
+  }
+  k.ranges = (vocab + k.range - 1) / k.range;
+  k.row_slots = rows < kWaves ? rows : kWaves;
+  k.parts = kWaves / k.row_slots;
+  k.lds = per_id * k.range + (touch ? k.range / 8 : 0) + 64;
+  return k;
+}
+
+extern "C" domino_status_t domino_verify_create(const domino_verify_config_t* cfg, domino_verify_t** out) {
+  if (!out) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: out is NULL");
+  *out = nullptr;
+  if (!cfg) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: cfg is NULL");
+  if (cfg->vocab < 1) return say(t_err, DOMINO_ERR_INVALID_CONFIG, "create: vocab must be positive");
+  if (cfg->max_requests < 1 || cfg->max_requests > 1024)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG, "create: max_requests must be in [1, 1024]");
+  if (cfg->max_rows < 1 || cfg->max_rows > kMaxRows)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG, "create: max_rows must be in [1, %d]", kMaxRows);
+  if (cfg->dtype != DOMINO_DTYPE_BF16 && cfg->dtype != DOMINO_DTYPE_FP32)
+    return say(t_err, DOMINO_ERR_INVALID_CONFIG,
+               "create: dtype must be DOMINO_DTYPE_BF16 or DOMINO_DTYPE_FP32");
+  if (cfg->vocab > (1 << 24))
+    return say(t_err, DOMINO_ERR_UNSUPPORTED, "create: vocab must be at most 2^24");
+  int dev = 0;
+  domino_status_t st = check_device(t_err, &dev);
+  if (st != DOMINO_OK) return st;
+  domino_verify* h = new (std::nothrow) domino_verify();
+  if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
+  h->cfg = *cfg;
+  h->device = dev;
+  if (hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+    (void)hipGetLastError();
+    h->cus = 256;
+  }
+  // bound of cut_vocab's requests * ranges, times the waves of a row
+  const int shortest = longest_range(lds_per_id(true, true, true));
+  const size_t words = ((size_t)cfg->max_requests * ((cfg->vocab + shortest - 1) / shortest) + 8 * h->cus) *
+                       (cfg->max_rows > kWaves ? cfg->max_rows : kWaves);
+  h->partial = (RowPart*)h->take(words * sizeof(RowPart));
+  h->drafted = (float*)h->take((size_t)cfg->max_requests * cfg->max_rows * 4);
+  if (!h->partial || !h->drafted) {
+    h->release();
+    delete h;
+    return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: workspace allocation failed");
+  }
+  *out = h;
+  return DOMINO_OK;
+}
+
+extern "C" void domino_verify_destroy(domino_verify_t* h) {
+  if (!h) return;
+  h->release();
+  delete h;
+}
+
+extern "C" const char* domino_verify_last_error(const domino_verify_t* h) { return h ? h->err : t_err; }
+
+static domino_status_t take_logits(domino_verify_t* h, const char* who, const domino_logits_t* l,
+                                   LogitsArgs& a) {
+  if (!l) return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: logits is NULL", who);
+  const domino_verify_config_t& f = h->cfg;
+  const int elem = f.dtype == DOMINO_DTYPE_BF16 ? 2 : 4;
+  if (!l->logits || ((uintptr_t)l->logits & (elem - 1)))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: the logits pointer is NULL or misaligned", who);
+  if (l->requests < 1 || l->requests > f.max_requests)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: requests %d outside [1, %d]", who, l->requests,
+               f.max_requests);
+  if (l->rows < 1 || l->rows > f.max_rows)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: rows %d outside [1, %d]", who, l->rows, f.max_rows);
+  if (l->request_stride < 0 || l->row_stride < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: strides must be >= 0", who);
+  if (l->draft && l->rows > 1 && l->draft_stride < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: strides must be >= 0", who);
+  if (l->history && (l->history_width < 0 || l->history_stride < 0))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: history_width and history_stride must be >= 0", who);
+  if ((l->bias_ids == nullptr) != (l->bias_values == nullptr))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: bias_ids and bias_values must be given together", who);
+  if (l->bias_ids && (l->bias_width < 0 || l->bias_stride < 0))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: bias_width and bias_stride must be >= 0", who);
+  if (l->mask && (l->mask_request_stride < 0 || l->mask_row_stride < 0))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: mask strides must be >= 0", who);
+  const void* words[] = {l->draft, l->draft_len, l->history, l->history_len, l->prompt_len, l->repetition,
+                         l->frequency, l->presence, l->bias_ids, l->bias_values, l->bias_len, l->mask};
+  for (const void* p : words)
+    if ((uintptr_t)p & 3)
+      return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: a list or mask pointer is not 4-byte aligned", who);
+  a.logits = l->logits;
+  a.req_stride = l->request_stride;
+  a.row_stride = l->row_stride;
+  a.requests = l->requests;
+  a.rows = l->rows;
+  a.vocab = f.vocab;
+  a.draft = l->rows > 1 ? l->draft : nullptr;
+  a.draft_stride = l->draft_stride;
+  a.draft_len = l->draft_len;
+  a.history = l->history_width > 0 ? l->history : nullptr;
+  a.history_stride = l->history_stride;
+  a.history_width = l->history_width;
+  a.history_len = l->history_len;
+  a.prompt_len = l->prompt_len;
+  a.repetition = l->repetition;
+  a.frequency = l->frequency;
+  a.presence = l->presence;
+  a.bias_ids = l->bias_width > 0 ? l->bias_ids : nullptr;
+  a.bias_values = l->bias_values;
+  a.bias_stride = l->bias_stride;
+  a.bias_width = l->bias_width;
+  a.bias_len = l->bias_len;
+  a.mask = l->mask;
+  a.mask_req = l->mask_request_stride;
+  a.mask_row = l->mask_row_stride;
+  return DOMINO_OK;
+}
+
+template <bool VERIFY>
+static void launch_logits(const domino_verify_t* h, LogitsArgs& a, Cut& k, hipStream_t st) {
+  const bool penalties = a.repetition || a.frequency || a.presence;
+  const bool touch = penalties || a.bias_ids;
+  k = cut_vocab(h->cfg.vocab, h->cus, a.requests, a.rows,
+                lds_per_id(VERIFY && a.noise, touch, a.bias_ids != nullptr), touch);
+  a.range = k.range;
+  a.row_slots = k.row_slots;
+  a.parts = k.parts;
+  const dim3 grid(k.ranges, a.requests), block(kThreads);
+  if (h->cfg.dtype == DOMINO_DTYPE_BF16) {
+    if (touch)
+      hipLaunchKernelGGL((logits_kernel<bf16_t, VERIFY, true>), grid, block, k.lds, st, a);
+    else
+      hipLaunchKernelGGL((logits_kernel<bf16_t, VERIFY, false>), grid, block, k.lds, st, a);
+  } else {
+    if (touch)
+      hipLaunchKernelGGL((logits_kernel<float, VERIFY, true>), grid, block, k.lds, st, a);
+    else
+      hipLaunchKernelGGL((logits_kernel<float, VERIFY, false>), grid, block, k.lds, st, a);
+  }
+}
+
+static domino_status_t launched(domino_verify_t* h, const char* who) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess)
+    return say(h->err, DOMINO_ERR_HIP, "%s: kernel launch failed: %s", who, hipGetErrorString(e));
+  h->err[0] = 0;
+  return DOMINO_OK;
+}
+
+extern "C" domino_status_t domino_verify_process(domino_verify_t* h, const domino_logits_t* logits, void* out,
+                                                 int64_t out_request_stride, int64_t out_row_stride,
+                                                 void* stream) {
+  if (!h) return DOMINO_ERR_INVALID_ARG;
+  LogitsArgs a{};
+  domino_status_t st = take_logits(h, "process", logits, a);
+  if (st != DOMINO_OK) return st;
+  const int elem = h->cfg.dtype == DOMINO_DTYPE_BF16 ? 2 : 4;
+  if (!out || ((uintptr_t)out & (elem - 1)))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "process: out is NULL or misaligned");
+  if ((a.rows > 1 && out_row_stride < a.vocab) || (a.requests > 1 && out_request_stride < a.vocab))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "process: rows of out overlap");
+  a.out = out;
+  a.out_req = out_request_stride;
+  a.out_row = out_row_stride;
+  DeviceGuard dg(h->device);
+  (void)hipGetLastError();
+  Cut k;
+  launch_logits<false>(h, a, k, (hipStream_t)stream);
+  return launched(h, "process");
+}
+
+extern "C" domino_status_t domino_verify_run(domino_verify_t* h, const domino_logits_t* logits,
+                                             const float* temperature, const float* accept_u,
+                                             int64_t accept_stride, const float* noise,
+                                             int64_t noise_stride, int32_t* out_tokens,
+                                             int32_t* out_accepted, float* out_logprob, void* stream) {
+  if (!h) return DOMINO_ERR_INVALID_ARG;
+  LogitsArgs a{};
+  domino_status_t st = take_logits(h, "run", logits, a);
+  if (st != DOMINO_OK) return st;
+  if (!out_tokens || !out_accepted)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: out_tokens and out_accepted must be non-NULL");
+  if (temperature && (!noise || (a.draft && !accept_u)))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: temperature needs noise, and accept_u where there are proposals");
+  if (noise_stride < 0 || accept_stride < 0)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: strides must be >= 0");
+  const void* words[] = {temperature, accept_u, noise, out_tokens, out_accepted, out_logprob};
+  for (const void* p : words)
+    if ((uintptr_t)p & 3) return say(h->err, DOMINO_ERR_INVALID_ARG, "run: a pointer is not 4-byte aligned");
+  a.temperature = temperature;
+  a.accept_u = accept_u;
+  a.accept_stride = accept_stride;
+  a.noise = temperature ? noise : nullptr;
+  a.noise_stride = noise_stride;
+  a.partial = h->partial;
+  a.drafted = h->drafted;
+  a.out_tokens = out_tokens;
+  a.out_accepted = out_accepted;
+  a.out_logprob = out_logprob;
+  DeviceGuard dg(h->device);
+  (void)hipGetLastError();
+  Cut k;
+  launch_logits<true>(h, a, k, (hipStream_t)stream);
+  hipLaunchKernelGGL(accept_kernel, dim3(a.requests), dim3(256), 0, (hipStream_t)stream, a, k.ranges * k.parts);
+  return launched(h, "run");
+}

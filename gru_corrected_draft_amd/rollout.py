@@ -32,7 +32,12 @@ EXPORTED = ("domino_rollout_create", "domino_rollout_run", "domino_rollout_run_g
             "domino_rollout_last_error", "domino_rollout_set_timing",
             "domino_rollout_kernel_times", "domino_rollout_set_pool_strategy",
             "domino_rollout_set_step_path", "domino_rollout_cached_graphs",
-            "domino_rollout_run_static")
+            "domino_rollout_run_static",
+            # declared in domino_verify.h, bound in verify.py
+            "domino_attention_create", "domino_attention_append", "domino_attention_run",
+            "domino_attention_destroy", "domino_attention_last_error", "domino_verify_create",
+            "domino_verify_process", "domino_verify_run", "domino_verify_destroy",
+            "domino_verify_last_error")
 STATIC_SCRATCH_BYTES = 4 << 20  # DOMINO_STATIC_SCRATCH_BYTES
 GRAPH_CACHE_MAX = 16  # DOMINO_GRAPH_CACHE_MAX
 # gru: the GRU gates (prefix launch, separate gate kernel); step: projector

@@ -1,0 +1,304 @@
+"""Operators around the verification of a draft block: a paged key-value cache with the attention
+that reads it, and the rules on the target's logits with the acceptance of the proposals.
+
+Thin ctypes binding of ``include/domino_verify.h``; the mathematics of each operator stands there.
+``PagedAttention`` and ``DraftVerifier`` marshal tensors: every argument is checked for type, shape,
+device and layout, work goes to the current stream of the tensors' device, and the handle must not
+be used by two threads at once.  Importing this module needs the built library; there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import rollout as _rollout
+from .rollout import DTYPE_BF16, DTYPE_FP32, DominoError
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class AttentionConfig(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in
+                ("q_heads", "kv_heads", "head_dim", "page_size", "max_requests", "dtype")]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [("k_cache", _vp), ("v_cache", _vp), ("page_stride", _i64), ("head_stride", _i64),
+                ("row_stride", _i64), ("num_pages", _i32), ("page_table", _vp), ("table_stride", _i64),
+                ("table_width", _i32), ("kv_len", _vp), ("q_start", _vp), ("requests", _i32),
+                ("tokens", _i32), ("max_new", _i32), ("max_kv", _i32)]
+
+
+class VerifyConfig(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("vocab", "max_requests", "max_rows", "dtype")]
+
+
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("request_stride", _i64), ("row_stride", _i64), ("requests", _i32),
+                ("rows", _i32), ("draft", _vp), ("draft_stride", _i64), ("draft_len", _vp),
+                ("history", _vp), ("history_stride", _i64), ("history_width", _i32),
+                ("history_len", _vp), ("prompt_len", _vp), ("repetition", _vp), ("frequency", _vp),
+                ("presence", _vp), ("bias_ids", _vp), ("bias_values", _vp), ("bias_stride", _i64),
+                ("bias_width", _i32), ("bias_len", _vp), ("mask", _vp),
+                ("mask_request_stride", _i64), ("mask_row_stride", _i64)]
+
+
+_lib = None
+
+
+def load_library():
+    """The in-tree library with this module's functions declared (raises if it has not been built)."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = _rollout.load_library()
+    p = ctypes.POINTER
+    lib.domino_attention_create.argtypes = [p(AttentionConfig), p(_vp)]
+    lib.domino_attention_append.argtypes = [_vp, p(CacheArgs), _vp, _i64, _i64, _vp, _i64, _i64, _vp]
+    lib.domino_attention_run.argtypes = [_vp, p(CacheArgs), _vp, _i64, _i64, _i32, _i32, _f32, _vp,
+                                         _i64, _i64, _vp, _vp]
+    lib.domino_verify_create.argtypes = [p(VerifyConfig), p(_vp)]
+    lib.domino_verify_process.argtypes = [_vp, p(LogitsArgs), _vp, _i64, _i64, _vp]
+    lib.domino_verify_run.argtypes = [_vp, p(LogitsArgs), _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
+    for name in ("domino_attention_create", "domino_attention_append", "domino_attention_run",
+                 "domino_verify_create", "domino_verify_process", "domino_verify_run"):
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("domino_attention_destroy", "domino_verify_destroy"):
+        getattr(lib, name).argtypes = [_vp]
+        getattr(lib, name).restype = None
+    for name in ("domino_attention_last_error", "domino_verify_last_error"):
+        getattr(lib, name).argtypes = [_vp]
+        getattr(lib, name).restype = ctypes.c_char_p
+    _lib = lib
+    return lib
+
+
+def _want(name, t, dtype, shape, device):
+    """A tensor of exactly this type and shape on the device, its last dimension contiguous."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if shape and shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+class _Handle:
+    def __init__(self, kind, cfg):
+        self.lib = load_library()
+        self._destroy = getattr(self.lib, f"domino_{kind}_destroy")
+        self._error = getattr(self.lib, f"domino_{kind}_last_error")
+        h = _vp()
+        st = getattr(self.lib, f"domino_{kind}_create")(ctypes.byref(cfg), ctypes.byref(h))
+        if st:
+            raise DominoError(st, self._error(None).decode())
+        self.handle = h
+
+    def _check(self, st):
+        if st:
+            raise DominoError(st, self._error(self.handle).decode())
+
+    def close(self):
+        if getattr(self, "handle", None):
+            self._destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagedAttention(_Handle):
+    """Key-value cache in pages and the attention of new tokens over it.
+
+    ``k_cache`` and ``v_cache`` are [pages, kv_heads, page_size, head_dim] tensors of the handle's
+    dtype with the same strides and a contiguous last dimension; any order of the other three in
+    memory will do (a permuted view of [pages, page_size, kv_heads, head_dim], a half of a tensor that
+    holds both).  ``page_table`` is [requests, width], ``kv_len`` [requests] with the new tokens
+    counted, ``q_start`` [requests + 1] the first token row of each request: int32 on the device,
+    read by the kernels alone.  ``max_new`` and ``max_kv`` bound the new tokens and the cache length of
+    a request; they default to what the arguments allow, and kernels are faster with tighter ones.
+    """
+
+    def __init__(self, q_heads, kv_heads, head_dim, page_size, dtype=torch.bfloat16, max_requests=64):
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+        super().__init__("attention", AttentionConfig(q_heads, kv_heads, head_dim, page_size,
+                                                      max_requests, _DTYPES[dtype]))
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.page_size, self.dtype = page_size, dtype
+
+    def _cache(self, k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, device):
+        n = k_cache.shape[0] if k_cache.dim() == 4 else 0
+        shape = (n, self.kv_heads, self.page_size, self.head_dim)
+        _want("k_cache", k_cache, self.dtype, shape, device)
+        _want("v_cache", v_cache, self.dtype, shape, device)
+        strides = k_cache.stride()
+        if v_cache.stride() != strides:
+            raise ValueError("k_cache and v_cache must have the same strides")
+        b = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        width = page_table.shape[1] if page_table.dim() == 2 else -1
+        _want("kv_len", kv_len, torch.int32, (b,), device)
+        _want("q_start", q_start, torch.int32, (b + 1,), device)
+        _want("page_table", page_table, torch.int32, (b, width), device)
+        if not device.type == "cuda":
+            raise ValueError("tensors must be on a GPU")
+        if max_new is None:
+            max_new = tokens
+        if max_kv is None:
+            max_kv = min(width * self.page_size, 2 ** 31 - 1)
+        return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], n,
+                         page_table.data_ptr(), page_table.stride(0), width, kv_len.data_ptr(),
+                         q_start.data_ptr(), b, tokens, max_new, max_kv)
+
+    def append(self, k, v, k_cache, v_cache, page_table, kv_len, q_start, max_new=None, max_kv=None):
+        """Write the new tokens' ``k`` and ``v`` ([tokens, kv_heads, head_dim]) into the cache."""
+        tokens, dev = k.shape[0], k.device
+        shape = (tokens, self.kv_heads, self.head_dim)
+        _want("k", k, self.dtype, shape, dev)
+        _want("v", v, self.dtype, shape, dev)
+        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, dev)
+        self._check(self.lib.domino_attention_append(
+            self.handle, ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+            v.stride(0), v.stride(1), _stream(dev)))
+
+    def run(self, q, k_cache, v_cache, page_table, kv_len, q_start, max_new=None, max_kv=None, window=0,
+            sinks=0, scale=None, out=None, return_lse=False):
+        """Attention of the new tokens' ``q`` ([tokens, q_heads, head_dim]); returns ``out`` of the
+        same shape, or (out, lse) with lse [tokens, q_heads] fp32.  ``window`` = 0 sees the whole
+        cache; otherwise a token sees the last ``window`` positions up to its own and the first
+        ``sinks``.  ``scale`` defaults to head_dim ** -0.5.  Rows of ``out`` that belong to no request
+        are left as they are."""
+        tokens, dev = q.shape[0], q.device
+        shape = (tokens, self.q_heads, self.head_dim)
+        _want("q", q, self.dtype, shape, dev)
+        if out is None:
+            out = torch.empty(shape, dtype=self.dtype, device=dev)
+        else:
+            _want("out", out, self.dtype, shape, dev)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if return_lse else None
+        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, dev)
+        self._check(self.lib.domino_attention_run(
+            self.handle, ctypes.byref(c), q.data_ptr(), q.stride(0), q.stride(1), window, sinks,
+            1.0 / math.sqrt(self.head_dim) if scale is None else scale, out.data_ptr(), out.stride(0),
+            out.stride(1), lse.data_ptr() if return_lse else None, _stream(dev)))
+        return (out, lse) if return_lse else out
+
+
+class DraftVerifier(_Handle):
+    """Rules on the target's logits and the acceptance of a draft block.
+
+    ``logits`` is [requests, rows, vocab] in the handle's dtype, rows and requests at any stride, row
+    t scoring what follows the request's text and its first t proposals; ``draft`` [requests, rows - 1]
+    int32 (or None: no proposals), of which ``draft_len`` [requests] int32 gives those in use.  Rules,
+    each optional: ``history`` [requests, width] int32 with ``history_len`` and ``prompt_len``
+    [requests] int32 (the first prompt_len entries are the prompt); ``repetition``, ``frequency``,
+    ``presence`` [requests] fp32; ``bias_ids`` and ``bias_values`` [requests, n] with ``bias_len``;
+    ``mask`` [requests, rows, ceil(vocab / 32)] int32 whose bit v % 32 of word v / 32 allows id v
+    (expanded views share a mask between rows or requests).
+    """
+
+    def __init__(self, vocab, dtype=torch.bfloat16, max_requests=64, max_rows=16):
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+        super().__init__("verify", VerifyConfig(vocab, max_requests, max_rows, _DTYPES[dtype]))
+        self.vocab, self.dtype = vocab, dtype
+
+    def _args(self, logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
+              presence, bias_ids, bias_values, bias_len, mask):
+        if logits.dim() != 3:
+            raise ValueError("logits must be [requests, rows, vocab]")
+        b, rows, _ = logits.shape
+        dev = logits.device
+        _want("logits", logits, self.dtype, (b, rows, self.vocab), dev)
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a GPU")
+        a = LogitsArgs(logits=logits.data_ptr(), request_stride=logits.stride(0),
+                       row_stride=logits.stride(1), requests=b, rows=rows)
+        if draft is not None and rows > 1:
+            _want("draft", draft, torch.int32, (b, rows - 1), dev)
+            a.draft, a.draft_stride = draft.data_ptr(), draft.stride(0)
+        if history is not None:
+            width = history.shape[1] if history.dim() == 2 else -1
+            _want("history", history, torch.int32, (b, width), dev)
+            a.history, a.history_stride, a.history_width = history.data_ptr(), history.stride(0), width
+        if (bias_ids is None) != (bias_values is None):
+            raise ValueError("bias_ids and bias_values must be given together")
+        if bias_ids is not None:
+            width = bias_ids.shape[1] if bias_ids.dim() == 2 else -1
+            _want("bias_ids", bias_ids, torch.int32, (b, width), dev)
+            _want("bias_values", bias_values, torch.float32, (b, width), dev)
+            if b > 1 and bias_ids.stride(0) != bias_values.stride(0):
+                raise ValueError("bias_ids and bias_values must have the same strides")
+            a.bias_ids, a.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
+            a.bias_stride, a.bias_width = bias_ids.stride(0), width
+        for name, t, dtype in (("draft_len", draft_len, torch.int32),
+                               ("history_len", history_len, torch.int32),
+                               ("prompt_len", prompt_len, torch.int32),
+                               ("bias_len", bias_len, torch.int32),
+                               ("repetition", repetition, torch.float32),
+                               ("frequency", frequency, torch.float32),
+                               ("presence", presence, torch.float32)):
+            if t is not None:
+                _want(name, t, dtype, (b,), dev)
+                setattr(a, name, t.data_ptr())
+        if mask is not None:
+            _want("mask", mask, torch.int32, (b, rows, (self.vocab + 31) // 32), dev)
+            a.mask, a.mask_request_stride, a.mask_row_stride = mask.data_ptr(), mask.stride(0), mask.stride(1)
+        return a
+
+    def process(self, logits, draft=None, draft_len=None, history=None, history_len=None, prompt_len=None,
+                repetition=None, frequency=None, presence=None, bias_ids=None, bias_values=None,
+                bias_len=None, mask=None, out=None):
+        """The processed logits, rounded once to the handle's dtype.  ``out`` may be ``logits``."""
+        a = self._args(logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
+                       presence, bias_ids, bias_values, bias_len, mask)
+        if out is None:
+            out = torch.empty(logits.shape, dtype=self.dtype, device=logits.device)
+        else:
+            _want("out", out, self.dtype, tuple(logits.shape), logits.device)
+            if out.data_ptr() == logits.data_ptr() and out.stride() != logits.stride():
+                raise ValueError("out over the logits must have their strides")
+        self._check(self.lib.domino_verify_process(self.handle, ctypes.byref(a), out.data_ptr(),
+                                                   out.stride(0), out.stride(1), _stream(logits.device)))
+        return out
+
+    def run(self, logits, draft=None, draft_len=None, temperature=None, accept_u=None, noise=None,
+            history=None, history_len=None, prompt_len=None, repetition=None, frequency=None,
+            presence=None, bias_ids=None, bias_values=None, bias_len=None, mask=None,
+            return_logprob=False):
+        """Accept proposals and choose the token after them; returns (tokens [requests, rows] int32,
+        accepted [requests] int32), and logprob [requests, rows] fp32 if asked for.  ``temperature``
+        [requests] fp32 (None: greedy) needs ``noise`` [requests, vocab] fp32 drawn from the unit
+        exponential and, with proposals, ``accept_u`` [requests, rows - 1] fp32 uniform in [0, 1)."""
+        a = self._args(logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
+                       presence, bias_ids, bias_values, bias_len, mask)
+        b, rows, dev = a.requests, a.rows, logits.device
+        u = n = None
+        u_stride = n_stride = 0
+        if temperature is not None:
+            _want("temperature", temperature, torch.float32, (b,), dev)
+            if noise is None or (accept_u is None and a.draft):
+                raise ValueError("temperature needs noise, and accept_u where there are proposals")
+            _want("noise", noise, torch.float32, (b, self.vocab), dev)
+            n, n_stride = noise.data_ptr(), noise.stride(0)
+            if a.draft:
+                _want("accept_u", accept_u, torch.float32, (b, rows - 1), dev)
+                u, u_stride = accept_u.data_ptr(), accept_u.stride(0)
+        tokens = torch.empty((b, rows), dtype=torch.int32, device=dev)
+        accepted = torch.empty((b,), dtype=torch.int32, device=dev)
+        logprob = torch.empty((b, rows), dtype=torch.float32, device=dev) if return_logprob else None
+        self._check(self.lib.domino_verify_run(
+            self.handle, ctypes.byref(a), None if temperature is None else temperature.data_ptr(),
+            u, u_stride, n, n_stride, tokens.data_ptr(), accepted.data_ptr(),
+            logprob.data_ptr() if return_logprob else None, _stream(dev)))
+        return (tokens, accepted, logprob) if return_logprob else (tokens, accepted)
