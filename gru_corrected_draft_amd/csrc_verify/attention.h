@@ -105,18 +105,12 @@ __device__ __forceinline__ bool visible(int key, int p, int window, int sinks) {
   return key <= p && (window == 0 || key > p - window || key < sinks);
 }
 
-__device__ __forceinline__ float load_elem(const float* p) { return *p; }
-__device__ __forceinline__ float load_elem(const bf16_t* p) { return bf16_to_f32(*p); }
-
 // two floats rounded to bf16 (nearest even, NaN kept), lower one first
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
   const v2bf r = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, r);
 }
-__device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_elem(bf16_t* p, float x) { *p = (bf16_t)pack_bf16(x, x); }
-
 __device__ __forceinline__ bool nonfinite(float x) {
   return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u;
 }

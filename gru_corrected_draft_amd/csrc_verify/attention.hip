@@ -4,7 +4,7 @@
 #include <new>
 
 #include "../../include/domino_verify.h"
-#include "attention.h"
+#include "attention_bf16.h"
 #include "handle.h"
 
 // ---------------------------------------------------------------- append
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   }
 }
 
-// ---------------------------------------------------------------- attention, 32-bit products
+// ---------------------------------------------------------------- fp32 attention
 // Four waves share a tile of 16 rows and take 16-key tiles in turn, each with
 // its own running maximum and sum; the four are joined in LDS at the end.
 // The scores are computed transposed (keys x rows), so the row's maximum and
@@ -58,20 +58,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // lanes so that every load is 16 bytes: step i of the first product takes
 // element 16 c + 4 q + i, and output row m of accumulator (blk, j) is element
 // 64 blk + 4 m + j.
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<bf16_t>(const bf16_t* p) {
-  const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-  return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
-                     __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-template <typename T, int D>
+template <int D>
 __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
   constexpr int KT = 16, ROWS = 16, C = D / 16, NB = D / 64;
   __shared__ float s_o[4][ROWS][D + 4];
@@ -87,10 +76,10 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
   const int row = min(r0 + n, last);
   const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
   const int pos = req.kv - req.n + tok;
-  const T* qp = (const T*)a.q + (req.q0 + tok) * a.q_tok + hq * a.q_head + 4 * q4;
+  const float* qp = (const float*)a.q + (req.q0 + tok) * a.q_tok + hq * a.q_head + 4 * q4;
   float4 Q[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) Q[c] = load4<T>(qp + 16 * c);
+  for (int c = 0; c < C; ++c) Q[c] = load4(qp + 16 * c);
   v4f O[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
@@ -106,11 +95,11 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
       break;
     }
     const int64_t base = page * a.page + h * a.head + (int64_t)(k0 & ((1 << a.page_shift) - 1)) * a.row;
-    const T* kp = (const T*)a.k + base + (int64_t)n * a.row + 4 * q4;
+    const float* kp = (const float*)a.k + base + (int64_t)n * a.row + 4 * q4;
     v4f s = zero4();
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const float4 k = load4<T>(kp + 16 * c);
+      const float4 k = load4(kp + 16 * c);
       s = mfma_f32(k.x, Q[c].x, s);
       s = mfma_f32(k.y, Q[c].y, s);
       s = mfma_f32(k.z, Q[c].z, s);
@@ -137,14 +126,14 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
     for (int x = 0; x < NB; ++x)
 #pragma unroll
       for (int j = 0; j < 4; ++j) O[x][j] *= alpha;
-    const T* vp = (const T*)a.v + base + (int64_t)(4 * q4) * a.row + 4 * n;
+    const float* vp = (const float*)a.v + base + (int64_t)(4 * q4) * a.row + 4 * n;
     float4 V[4][NB];
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        V[j][x] = load4<T>(vp + (int64_t)j * a.row + 64 * x);
+        V[j][x] = load4(vp + (int64_t)j * a.row + 64 * x);
         odd |= nonfinite(V[j][x].x) || nonfinite(V[j][x].y) || nonfinite(V[j][x].z) ||
                nonfinite(V[j][x].w);
       }
@@ -155,12 +144,12 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
         const float mine = (kk & 2) ? ((kk & 1) ? p[3] : p[2]) : ((kk & 1) ? p[1] : p[0]);
         const float pk = __shfl(mine, (kk >> 2) * 16 + n, 64);
         if (!visible(k0 + kk, pos, a.window, a.sinks)) continue;
-        const T* vk = (const T*)a.v + base + (int64_t)kk * a.row;
+        const float* vk = (const float*)a.v + base + (int64_t)kk * a.row;
 #pragma unroll
         for (int x = 0; x < NB; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 v = load4<T>(vk + 64 * x + 16 * q4 + 4 * e);
+            const float4 v = load4(vk + 64 * x + 16 * q4 + 4 * e);
             O[x][0][e] += pk * v.x;
             O[x][1][e] += pk * v.y;
             O[x][2][e] += pk * v.z;
@@ -212,7 +201,7 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
     float o = den == 0.f && top == -INFINITY ? 0.f : num / den;
     if (spoilt) o = NAN;
     const int tk = (r0 + rr) / a.group, hd = h * a.group + (r0 + rr) - tk * a.group;
-    store_elem((T*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + d, o);
+    ((float*)a.out)[(req.q0 + tk) * a.o_tok + hd * a.o_head + d] = o;
     if (d == 0 && a.lse)
       a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] =
           spoilt ? NAN : (den == 0.f && top == -INFINITY ? -INFINITY : top * a.scale + logf(den));
@@ -222,6 +211,9 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
 // ---------------------------------------------------------------- handle
 struct domino_attention : HandleBase {
   domino_attention_config_t cfg;
+  int cus = 256;
+  float* part = nullptr;    // split segments: outputs, then (m, l)
+  int32_t* plan = nullptr;  // running sum of the requests' steps
 };
 
 static thread_local char t_err[256] = "";
@@ -255,6 +247,19 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
   h->cfg = *cfg;
   h->device = dev;
+  if (hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
+    (void)hipGetLastError();
+    h->cus = 256;
+  }
+  if (cfg->dtype == DOMINO_DTYPE_BF16) {
+    h->part = (float*)h->take(attend_split_floats(cfg->head_dim, h->cus) * sizeof(float));
+    h->plan = (int32_t*)h->take((size_t)(cfg->max_requests + 1) * sizeof(int32_t));
+    if (!h->part || !h->plan) {
+      h->release();
+      delete h;
+      return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: workspace allocation failed");
+    }
+  }
   *out = h;
   return DOMINO_OK;
 }
@@ -363,16 +368,15 @@ extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const 
   return launched(h, "append");
 }
 
-template <typename T>
 static void launch_attend_f32(int D, const AttendArgs& a, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
   const dim3 grid((unsigned)((rows + 15) / 16), a.kv_heads, a.requests);
   if (D == 64)
-    hipLaunchKernelGGL((attend_f32_kernel<T, 64>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attend_f32_kernel<64>), grid, dim3(256), 0, st, a);
   else if (D == 128)
-    hipLaunchKernelGGL((attend_f32_kernel<T, 128>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attend_f32_kernel<128>), grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((attend_f32_kernel<T, 256>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attend_f32_kernel<256>), grid, dim3(256), 0, st, a);
 }
 
 extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t* c,
@@ -434,9 +438,14 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
   a.scale_log2 = scale * 1.44269504088896340736f;
   DeviceGuard dg(h->device);
   (void)hipGetLastError();
-  if (f.dtype == DOMINO_DTYPE_BF16)
-    launch_attend_f32<bf16_t>(f.head_dim, a, (hipStream_t)stream);
-  else
-    launch_attend_f32<float>(f.head_dim, a, (hipStream_t)stream);
+  if (f.dtype == DOMINO_DTYPE_BF16) {
+    a.part_o = h->part;
+    a.part_ml = h->part + attend_split_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;
+    a.plan = h->plan;
+    a.min_share = 2;
+    launch_attend_split(f.head_dim, a, h->cus, (hipStream_t)stream);
+  } else {
+    launch_attend_f32(f.head_dim, a, (hipStream_t)stream);
+  }
   return launched(h, "run");
 }

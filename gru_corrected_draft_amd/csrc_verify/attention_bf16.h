@@ -1,0 +1,209 @@
+// What the bf16 attention kernels share: key tiles in LDS and the two products
+// on 32 x 32 matrix-core tiles.
+//
+// Both products are computed transposed, so that a lane keeps one row of the
+// row tile: S^T = K Q^T (keys x rows) and O^T = V^T P^T (elements x rows).
+// With V_MFMA_F32_32X32X16_BF16 lane l (n = l % 32, h = l / 32) holds in
+// accumulator register i row 8 (i / 4) + 4 h + i % 4 of column n.  The keys
+// are dealt to the rows of S^T so that registers 8 c .. 8 c + 7 are the keys
+// 16 c + 8 h .. + 7: exactly the slots of the second product's operand, so the
+// weights go from one product to the next without leaving their lane.
+//
+// A key tile is 32 rows of K and 32 of V, copied from the pages straight into
+// LDS as rows of 2 D bytes.  Within a row the 16-byte pieces are permuted by
+// an exclusive or with a function of the row, chosen so that neither the
+// fragments of K (16 rows at one piece) nor those of V (8 rows at four pieces,
+// read through the transposing load) meet in a bank more than they must.  The
+// copy writes LDS in lane order, so each lane picks the piece that belongs
+// where it lands.
+#pragma once
+#include "attention.h"
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+
+__device__ __forceinline__ v16f mfma_32x32(v8s a, v8s b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c,
+                                                 0, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int D>
+struct KeyTile {
+  static constexpr int kPieces = D / 8;            // 16-byte pieces of a row
+  static constexpr int kRow = 2 * D;               // bytes
+  static constexpr int kHalf = 32 * kRow;          // bytes of the K (or V) tile
+  static constexpr int kBytes = 2 * kHalf;
+  static constexpr int kChunkLoads = 16 * kRow / 1024;  // copies of 1 KB to 16 rows
+  static constexpr int kLoads = 4 * kChunkLoads;   // copies of a tile
+
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (D == 64) {
+      const int r = (row >> 1) & 7;
+      return ((r & 1) << 2) | (r & 2) | (r >> 2);
+    } else {
+      const int r = row & 15;
+      return ((r & 3) << 2) | (r >> 2);
+    }
+  }
+
+  // bytes from the start of a 16-row chunk in the cache to what lane `lane`
+  // copies in the chunk's j-th copy
+  static __device__ __forceinline__ uint32_t source(int j, int lane, int row_bytes) {
+    const int piece = j * 64 + lane, row = piece / kPieces;
+    return row * row_bytes + (((piece % kPieces) ^ swizzle(row)) << 4);
+  }
+
+  // LDS bytes (from the tile's start) of this lane's K fragment of step 0; step
+  // kc is at k_step(that, kc)
+  static __device__ __forceinline__ uint32_t k_first(int lane) {
+    const int m = lane & 31, h = lane >> 5;
+    const int key = 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);
+    return key * kRow + ((h ^ swizzle(key)) << 4);
+  }
+  static __device__ __forceinline__ uint32_t k_step(uint32_t first, int kc) {
+    return (first ^ ((kc & 7) << 5)) + (kc >> 3) * 256;
+  }
+  // of the half e of this lane's V fragment of elements 0..31, keys 0..15
+  static __device__ __forceinline__ uint32_t v_first(int lane, int e) {
+    const int g = lane >> 4, j = lane & 15;
+    const int key = 8 * (g >> 1) + 4 * e + (j >> 2), piece = 2 * (g & 1) + ((j & 3) >> 1);
+    return kHalf + key * kRow + ((piece ^ swizzle(key)) << 4) + ((j & 1) << 3);
+  }
+  static __device__ __forceinline__ uint32_t v_step(uint32_t first, int block, int c) {
+    return (first ^ ((block & 3) << 6)) + (block >> 2) * 256 + c * 16 * kRow;
+  }
+};
+
+// 16 bytes of LDS per lane
+__device__ __forceinline__ v8s lds_read16(const lds_byte* p) {
+  return *(const __attribute__((address_space(3))) v8s*)p;
+}
+// Transposing read: of the 16 x 4 block that 16 lanes point at (4 rows of 16
+// elements), lane j of them gets column j.
+__device__ __forceinline__ v4s lds_read_tr(const lds_byte* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
+}
+
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// One row tile's state in a wave: 32 rows, lane n = l % 32 holds row n in both
+// halves (m in both, l as each half's part).
+template <int D>
+struct RowState {
+  v16f o[D / 32];
+  float m, l;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+  }
+};
+
+// Scores of a tile to weights: updates the running maximum and sum, rescales
+// the sums so far where the maximum grew, and leaves the weights in s and,
+// rounded to bf16 for the second product, in p.
+template <int D>
+__device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[2], float scale_log2) {
+  float top = fmaxf(s[0], s[1]);
+#pragma unroll
+  for (int i = 2; i < 16; ++i) top = fmaxf(top, s[i]);
+  top = max_halves(top);
+  const float mn = fmaxf(st.m, top);
+  const float ref = mn == -INFINITY ? 0.f : mn * scale_log2;
+  if (__any(mn > st.m)) {
+    const float alpha = __builtin_amdgcn_exp2f(st.m * scale_log2 - ref);
+    st.l *= alpha;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) st.o[i] *= alpha;
+    st.m = mn;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale_log2, -ref));
+    sum += s[i];
+  }
+  st.l += sum;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    p[c] = __builtin_bit_cast(v8s, (u32x4{w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]}));
+}
+
+// O^T += V^T P^T for one tile
+template <int D, int NT>
+__device__ __forceinline__ void weighted_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D> (&st)[NT],
+                                                const v8s (&p)[NT][2]) {
+#pragma unroll
+  for (int blk = 0; blk < D / 32; ++blk)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const v4s lo = lds_read_tr(tile + KeyTile<D>::v_step(v0[0], blk, c));
+      const v4s hi = lds_read_tr(tile + KeyTile<D>::v_step(v0[1], blk, c));
+      const v8s v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) st[t].o[blk] = mfma_32x32(v, p[t][c], st[t].o[blk]);
+    }
+}
+
+// whether the tile's values hold an infinity or NaN
+template <int D>
+__device__ __forceinline__ bool odd_values(const lds_byte* tile, int lane) {
+  bool odd = false;
+#pragma unroll 4
+  for (int i = 0; i < KeyTile<D>::kHalf / 1024; ++i) {
+    const v8s v = lds_read16(tile + KeyTile<D>::kHalf + i * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) odd |= (v[j] & 0x7F80) == 0x7F80;
+  }
+  return __any(odd);
+}
+
+// The same sum for a tile with infinities or NaN that some rows do not see:
+// the product would multiply them by a weight of zero, so the values are added
+// key by key to the rows that see them.
+template <int D>
+__device__ __forceinline__ void careful_values(const lds_byte* tile, RowState<D>& st, const v16f& s, int k0, int pos,
+                                               int window, int sinks, int lane) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int blk = 0; blk < D / 32; ++blk)
+#pragma unroll 1
+    for (int key = 0; key < 32; ++key) {
+      const int want = 8 * (key >> 4) + (key & 7);
+      float mine = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mine = i == want ? s[i] : mine;
+      const float p = __shfl(mine, (lane & 31) + 32 * ((key >> 3) & 1), 64);
+      if (!visible(k0 + key, pos, window, sinks)) continue;
+      const lds_byte* row = tile + KeyTile<D>::kHalf + key * KeyTile<D>::kRow;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        // elements 32 blk + 8 a + 4 h ..: half a piece
+        const int piece = (4 * blk + a) ^ KeyTile<D>::swizzle(key);
+        const v4s v = *(const __attribute__((address_space(3))) v4s*)(row + piece * 16 + h * 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.o[blk][4 * a + j] += p * bf16_to_f32((uint16_t)v[j]);
+      }
+    }
+}
+
+void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st);
+size_t attend_split_floats(int head_dim, int cus);
