@@ -52,8 +52,11 @@ struct Request {
   bool bad;
 };
 
-__device__ __forceinline__ Request request_of(const int32_t* q_start, const int32_t* kv_len, int b,
+__device__ __forceinline__ Request request_of(const int32_t* q_start_, const int32_t* kv_len_, int b,
                                               int tokens, int max_new, int max_kv) {
+  // constant memory: scalar loads where b is the same in every lane
+  const_i32* const q_start = (const_i32*)q_start_;
+  const_i32* const kv_len = (const_i32*)kv_len_;
   const int s0 = q_start[b], s1 = q_start[b + 1];
   Request r;
   r.kv = kv_len[b];

@@ -148,18 +148,16 @@ __device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[
 }
 
 // O^T += V^T P^T for one tile
-template <int D, int NT>
-__device__ __forceinline__ void weighted_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D> (&st)[NT],
-                                                const v8s (&p)[NT][2]) {
+template <int D>
+__device__ __forceinline__ void weighted_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D>& st,
+                                                const v8s (&p)[2]) {
 #pragma unroll
   for (int blk = 0; blk < D / 32; ++blk)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const v4s lo = lds_read_tr(tile + KeyTile<D>::v_step(v0[0], blk, c));
       const v4s hi = lds_read_tr(tile + KeyTile<D>::v_step(v0[1], blk, c));
-      const v8s v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) st[t].o[blk] = mfma_32x32(v, p[t][c], st[t].o[blk]);
+      st.o[blk] = mfma_32x32(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p[c], st.o[blk]);
     }
 }
 
@@ -176,33 +174,48 @@ __device__ __forceinline__ bool odd_values(const lds_byte* tile, int lane) {
   return __any(odd);
 }
 
-// The same sum for a tile with infinities or NaN that some rows do not see:
-// the product would multiply them by a weight of zero, so the values are added
-// key by key to the rows that see them.
+// The same sum for a tile that holds infinities or NaN and has rows that do not
+// see all its keys: a product would multiply those values by a weight of zero.
+// They count as zero in the sum; a second product counts, for each row and
+// element, the +inf, -inf and NaN among the keys that the row sees (1, 2^10
+// and 2^20 apiece, at most 32 of each: exact), and the row gets what their sum
+// is.
 template <int D>
-__device__ __forceinline__ void careful_values(const lds_byte* tile, RowState<D>& st, const v16f& s, int k0, int pos,
-                                               int window, int sinks, int lane) {
-  const int h = lane >> 5;
+__device__ __forceinline__ void careful_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D>& st,
+                                               const v8s (&p)[2], int first_key, int pos, int window, int sinks) {
+  v8s sees[2];
 #pragma unroll
-  for (int blk = 0; blk < D / 32; ++blk)
-#pragma unroll 1
-    for (int key = 0; key < 32; ++key) {
-      const int want = 8 * (key >> 4) + (key & 7);
-      float mine = 0.f;
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mine = i == want ? s[i] : mine;
-      const float p = __shfl(mine, (lane & 31) + 32 * ((key >> 3) & 1), 64);
-      if (!visible(k0 + key, pos, window, sinks)) continue;
-      const lds_byte* row = tile + KeyTile<D>::kHalf + key * KeyTile<D>::kRow;
+    for (int j = 0; j < 8; ++j) sees[c][j] = visible(first_key + 16 * c + j, pos, window, sinks) ? 0x3F80 : 0;
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        // elements 32 blk + 8 a + 4 h ..: half a piece
-        const int piece = (4 * blk + a) ^ KeyTile<D>::swizzle(key);
-        const v4s v = *(const __attribute__((address_space(3))) v4s*)(row + piece * 16 + h * 8);
+  for (int blk = 0; blk < D / 32; ++blk) {
+    v16f odd;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) st.o[blk][4 * a + j] += p * bf16_to_f32((uint16_t)v[j]);
+    for (int i = 0; i < 16; ++i) odd[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const v4s lo = lds_read_tr(tile + KeyTile<D>::v_step(v0[0], blk, c));
+      const v4s hi = lds_read_tr(tile + KeyTile<D>::v_step(v0[1], blk, c));
+      v8s v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), mark;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool fine = (v[j] & 0x7F80) != 0x7F80;
+        // bf16 of 2^20, 2^10 and 1
+        mark[j] = fine ? 0 : (v[j] & 0x7F) ? 0x4980 : v[j] < 0 ? 0x4480 : 0x3F80;
+        v[j] = fine ? v[j] : (short)0;
       }
+      st.o[blk] = mfma_32x32(v, p[c], st.o[blk]);
+      odd = mfma_32x32(mark, sees[c], odd);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = (int)odd[i];
+      const bool minus = (k >> 10) & 1023, plus = k & 1023;
+      st.o[blk][i] += k >> 20 || (plus && minus) ? NAN : minus ? -INFINITY : plus ? INFINITY : 0.f;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st);

@@ -1,32 +1,47 @@
-// bf16 attention of few rows over long caches: the work of all requests is one
-// list of steps, dealt evenly to the workgroups, and split segments are joined
-// by a second launch.
+// bf16 attention kernels.
+//
+// A workgroup takes R * 32 rows of one request and key head (a row tile) and S
+// streams of key tiles: wave w works for row group w / S on stream w % S, with
+// its own running maximum and sum.  The streams of a row group are joined in
+// LDS at the end.  One group of 32 rows to a wave keeps a wave's sums, queries
+// and scores in 256 registers; with more rows the sums move to accumulation
+// registers, and the moves cost more than the halved reads of LDS save.
+//   R = 1: a wave copies its own tiles into its own ring and never waits for
+//          another; no barrier in the walk.  For few rows, bound by the
+//          cache's bytes.
+//   R > 1: the R waves on a stream share its tiles, each copies a part, and a
+//          barrier separates the tiles.  R = 2 and 4 for up to 64 and 128 rows,
+//          so that a draft block of 16 positions with 4 or 8 heads to a key
+//          head reads its keys once; R = 8 for prompts, bound by the matrix
+//          cores.
 //
 // Steps.  A segment is one (request, row tile, key head); it has one step for
-// each W key tiles (one for each of the workgroup's W waves), and at least
-// one, so that rows without keys are written too.  The steps of all segments
-// in order are cut into equal shares, one for each workgroup, whatever the
-// lengths of the requests: each workgroup sums up the lengths itself.  A share
-// ends at most two segments inside; those leave their unnormalised output,
-// maximum and sum in the workspace.
-//
-// Bound by the cache's bytes.  Each wave copies its own tiles into its own
-// ring in LDS and never waits for another: no barrier in the walk.
+// each S key tiles, and at least one, so that rows without keys are written
+// too.  With WHOLE a workgroup takes one segment.  Otherwise the steps of all
+// segments in order are cut into equal shares, one for each workgroup,
+// whatever the lengths of the requests: each workgroup sums up the lengths
+// itself.  A share ends at most two segments inside; those leave their
+// unnormalised output, maximum and sum in the workspace, and a second launch
+// joins them.
 #include "attention_bf16.h"
 
 namespace {
 
-template <int D>
-struct Split {
-  static constexpr int kWaves = D == 256 ? 2 : 4;
-  static constexpr int kRing = D == 64 ? 4 : 2;
-  static constexpr int kRingBytes = kRing * KeyTile<D>::kBytes;  // of a wave
-  static constexpr int kLds = kWaves * kRingBytes;               // 128 KB for every D
-  static constexpr int kThreads = kWaves * 64;
+template <int D, int R>
+struct Shape {
+  static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : 8 / R);  // streams
+  static constexpr int W = R * S;                                                // waves
+  static constexpr int kThreads = 64 * W;
+  static constexpr int kRows = 32 * R;
+  // tiles of a stream in LDS: 128 KB in all at D = 128 and 256 up to R = 4
+  static constexpr int kRing = D == 64 ? 4 : (R <= 2 ? 2 : 4);
+  static constexpr int kLds = S * kRing * KeyTile<D>::kBytes;
+  static constexpr int kJoin = kLds / (W * D * 4) < 32 ? kLds / (W * D * 4) : 32;  // rows joined at a time
+  static constexpr int kLoads = KeyTile<D>::kLoads / R;  // copies of a tile by one wave
 };
 
-__device__ __forceinline__ int steps_of(int count, int waves) {
-  return count > 0 ? (count + waves - 1) / waves : 1;
+__device__ __forceinline__ int steps_of(int count, int streams) {
+  return count > 0 ? (count + streams - 1) / streams : 1;
 }
 
 template <int ROWS>
@@ -36,68 +51,97 @@ __device__ __forceinline__ KeySpan row_tile_span(const AttendArgs& a, const Requ
   return key_span<32>(r, r0 / a.group, last / a.group, a.window, a.sinks);
 }
 
-// steps of request b
-template <int ROWS, int W>
-__device__ __forceinline__ int request_steps(const AttendArgs& a, int b) {
-  const Request r = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+// steps of a request
+template <int ROWS, int S>
+__device__ __forceinline__ int request_steps(const AttendArgs& a, const Request& r) {
   int n = 0;
-  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += steps_of(row_tile_span<ROWS>(a, r, rt).count, W);
+  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += steps_of(row_tile_span<ROWS>(a, r, rt).count, S);
   return n * a.kv_heads;
 }
 
-template <int D, int NT>
-__global__ __launch_bounds__(Split<D>::kThreads, D * NT < 128 ? 2 : 1) void attend_split_kernel(AttendArgs a) {
+template <int D, int R, bool WHOLE>
+__global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void attend_split_kernel(AttendArgs a) {
   using T = KeyTile<D>;
-  constexpr int W = Split<D>::kWaves, ROWS = 32 * NT, RING = Split<D>::kRing, THREADS = Split<D>::kThreads;
+  using C = Shape<D, R>;
+  constexpr int S = C::S, ROWS = C::kRows, RING = C::kRing, THREADS = C::kThreads, JOIN = C::kJoin;
   extern __shared__ __align__(1024) unsigned char ring[];
-  __shared__ int s_pre[1025];
-  __shared__ int s_sum[4];
-  __shared__ float s_m[W][ROWS], s_l[W][ROWS];
+  __shared__ int s_sum[C::W];
+  __shared__ float s_m[C::W][32], s_l[C::W][32];
+  __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 31, h2 = lane >> 5;
+  const int rg = w / S, stream = w - rg * S;
 
-  // running sum of the requests' steps
-  int carry = 0;
-  for (int b0 = 0; b0 < a.requests; b0 += THREADS) {
-    const int b = b0 + tid;
-    int x = b < a.requests ? request_steps<ROWS, W>(a, b) : 0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(x, d, 64);
-      if (lane >= d) x += y;
+  int b = 0, begin = 0, at = 0, end = 1, upto = 0;
+  Request mine{0, 0, 0, false};
+  const bool few = a.requests <= 64;
+  if constexpr (!WHOLE) {
+    // Running sum of the requests' steps.  Up to 64 requests a wave holds it in
+    // its lanes, each wave for itself, without a barrier; beyond that it goes
+    // through LDS, over the rings.
+    int total;
+    if (few) {
+      if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
+      upto = lane < a.requests ? request_steps<ROWS, S>(a, mine) : 0;
+  #pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(upto, d, 64);
+        if (lane >= d) upto += y;
+      }
+      total = __builtin_amdgcn_readlane(upto, 63);
+      if (blockIdx.x == 0 && w == 0) {
+        if (lane == 0) a.plan[0] = 0;
+        if (lane < a.requests) a.plan[lane + 1] = upto;
+      }
+    } else {
+      int* const s_pre = (int*)ring;
+      int carry = 0;
+      for (int b0 = 0; b0 < a.requests; b0 += THREADS) {
+        const int b = b0 + tid;
+        int x = b < a.requests
+                    ? request_steps<ROWS, S>(a, request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv))
+                    : 0;
+  #pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int y = __shfl_up(x, d, 64);
+          if (lane >= d) x += y;
+        }
+        if (lane == 63) s_sum[w] = x;
+        __syncthreads();
+        for (int i = 0; i < w; ++i) x += s_sum[i];
+        if (b < a.requests) s_pre[b + 1] = carry + x;
+        for (int i = 0; i < C::W; ++i) carry += s_sum[i];
+        __syncthreads();
+      }
+      if (tid == 0) s_pre[0] = 0;
+      __syncthreads();
+      total = __builtin_amdgcn_readfirstlane(carry);
+      if (blockIdx.x == 0)
+        for (int b = tid; b <= a.requests; b += THREADS) a.plan[b] = s_pre[b];
     }
-    if (lane == 63) s_sum[w] = x;
-    __syncthreads();
-    for (int i = 0; i < w; ++i) x += s_sum[i];
-    if (b < a.requests) s_pre[b + 1] = carry + x;
-    for (int i = 0; i < W; ++i) carry += s_sum[i];
-    __syncthreads();
-  }
-  if (tid == 0) s_pre[0] = 0;
-  __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(carry);
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= a.requests; b += THREADS) a.plan[b] = s_pre[b];
-  const int share = max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  int at = blockIdx.x * share;
-  const int end = min(at + share, total);
-  if (at >= end) return;
+    const int share = max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    at = blockIdx.x * share;
+    end = min(at + share, total);
+    if (at >= end) return;
 
-  // request of the first step: the last one that begins at or before it
-  int b = 0;
-  {
-    int hi = a.requests;  // s_pre[b] <= at < s_pre[hi]
-    while (hi - b > 1) {
-      const int mid = (b + hi) >> 1;
-      if (s_pre[mid] <= at)
-        b = mid;
-      else
-        hi = mid;
+    // request of the first step (the last one that begins at or before it) and
+    // the step its own begin at
+    if (!few) {
+      const int* const s_pre = (const int*)ring;
+      int hi = a.requests;  // s_pre[b] <= at < s_pre[hi]
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (s_pre[mid] <= at)
+          b = mid;
+        else
+          hi = mid;
+      }
+      begin = __builtin_amdgcn_readfirstlane(s_pre[b]);
+      b = __builtin_amdgcn_readfirstlane(b);
+      __syncthreads();  // the rings are free again
     }
   }
-  b = __builtin_amdgcn_readfirstlane(b);
 
-  lds_byte* const lds = (lds_byte*)ring;
-  lds_byte* const mine = lds + w * Split<D>::kRingBytes;
+  lds_byte* const own = (lds_byte*)ring + stream * (RING * T::kBytes);
   const uint32_t k0_off = T::k_first(lane);
   const uint32_t v0_off[2] = {T::v_first(lane, 0), T::v_first(lane, 1)};
   uint32_t src[T::kChunkLoads];
@@ -105,175 +149,244 @@ __global__ __launch_bounds__(Split<D>::kThreads, D * NT < 128 ? 2 : 1) void atte
   for (int j = 0; j < T::kChunkLoads; ++j) src[j] = T::source(j, lane, 2 * a.row);
 
   while (at < end) {
-    while (s_pre[b + 1] <= at) ++b;  // requests without rows have no steps
-    const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
-    int off = at - __builtin_amdgcn_readfirstlane(s_pre[b]), rt = 0;
-    KeySpan span = row_tile_span<ROWS>(a, req, 0);
-    int seg = steps_of(span.count, W);
-    while (off >= seg * a.kv_heads) {
-      off -= seg * a.kv_heads;
-      span = row_tile_span<ROWS>(a, req, ++rt);
-      seg = steps_of(span.count, W);
+    Request req;
+    int rt = 0, h, first, stop, seg;
+    KeySpan span;
+    if constexpr (WHOLE) {
+      // key heads vary fastest, so that the row tiles of a head, which read the
+      // same keys, meet in one XCD's cache when there are 8 of them; the last
+      // row tiles see the most keys and go first
+      b = blockIdx.z;
+      h = blockIdx.x;
+      rt = gridDim.y - 1 - blockIdx.y;
+      req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+      if (rt * ROWS >= req.n * a.group) return;
+      span = row_tile_span<ROWS>(a, req, rt);
+      first = 0;
+      stop = seg = steps_of(span.count, S);
+    } else {
+      if (few) {
+        b = __builtin_ctzll(__ballot(upto > at));
+        begin = b ? __builtin_amdgcn_readlane(upto, b - 1) : 0;
+        req.q0 = __builtin_amdgcn_readlane(mine.q0, b);
+        req.n = __builtin_amdgcn_readlane(mine.n, b);
+        req.kv = __builtin_amdgcn_readlane(mine.kv, b);
+        req.bad = __builtin_amdgcn_readlane((int)mine.bad, b);
+      } else {
+        for (;;) {  // requests without rows have no steps
+          req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+          const int steps = request_steps<ROWS, S>(a, req);
+          if (at < begin + steps) break;
+          begin += steps;
+          ++b;
+        }
+      }
+      int off = at - begin;
+      span = row_tile_span<ROWS>(a, req, 0);
+      seg = steps_of(span.count, S);
+      while (off >= seg * a.kv_heads) {
+        off -= seg * a.kv_heads;
+        span = row_tile_span<ROWS>(a, req, ++rt);
+        seg = steps_of(span.count, S);
+      }
+      h = off / seg;
+      first = off - h * seg;
+      stop = min(seg, first + end - at);
     }
-    const int h = off / seg, first = off - h * seg, stop = min(seg, first + end - at);
-
-    const int rows = req.n * a.group, r0 = rt * ROWS, last = min(r0 + ROWS, rows) - 1;
-    v8s Q[NT][D / 16];
-    int pos[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int row = min(r0 + 32 * t + n, last), tok = row / a.group;
-      pos[t] = req.kv - req.n + tok;
-      const bf16_t* qp = (const bf16_t*)a.q + (req.q0 + tok) * a.q_tok +
-                         (h * a.group + row - tok * a.group) * a.q_head + 8 * h2;
-#pragma unroll
-      for (int kc = 0; kc < D / 16; ++kc) Q[t][kc] = load_frag_bf16(qp + 16 * kc);
-    }
-    RowState<D> st[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) st[t].clear();
     bool bad = req.bad;
 
     const_i32* const table = (const_i32*)(a.table + b * a.table_stride);
     const int64_t head = h * a.head;
     const int page_mask = (1 << a.page_shift) - 1;
-    const int tiles = min(stop * W, span.count);
-    int next = first * W + w, ahead = 0, slot_in = 0, slot_out = 0;
+    const int tiles = min(stop * S, span.count);
+    int next = first * S + stream, ahead = 0, slot_in = 0, slot_out = 0;
 
-    // copies the wave's next tile into its ring
+    // where the 16 keys from `key` on lie, in elements; keys that no row sees
+    // may have no page and take that of `other`, the tile's other half
+    auto chunk = [&](int key, int other) -> int64_t {
+      const bool seen = key < span.hi && (key + 15 >= span.lo || key < a.sinks);
+      int page = table[(seen ? key : other) >> a.page_shift];
+      if (page < 0 || page >= a.num_pages) {
+        bad = true;
+        page = 0;
+      }
+      return page * a.page + head + (int64_t)(key & page_mask) * a.row;
+    };
+    auto copy = [&](const void* cache, int64_t at16, const lds_byte* dst, int j0, int j1) {
+      const char* from = (const char*)cache + 2 * at16;
+#pragma unroll
+      for (int j = 0; j < T::kChunkLoads; ++j)
+        if (j >= j0 && j < j1)
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + src[j]),
+                                           (__attribute__((address_space(3))) void*)(dst + j * 1024), 16, 0, 0);
+    };
+    // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
       const int key = tile_of(span, next) * 32;
-      next += W;
+      next += S;
       ++ahead;
-      const lds_byte* dst = mine + slot_in * T::kBytes;
+      const lds_byte* dst = own + slot_in * T::kBytes;
       slot_in = slot_in + 1 == RING ? 0 : slot_in + 1;
-      int64_t base[2];
-      int page[2];
-      // a chunk of 16 keys lies in one page; one that no row sees may have
-      // none, and takes its neighbour's
-      const bool see0 = key < span.hi && (key + 15 >= span.lo || key < a.sinks);
-      const bool see1 = key + 16 < span.hi && (key + 31 >= span.lo || key + 16 < a.sinks);
-      page[0] = table[(see0 ? key : key + 16) >> a.page_shift];
-      page[1] = table[(see1 ? key + 16 : key) >> a.page_shift];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (page[c] < 0 || page[c] >= a.num_pages) {
-          bad = true;
-          page[c] = 0;
+      if constexpr (R >= 4) {  // 16 rows of K or of V, or half the copies of them
+        constexpr int PART = R / 4, LOADS = T::kChunkLoads / PART;
+        const int x = rg / (2 * PART), c = rg / PART % 2, j0 = rg % PART * LOADS;
+        copy(x ? a.v : a.k, chunk(key + 16 * c, key + 16 - 16 * c), dst + x * T::kHalf + c * (T::kHalf / 2), j0,
+             j0 + LOADS);
+      } else {
+        const int64_t c0 = chunk(key, key + 16), c1 = chunk(key + 16, key);
+        if (R == 1 || rg == 0) {
+          copy(a.k, c0, dst, 0, T::kChunkLoads);
+          copy(a.k, c1, dst + T::kHalf / 2, 0, T::kChunkLoads);
         }
-        base[c] = 2 * (page[c] * a.page + head + (int64_t)((key + 16 * c) & page_mask) * a.row);
+        if (R == 1 || rg == 1) {
+          copy(a.v, c0, dst + T::kHalf, 0, T::kChunkLoads);
+          copy(a.v, c1, dst + T::kHalf + T::kHalf / 2, 0, T::kChunkLoads);
+        }
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const char* from = (const char*)(x ? a.v : a.k) + base[c];
-#pragma unroll
-          for (int j = 0; j < T::kChunkLoads; ++j)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(from + src[j]),
-                (__attribute__((address_space(3))) void*)(dst + x * T::kHalf + (c * T::kChunkLoads + j) * 1024), 16,
-                0, 0);
-        }
     };
-    for (int i = first * W + w - (RING - 1) * W; i < tiles; i += W) {
-      if (next < tiles) fetch();
-      if (i < first * W) continue;  // fills the ring
+    // waits until the oldest of `ahead` tiles in flight has landed
+    auto land = [&]() {
       --ahead;
-      if (ahead >= RING - 1)
-        wait_copies<(RING - 1) * T::kLoads>();
-      else if (RING > 2 && ahead == 2)
-        wait_copies<2 * T::kLoads>();
-      else if (RING > 2 && ahead == 1)
-        wait_copies<T::kLoads>();
+      if (ahead >= 3)
+        wait_copies<(RING > 3 ? 3 : 0) * C::kLoads>();
+      else if (ahead == 2)
+        wait_copies<(RING > 2 ? 2 : 0) * C::kLoads>();
+      else if (ahead == 1)
+        wait_copies<C::kLoads>();
       else
         wait_copies<0>();
-      const lds_byte* tile = mine + slot_out * T::kBytes;
+    };
+    // the ring's first copies leave before the queries are read, so that the
+    // wait for the queries does not hold them up
+#pragma unroll 1
+    for (int i = 0; i < RING - 1; ++i)
+      if (next < tiles) fetch();
+
+    const int rows = req.n * a.group, r0 = rt * ROWS, last = min(r0 + ROWS, rows) - 1;
+    const int w0 = r0 + rg * 32;  // this wave's first row
+    v8s Q[D / 16];
+    int pos;
+    {
+      const int row = min(w0 + n, last), tok = row / a.group;
+      pos = req.kv - req.n + tok;
+      const bf16_t* qp = (const bf16_t*)a.q + (req.q0 + tok) * a.q_tok +
+                         (h * a.group + row - tok * a.group) * a.q_head + 8 * h2;
+#pragma unroll
+      for (int kc = 0; kc < D / 16; ++kc) Q[kc] = load_frag_bf16(qp + 16 * kc);
+    }
+    // positions of this wave's rows
+    KeySpan seen = span;
+    if (R > 1) {
+      seen.pmin = req.kv - req.n + min(w0, last) / a.group;
+      seen.pmax = req.kv - req.n + min(w0 + 31, last) / a.group;
+    }
+    RowState<D> st;
+    st.clear();
+
+#pragma unroll 1
+    for (int i = first * S + stream; i - stream < tiles; i += S) {
+      if constexpr (R == 1) {
+        if (i >= tiles) break;
+        if (next < tiles) fetch();
+        land();
+      } else {
+        // every wave's copies of this tile have landed, and every wave is done
+        // with the tile before it, whose place the next copies take
+        if (i < tiles) land();
+        asm volatile("s_barrier" ::: "memory");
+        if (next < tiles) fetch();
+        if (i >= tiles) continue;
+      }
+      const lds_byte* tile = own + slot_out * T::kBytes;
       slot_out = slot_out + 1 == RING ? 0 : slot_out + 1;
       const int key = tile_of(span, i) * 32;
-      v16f s[NT];
+      if (R > 1 && (key > seen.pmax ||
+                    (a.window && key + 31 <= seen.pmin - a.window && key >= a.sinks)))
+        continue;  // none of this wave's rows sees it
+      const bool edge = !all_visible(seen, key, 32, a.window, a.sinks);
+      const bool odd = edge && odd_values<D>(tile, lane);
+      v16f s;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int j = 0; j < 16; ++j) s[j] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[t][j] = 0.f;
+      for (int kc = 0; kc < D / 16; ++kc) s = mfma_32x32(lds_read16(tile + T::k_step(k0_off, kc)), Q[kc], s);
+      if (edge) {
 #pragma unroll
-      for (int kc = 0; kc < D / 16; ++kc) {
-        const v8s k = lds_read16(tile + T::k_step(k0_off, kc));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = mfma_32x32(k, Q[t][kc], s[t]);
+        for (int j = 0; j < 16; ++j)
+          if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[j] = -INFINITY;
       }
-      const bool edge = !all_visible(span, key, 32, a.window, a.sinks);
-      v8s p[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos[t], a.window, a.sinks)) s[t][j] = -INFINITY;
-        }
-        softmax_step<D>(s[t], st[t], p[t], a.scale_log2);
-      }
-      if (edge && odd_values<D>(tile, lane)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) careful_values<D>(tile, st[t], s[t], key, pos[t], a.window, a.sinks, lane);
-      } else {
-        weighted_values<D, NT>(tile, v0_off, st, p);
-      }
+      v8s p[2];
+      softmax_step<D>(s, st, p, a.scale_log2);
+      if (__builtin_expect(odd, 0))
+        careful_values<D>(tile, v0_off, st, p, key + 8 * h2, pos, a.window, a.sinks);
+      else
+        weighted_values<D>(tile, v0_off, st, p);
     }
 
-    // join the waves: each writes its rows to LDS over the rings
-    __syncthreads();
+    // join the streams of a row group: each wave writes JOIN rows at a time to
+    // LDS, over the rings
+    const bool whole = WHOLE || (first == 0 && stop == seg);
+    const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0);
     float* const so = (float*)ring;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float l = sum_halves(st[t].l);
-      const int row = 32 * t + n;
+    if (tid == 0) s_bad = 0;
+    {
+      const float l = sum_halves(st.l);
       if (h2 == 0) {
-        s_m[w][row] = st[t].m;
-        s_l[w][row] = bad ? NAN : l;
+        s_m[w][n] = st.m;
+        s_l[w][n] = l;
       }
-#pragma unroll
-      for (int blk = 0; blk < D / 32; ++blk)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int piece = (8 * blk + 2 * x + h2) ^ (row & (D / 4 - 1));
-          *(float4*)(so + ((w * ROWS + row) * D + piece * 4)) =
-              make_float4(st[t].o[blk][4 * x], st[t].o[blk][4 * x + 1], st[t].o[blk][4 * x + 2], st[t].o[blk][4 * x + 3]);
-        }
     }
     __syncthreads();
-    const bool whole = first == 0 && stop == seg;
-    const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0);
-    for (int i = tid; i < (last - r0 + 1) * (D / 4); i += THREADS) {
-      const int row = i / (D / 4), piece = i - row * (D / 4);
-      float top = -INFINITY;
+    if (bad) s_bad = 1;
+#pragma unroll 1
+    for (int j0 = 0; j0 < 32; j0 += JOIN) {
+      if (j0) __syncthreads();
+      if (n >= j0 && n < j0 + JOIN) {
 #pragma unroll
-      for (int x = 0; x < W; ++x) top = fmaxf(top, s_m[x][row]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f;
+        for (int blk = 0; blk < D / 32; ++blk)
 #pragma unroll
-      for (int x = 0; x < W; ++x) {
-        const float f = __builtin_amdgcn_exp2f((s_m[x][row] - ref) * a.scale_log2);
-        den += f * s_l[x][row];
-        const float4 y = *(const float4*)(so + ((x * ROWS + row) * D + (piece ^ (row & (D / 4 - 1))) * 4));
-        o.x += f * y.x;
-        o.y += f * y.y;
-        o.z += f * y.z;
-        o.w += f * y.w;
+          for (int x = 0; x < 4; ++x) {
+            const int piece = (8 * blk + 2 * x + h2) ^ (n & (D / 4 - 1));
+            *(float4*)(so + ((w * JOIN + n - j0) * D + piece * 4)) = make_float4(
+                st.o[blk][4 * x], st.o[blk][4 * x + 1], st.o[blk][4 * x + 2], st.o[blk][4 * x + 3]);
+          }
       }
-      if (whole) {
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        const int tok = (r0 + row) / a.group, hq = h * a.group + r0 + row - tok * a.group;
-        *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
-            u32x2{pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)};
-        if (piece == 0 && a.lse)
-          a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
-      } else {
-        *(float4*)(a.part_o + (part * ROWS + row) * D + 4 * piece) = o;
-        if (piece == 0) {
-          a.part_ml[(part * ROWS + row) * 2] = top;
-          a.part_ml[(part * ROWS + row) * 2 + 1] = den;
+      __syncthreads();
+      const bool spoilt = s_bad != 0;
+      for (int i = tid; i < R * JOIN * (D / 4); i += THREADS) {
+        const int piece = i % (D / 4), row = j0 + (i / (D / 4)) % JOIN, g = i / (D / 4) / JOIN;
+        const int in_tile = g * 32 + row;  // row of the row tile
+        if (r0 + in_tile > last) continue;
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[g * S + x][row]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = spoilt ? NAN : 0.f;
+#pragma unroll
+        for (int x = 0; x < S; ++x) {
+          const float f = __builtin_amdgcn_exp2f((s_m[g * S + x][row] - ref) * a.scale_log2);
+          den += f * s_l[g * S + x][row];
+          const float4 y =
+              *(const float4*)(so + (((g * S + x) * JOIN + row - j0) * D + (piece ^ (row & (D / 4 - 1))) * 4));
+          o.x += f * y.x;
+          o.y += f * y.y;
+          o.z += f * y.z;
+          o.w += f * y.w;
+        }
+        if (whole) {
+          const float inv = den == 0.f ? 0.f : 1.f / den;
+          const int r = r0 + in_tile, tok = r / a.group, hq = h * a.group + r - tok * a.group;
+          *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
+              u32x2{pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)};
+          if (piece == 0 && a.lse)
+            a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
+        } else {
+          *(float4*)(a.part_o + (part * ROWS + in_tile) * D + 4 * piece) = o;
+          if (piece == 0) {
+            a.part_ml[(part * ROWS + in_tile) * 2] = top;
+            a.part_ml[(part * ROWS + in_tile) * 2 + 1] = den;
+          }
         }
       }
     }
@@ -284,9 +397,9 @@ __global__ __launch_bounds__(Split<D>::kThreads, D * NT < 128 ? 2 : 1) void atte
 
 // Joins the parts of split segments: 256 threads take 1024 / D rows of one
 // (request, row tile, key head).
-template <int D, int NT>
+template <int D, int R>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int workers, int row_groups) {
-  constexpr int W = Split<D>::kWaves, ROWS = 32 * NT, PER = 1024 / D;
+  constexpr int S = Shape<D, R>::S, ROWS = Shape<D, R>::kRows, PER = 1024 / D;
   const int b = blockIdx.z, rt = blockIdx.x, h = blockIdx.y / row_groups, group = blockIdx.y - h * row_groups;
   const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
   const int rows = req.n * a.group, r0 = rt * ROWS;
@@ -295,8 +408,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
   const int total = a.plan[a.requests];
   const int share = max(a.min_share, (total + workers - 1) / workers);
   int from = a.plan[b];
-  for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, W) * a.kv_heads;
-  const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, W);
+  for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, S) * a.kv_heads;
+  const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, S);
   from += h * seg;
   const int g0 = from / share, g1 = (from + seg - 1) / share;
   if (g0 == g1) return;
@@ -325,39 +438,58 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
     a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
 }
 
-template <int D, int NT>
-void launch(const AttendArgs& a, int cus, hipStream_t st) {
-  constexpr int ROWS = 32 * NT, W = Split<D>::kWaves, PER = 1024 / D;
-  const int64_t rows = (int64_t)a.max_new * a.group;
-  const int64_t row_tiles = (rows + ROWS - 1) / ROWS;
-  const int64_t seg_most = a.max_kv > 32 * W ? (a.max_kv + 32 * W - 1) / (32 * W) + 1 : 1;
-  const int64_t most = (int64_t)a.requests * row_tiles * a.kv_heads * seg_most;
-  const int64_t need = (most + a.min_share - 1) / a.min_share;
-  const int workers = (int)(need < cus ? need : cus);
-  static const hipError_t big = hipFuncSetAttribute((const void*)&attend_split_kernel<D, NT>,
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, Split<D>::kLds);
+template <int D, int R, bool WHOLE>
+void launch_kernel(const AttendArgs& a, dim3 grid, hipStream_t st) {
+  using C = Shape<D, R>;
+  // more than the default 64 KB of LDS; asked for once
+  static const hipError_t big = hipFuncSetAttribute((const void*)&attend_split_kernel<D, R, WHOLE>,
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
   (void)big;
-  hipLaunchKernelGGL((attend_split_kernel<D, NT>), dim3(workers), dim3(Split<D>::kThreads), Split<D>::kLds, st, a);
-  if (workers == 1) return;  // nothing is split
-  const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
-  hipLaunchKernelGGL((attend_join_kernel<D, NT>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests), dim3(256),
-                     0, st, a, workers, groups);
+  hipLaunchKernelGGL((attend_split_kernel<D, R, WHOLE>), grid, dim3(C::kThreads), C::kLds, st, a);
 }
 
+template <int D, int R>
+void launch(const AttendArgs& a, int cus, hipStream_t st) {
+  using C = Shape<D, R>;
+  constexpr int ROWS = C::kRows, PER = 1024 / D;
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  const int64_t row_tiles = (rows + ROWS - 1) / ROWS;
+  const int64_t segments = a.requests * row_tiles * a.kv_heads;
+  const int64_t seg_most = (a.max_kv + 32 * C::S - 1) / (32 * C::S) + 1;
+  // one launch where there is little to split, or enough segments to fill the
+  // chip several times over
+  if (seg_most <= 4 || segments >= (R >= 4 ? 2 : 8) * (int64_t)cus)
+    return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
+  const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
+  const int workers = (int)(need < cus ? need : cus);
+  launch_kernel<D, R, false>(a, dim3(workers), st);
+  const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
+  hipLaunchKernelGGL((attend_join_kernel<D, R>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests),
+                     dim3(256), 0, st, a, workers, groups);
+}
+
+// The fewest rows to a workgroup that hold a request's, so that its keys are
+// read once; beyond 128 rows the largest.
 template <int D>
 void launch_d(const AttendArgs& a, int cus, hipStream_t st) {
-  // two row tiles to a wave halve the reads of the keys; at D = 256 their
-  // sums do not fit the registers
-  if (D == 256 || (int64_t)a.max_new * a.group <= 32)
-    launch<D, 1>(a, cus, st);
-  else
-    launch<D == 256 ? 128 : D, 2>(a, cus, st);
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  if (rows <= 32) return launch<D, 1>(a, cus, st);
+  if constexpr (D == 256) {
+    launch<D, 4>(a, cus, st);
+  } else {
+    if (rows <= 64) return launch<D, 2>(a, cus, st);
+    if (rows <= 128) return launch<D, 4>(a, cus, st);
+    launch<D, 8>(a, cus, st);
+  }
 }
 
 }  // namespace
 
-// workspace: two parts of 64 rows, their outputs and (m, l), for each workgroup
-size_t attend_split_floats(int head_dim, int cus) { return (size_t)2 * cus * 64 * (head_dim + 2); }
+// workspace: two parts of the most rows, their outputs and (m, l), for each
+// workgroup
+size_t attend_split_floats(int head_dim, int cus) {
+  return (size_t)2 * cus * (head_dim == 256 ? 128 : 256) * (head_dim + 2);
+}
 
 void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st) {
   if (head_dim == 64)
