@@ -46,6 +46,10 @@ struct AttendArgs {
   int32_t min_share;
 };
 
+// A value that is the same in every lane, in a scalar register: branches and
+// loads that follow from it stay scalar.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // rows of the token arrays and keys of request b
 struct Request {
   int q0, n, kv;
@@ -93,6 +97,11 @@ __device__ __forceinline__ KeySpan key_span(const Request& r, int t_first, int t
   s.sink_tiles = st < s.first ? st : s.first;
   s.count = s.sink_tiles + (s.hi + KT - 1) / KT - s.first;
   return s;
+}
+
+__device__ __forceinline__ KeySpan uniform(const KeySpan& s) {
+  return KeySpan{uniform(s.pmin),       uniform(s.pmax),  uniform(s.hi),   uniform(s.lo),
+                 uniform(s.sink_tiles), uniform(s.first), uniform(s.count)};
 }
 
 __device__ __forceinline__ int tile_of(const KeySpan& s, int i) {

@@ -27,6 +27,22 @@ __device__ __forceinline__ v16f mfma_32x32(v8s a, v8s b, v16f c) {
                                                  0, 0, 0);
 }
 
+// Copies 16 bytes per lane from base + off into LDS, lane l at dst + 16 l.
+// Written out because the compiler, which knows what the builtin writes, waits
+// for every copy in flight before each transposing read of LDS; no register is
+// written, and wait_copies is what orders the copies.  m0 is free: the compiler
+// sets it right before each use of its own.
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, const lds_byte* dst) {
+  const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)dst);
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(off), "s"(base), "s"(to)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");

@@ -88,10 +88,6 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         if (lane >= d) upto += y;
       }
       total = __builtin_amdgcn_readlane(upto, 63);
-      if (blockIdx.x == 0 && w == 0) {
-        if (lane == 0) a.plan[0] = 0;
-        if (lane < a.requests) a.plan[lane + 1] = upto;
-      }
     } else {
       int* const s_pre = (int*)ring;
       int carry = 0;
@@ -114,14 +110,21 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       }
       if (tid == 0) s_pre[0] = 0;
       __syncthreads();
-      total = __builtin_amdgcn_readfirstlane(carry);
-      if (blockIdx.x == 0)
-        for (int b = tid; b <= a.requests; b += THREADS) a.plan[b] = s_pre[b];
+      total = carry;
     }
+    total = uniform(total);
     const int share = max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     at = blockIdx.x * share;
     end = min(at + share, total);
     if (at >= end) return;
+    if (blockIdx.x == 0) {  // for the join
+      if (few) {
+        if (w == 0 && lane == 0) a.plan[0] = 0;
+        if (w == 0 && lane < a.requests) a.plan[lane + 1] = upto;
+      } else {
+        for (int i = tid; i <= a.requests; i += THREADS) a.plan[i] = ((const int*)ring)[i];
+      }
+    }
 
     // request of the first step (the last one that begins at or before it) and
     // the step its own begin at
@@ -135,10 +138,15 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         else
           hi = mid;
       }
-      begin = __builtin_amdgcn_readfirstlane(s_pre[b]);
-      b = __builtin_amdgcn_readfirstlane(b);
+      begin = s_pre[b];
       __syncthreads();  // the rings are free again
     }
+    // the branches above hide from the compiler that these are the same in
+    // every lane
+    begin = uniform(begin);
+    b = uniform(b);
+    at = uniform(at);
+    end = uniform(end);
   }
 
   lds_byte* const own = (lds_byte*)ring + stream * (RING * T::kBytes);
@@ -163,7 +171,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       if (rt * ROWS >= req.n * a.group) return;
       span = row_tile_span<ROWS>(a, req, rt);
       first = 0;
-      stop = seg = steps_of(span.count, S);
+      stop = seg = uniform(steps_of(span.count, S));
     } else {
       if (few) {
         b = __builtin_ctzll(__ballot(upto > at));
@@ -176,23 +184,27 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         for (;;) {  // requests without rows have no steps
           req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
           const int steps = request_steps<ROWS, S>(a, req);
-          if (at < begin + steps) break;
-          begin += steps;
-          ++b;
+          if (uniform(at < begin + steps)) break;
+          begin = uniform(begin + steps);
+          b = uniform(b + 1);
         }
       }
       int off = at - begin;
       span = row_tile_span<ROWS>(a, req, 0);
       seg = steps_of(span.count, S);
-      while (off >= seg * a.kv_heads) {
+      while (uniform(off >= seg * a.kv_heads)) {
         off -= seg * a.kv_heads;
         span = row_tile_span<ROWS>(a, req, ++rt);
         seg = steps_of(span.count, S);
       }
-      h = off / seg;
-      first = off - h * seg;
+      rt = uniform(rt);
+      seg = uniform(seg);
+      h = uniform(off / seg);
+      first = uniform(off - h * seg);
       stop = min(seg, first + end - at);
     }
+    span = uniform(span);
+    req = Request{uniform(req.q0), uniform(req.n), uniform(req.kv), (bool)uniform(req.bad)};
     bool bad = req.bad;
 
     const_i32* const table = (const_i32*)(a.table + b * a.table_stride);
@@ -217,8 +229,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 #pragma unroll
       for (int j = 0; j < T::kChunkLoads; ++j)
         if (j >= j0 && j < j1)
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + src[j]),
-                                           (__attribute__((address_space(3))) void*)(dst + j * 1024), 16, 0, 0);
+          copy_to_lds(from, src[j], dst + j * 1024);
     };
     // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
@@ -274,11 +285,15 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 #pragma unroll
       for (int kc = 0; kc < D / 16; ++kc) Q[kc] = load_frag_bf16(qp + 16 * kc);
     }
+    // the queries are waited for here, not in the walk, where the wait would
+    // hold up the copies in flight
+#pragma unroll
+    for (int kc = 0; kc < D / 16; ++kc) asm volatile("" : "+v"(Q[kc]));
     // positions of this wave's rows
     KeySpan seen = span;
     if (R > 1) {
-      seen.pmin = req.kv - req.n + min(w0, last) / a.group;
-      seen.pmax = req.kv - req.n + min(w0 + 31, last) / a.group;
+      seen.pmin = uniform(req.kv - req.n + min(w0, last) / a.group);
+      seen.pmax = uniform(req.kv - req.n + min(w0 + 31, last) / a.group);
     }
     RowState<D> st;
     st.clear();
@@ -391,7 +406,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       }
     }
     __syncthreads();
-    at += stop - first;
+    at = uniform(at + stop - first);
   }
 }
 
