@@ -115,7 +115,11 @@ __device__ __forceinline__ float sum_halves(float x) {
 }
 
 // One row tile's state in a wave: 32 rows, lane n = l % 32 holds row n in both
-// halves (m in both, l as each half's part).
+// halves (m in both, l as each half's part).  m is what the exponents are taken
+// against: a score the row has met, at most kSlack (in powers of two) below its
+// largest, so that the sums are rescaled only when a row's maximum has grown by
+// more than that.  Weights stay below 2^kSlack, and neither fp32 sums nor bf16
+// weights lose by a common factor.
 template <int D>
 struct RowState {
   v16f o[D / 32];
@@ -130,24 +134,27 @@ struct RowState {
   }
 };
 
-// Scores of a tile to weights: updates the running maximum and sum, rescales
-// the sums so far where the maximum grew, and leaves the weights in s and,
-// rounded to bf16 for the second product, in p.
+constexpr float kSlack = 8.f;
+
+// Scores of a tile to weights: updates the running sum, first rescaling what
+// there is where the maximum has outgrown m, and leaves the weights, rounded to
+// bf16 for the second product, in p.
 template <int D>
 __device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[2], float scale_log2) {
   float top = fmaxf(s[0], s[1]);
 #pragma unroll
   for (int i = 2; i < 16; ++i) top = fmaxf(top, s[i]);
   top = max_halves(top);
-  const float mn = fmaxf(st.m, top);
-  const float ref = mn == -INFINITY ? 0.f : mn * scale_log2;
-  if (__any(mn > st.m)) {
-    const float alpha = __builtin_amdgcn_exp2f(st.m * scale_log2 - ref);
+  // also true at a row's first visible score, where m is -inf
+  if (__any(top * scale_log2 > st.m * scale_log2 + kSlack)) {
+    const float mn = fmaxf(st.m, top);
+    const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((st.m - mn) * scale_log2);
     st.l *= alpha;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) st.o[i] *= alpha;
     st.m = mn;
   }
+  const float ref = st.m == -INFINITY ? 0.f : st.m * scale_log2;
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -177,11 +184,17 @@ __device__ __forceinline__ void weighted_values(const lds_byte* tile, const uint
     }
 }
 
+// Values that are not finite, in tiles that some rows do not see whole: a
+// product would multiply them by a weight of zero and spoil rows that do not
+// see them.  In such a tile they are noted for the rows that do, and become
+// zeros in LDS before its product.  A note is 2 bits for each row and element, +inf and -inf,
+// both for NaN; the notes of a wave are [32 rows][D / 8] words of 8 elements.
+
 // whether the tile's values hold an infinity or NaN
 template <int D>
 __device__ __forceinline__ bool odd_values(const lds_byte* tile, int lane) {
-  bool odd = false;
-#pragma unroll 4
+  int odd = 0;
+#pragma unroll 1
   for (int i = 0; i < KeyTile<D>::kHalf / 1024; ++i) {
     const v8s v = lds_read16(tile + KeyTile<D>::kHalf + i * 1024 + lane * 16);
 #pragma unroll
@@ -190,48 +203,44 @@ __device__ __forceinline__ bool odd_values(const lds_byte* tile, int lane) {
   return __any(odd);
 }
 
-// The same sum for a tile that holds infinities or NaN and has rows that do not
-// see all its keys: a product would multiply those values by a weight of zero.
-// They count as zero in the sum; a second product counts, for each row and
-// element, the +inf, -inf and NaN among the keys that the row sees (1, 2^10
-// and 2^20 apiece, at most 32 of each: exact), and the row gets what their sum
-// is.
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+
 template <int D>
-__device__ __forceinline__ void careful_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D>& st,
-                                               const v8s (&p)[2], int first_key, int pos, int window, int sinks) {
-  v8s sees[2];
+__device__ __forceinline__ void note_odd_values(const lds_byte* tile, lds_u16* notes, int first_key, int pos,
+                                                int window, int sinks, int lane) {
+  if (lane >= D / 8) return;  // a lane for each piece of a row
+#pragma unroll 1
+  for (int key = 0; key < 32; ++key) {
+    const v8s v = lds_read16(tile + KeyTile<D>::kHalf + key * KeyTile<D>::kRow +
+                             ((lane ^ KeyTile<D>::swizzle(key)) << 4));
+    uint32_t note = 0;
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sees[c][j] = visible(first_key + 16 * c + j, pos, window, sinks) ? 0x3F80 : 0;
-#pragma unroll
-  for (int blk = 0; blk < D / 32; ++blk) {
-    v16f odd;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) odd[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const v4s lo = lds_read_tr(tile + KeyTile<D>::v_step(v0[0], blk, c));
-      const v4s hi = lds_read_tr(tile + KeyTile<D>::v_step(v0[1], blk, c));
-      v8s v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), mark;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool fine = (v[j] & 0x7F80) != 0x7F80;
-        // bf16 of 2^20, 2^10 and 1
-        mark[j] = fine ? 0 : (v[j] & 0x7F) ? 0x4980 : v[j] < 0 ? 0x4480 : 0x3F80;
-        v[j] = fine ? v[j] : (short)0;
-      }
-      st.o[blk] = mfma_32x32(v, p[c], st.o[blk]);
-      odd = mfma_32x32(mark, sees[c], odd);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int k = (int)odd[i];
-      const bool minus = (k >> 10) & 1023, plus = k & 1023;
-      st.o[blk][i] += k >> 20 || (plus && minus) ? NAN : minus ? -INFINITY : plus ? INFINITY : 0.f;
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < 8; ++j)
+      if ((v[j] & 0x7F80) == 0x7F80) note |= ((v[j] & 0x7F) ? 3 : v[j] < 0 ? 2 : 1) << (2 * j);
+    if (!note) continue;
+#pragma unroll 1
+    for (int row = 0; row < 32; ++row)
+      if (visible(first_key + key, __builtin_amdgcn_readlane(pos, row), window, sinks))
+        notes[row * (D / 8) + lane] |= (uint16_t)note;
   }
+}
+
+// zeros in their place, in part `part` of `parts` of the tile
+template <int D>
+__device__ __forceinline__ void clear_odd_values(lds_byte* tile, int part, int parts, int lane) {
+#pragma unroll 1
+  for (int i = part; i < KeyTile<D>::kHalf / 1024; i += parts) {
+    lds_byte* const at = tile + KeyTile<D>::kHalf + i * 1024 + lane * 16;
+    v8s v = lds_read16(at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (v[j] & 0x7F80) == 0x7F80 ? (short)0 : v[j];
+    *(__attribute__((address_space(3))) v8s*)at = v;
+  }
+}
+
+// what a sum becomes by a note's 2 bits
+__device__ __forceinline__ float noted(float x, uint32_t bits) {
+  return bits == 0 ? x : x + (bits == 3 ? NAN : bits == 2 ? -INFINITY : INFINITY);
 }
 
 void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st);

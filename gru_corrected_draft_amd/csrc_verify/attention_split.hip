@@ -68,6 +68,8 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
   __shared__ int s_sum[C::W];
   __shared__ float s_m[C::W][32], s_l[C::W][32];
   __shared__ int s_bad;
+  __shared__ uint16_t s_notes[C::W][32 * (D / 8)];
+  __shared__ int s_noting[C::W];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 31, h2 = lane >> 5;
   const int rg = w / S, stream = w - rg * S;
 
@@ -150,6 +152,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
   }
 
   lds_byte* const own = (lds_byte*)ring + stream * (RING * T::kBytes);
+  lds_u16* const notes = (lds_u16*)s_notes[w];
   const uint32_t k0_off = T::k_first(lane);
   const uint32_t v0_off[2] = {T::v_first(lane, 0), T::v_first(lane, 1)};
   uint32_t src[T::kChunkLoads];
@@ -213,11 +216,27 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     const int tiles = min(stop * S, span.count);
     int next = first * S + stream, ahead = 0, slot_in = 0, slot_out = 0;
 
-    // where the 16 keys from `key` on lie, in elements; keys that no row sees
-    // may have no page and take that of `other`, the tile's other half
-    auto chunk = [&](int key, int other) -> int64_t {
+    // The page of the 16 keys from `key` on; keys that no row sees may have
+    // none and take that of `other`, the tile's other half.  Read for a tile
+    // ahead of its copies.
+    auto page_of = [&](int key, int other) -> int {
       const bool seen = key < span.hi && (key + 15 >= span.lo || key < a.sinks);
-      int page = table[(seen ? key : other) >> a.page_shift];
+      return table[(seen ? key : other) >> a.page_shift];
+    };
+    int page0 = 0, page1 = 0;
+    auto look_up = [&]() {
+      const int key = tile_of(span, next) * 32;
+      if constexpr (R >= 4) {
+        const int c = rg / (R / 4) % 2;
+        page0 = page_of(key + 16 * c, key + 16 - 16 * c);
+      } else {
+        page0 = page_of(key, key + 16);
+        page1 = page_of(key + 16, key);
+      }
+    };
+    if (next < tiles) look_up();
+    // where 16 keys lie, in elements
+    auto chunk = [&](int key, int page) -> int64_t {
       if (page < 0 || page >= a.num_pages) {
         bad = true;
         page = 0;
@@ -233,18 +252,19 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     };
     // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
-      const int key = tile_of(span, next) * 32;
+      const int key = tile_of(span, next) * 32, p0 = page0, p1 = page1;
       next += S;
       ++ahead;
+      if (next < tiles) look_up();
       const lds_byte* dst = own + slot_in * T::kBytes;
       slot_in = slot_in + 1 == RING ? 0 : slot_in + 1;
       if constexpr (R >= 4) {  // 16 rows of K or of V, or half the copies of them
         constexpr int PART = R / 4, LOADS = T::kChunkLoads / PART;
         const int x = rg / (2 * PART), c = rg / PART % 2, j0 = rg % PART * LOADS;
-        copy(x ? a.v : a.k, chunk(key + 16 * c, key + 16 - 16 * c), dst + x * T::kHalf + c * (T::kHalf / 2), j0,
+        copy(x ? a.v : a.k, chunk(key + 16 * c, p0), dst + x * T::kHalf + c * (T::kHalf / 2), j0,
              j0 + LOADS);
       } else {
-        const int64_t c0 = chunk(key, key + 16), c1 = chunk(key + 16, key);
+        const int64_t c0 = chunk(key, p0), c1 = chunk(key + 16, p1);
         if (R == 1 || rg == 0) {
           copy(a.k, c0, dst, 0, T::kChunkLoads);
           copy(a.k, c1, dst + T::kHalf / 2, 0, T::kChunkLoads);
@@ -297,45 +317,66 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     }
     RowState<D> st;
     st.clear();
+    bool noting = false;
+
+    // notes and clears the odd values of a tile that some row does not see whole
+    auto note = [&](const lds_byte* tile, int key) -> bool {
+      if (!odd_values<D>(tile, lane)) return false;
+      if (!noting) {
+        noting = true;
+#pragma unroll 1
+        for (int x = lane; x < 32 * (D / 8); x += 64) notes[x] = 0;
+      }
+      note_odd_values<D>(tile, notes, key, pos, a.window, a.sinks, lane);
+      return true;
+    };
 
 #pragma unroll 1
     for (int i = first * S + stream; i - stream < tiles; i += S) {
+      lds_byte* const tile = own + slot_out * T::kBytes;
+      const int key = tile_of(span, i) * 32;
       if constexpr (R == 1) {
         if (i >= tiles) break;
         if (next < tiles) fetch();
         land();
+        if (!all_visible(span, key, 32, a.window, a.sinks) && note(tile, key)) clear_odd_values<D>(tile, 0, 1, lane);
       } else {
         // every wave's copies of this tile have landed, and every wave is done
         // with the tile before it, whose place the next copies take
         if (i < tiles) land();
         asm volatile("s_barrier" ::: "memory");
         if (next < tiles) fetch();
+        bool edge = false;  // of any stream: all waves come to the barriers
+#pragma unroll
+        for (int x = 0; x < S; ++x) {
+          const int j = i - stream + x;
+          edge |= j < tiles && !all_visible(span, tile_of(span, j) * 32, 32, a.window, a.sinks);
+        }
+        if (uniform(edge)) {
+          const bool odd = i < tiles && note(tile, key);
+          __syncthreads();
+          if (odd) clear_odd_values<D>(tile, rg, R, lane);
+          __syncthreads();
+        }
         if (i >= tiles) continue;
       }
-      const lds_byte* tile = own + slot_out * T::kBytes;
       slot_out = slot_out + 1 == RING ? 0 : slot_out + 1;
-      const int key = tile_of(span, i) * 32;
       if (R > 1 && (key > seen.pmax ||
                     (a.window && key + 31 <= seen.pmin - a.window && key >= a.sinks)))
         continue;  // none of this wave's rows sees it
-      const bool edge = !all_visible(seen, key, 32, a.window, a.sinks);
-      const bool odd = edge && odd_values<D>(tile, lane);
       v16f s;
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] = 0.f;
 #pragma unroll
       for (int kc = 0; kc < D / 16; ++kc) s = mfma_32x32(lds_read16(tile + T::k_step(k0_off, kc)), Q[kc], s);
-      if (edge) {
+      if (!all_visible(seen, key, 32, a.window, a.sinks)) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[j] = -INFINITY;
       }
       v8s p[2];
       softmax_step<D>(s, st, p, a.scale_log2);
-      if (__builtin_expect(odd, 0))
-        careful_values<D>(tile, v0_off, st, p, key + 8 * h2, pos, a.window, a.sinks);
-      else
-        weighted_values<D>(tile, v0_off, st, p);
+      weighted_values<D>(tile, v0_off, st, p);
     }
 
     // join the streams of a row group: each wave writes JOIN rows at a time to
@@ -344,6 +385,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     const int64_t part = 2 * (int64_t)blockIdx.x + (first == 0);
     float* const so = (float*)ring;
     if (tid == 0) s_bad = 0;
+    if (lane == 0) s_noting[w] = noting;
     {
       const float l = sum_halves(st.l);
       if (h2 == 0) {
@@ -389,6 +431,15 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
           o.z += f * y.z;
           o.w += f * y.w;
         }
+#pragma unroll 1
+        for (int x = 0; x < S; ++x)
+          if (s_noting[g * S + x]) {
+            const uint32_t note = s_notes[g * S + x][row * (D / 8) + piece / 2] >> (8 * (piece & 1));
+            o.x = noted(o.x, note & 3);
+            o.y = noted(o.y, note >> 2 & 3);
+            o.z = noted(o.z, note >> 4 & 3);
+            o.w = noted(o.w, note >> 6 & 3);
+          }
         if (whole) {
           const float inv = den == 0.f ? 0.f : 1.f / den;
           const int r = r0 + in_tile, tok = r / a.group, hq = h * a.group + r - tok * a.group;
@@ -409,6 +460,9 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     at = uniform(at + stop - first);
   }
 }
+
+// x f, an infinity kept where f has underflowed
+__device__ __forceinline__ float scaled(float x, float f) { return __builtin_isinf(x) ? x : x * f; }
 
 // Joins the parts of split segments: 256 threads take 1024 / D rows of one
 // (request, row tile, key head).
@@ -439,10 +493,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
     const float fo = __builtin_amdgcn_exp2f((top - ref) * a.scale_log2);
     const float fn = __builtin_amdgcn_exp2f((ml.x - ref) * a.scale_log2);
     den = den * fo + ml.y * fn;
-    o.x = o.x * fo + y.x * fn;
-    o.y = o.y * fo + y.y * fn;
-    o.z = o.z * fo + y.z * fn;
-    o.w = o.w * fo + y.w * fn;
+    o.x = scaled(o.x, fo) + scaled(y.x, fn);
+    o.y = scaled(o.y, fo) + scaled(y.y, fn);
+    o.z = scaled(o.z, fo) + scaled(y.z, fn);
+    o.w = scaled(o.w, fo) + scaled(y.w, fn);
     top = mn;
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
