@@ -170,18 +170,49 @@ __device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[
     p[c] = __builtin_bit_cast(v8s, (u32x4{w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]}));
 }
 
-// O^T += V^T P^T for one tile
+// S^T = K Q^T for one tile.  The fragments are all on their way before the
+// first product: left to itself the compiler reads one at a time and waits.
 template <int D>
-__device__ __forceinline__ void weighted_values(const lds_byte* tile, const uint32_t (&v0)[2], RowState<D>& st,
-                                                const v8s (&p)[2]) {
+__device__ __forceinline__ v16f scores(const lds_byte* tile, uint32_t k0, const v8s (&q)[D / 16]) {
+  constexpr int STEP = D / 16 < 8 ? D / 16 : 8;
+  v16f s;
 #pragma unroll
-  for (int blk = 0; blk < D / 32; ++blk)
+  for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const v4s lo = lds_read_tr(tile + KeyTile<D>::v_step(v0[0], blk, c));
-      const v4s hi = lds_read_tr(tile + KeyTile<D>::v_step(v0[1], blk, c));
-      st.o[blk] = mfma_32x32(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p[c], st.o[blk]);
-    }
+  for (int c0 = 0; c0 < D / 16; c0 += STEP) {
+    v8s k[STEP];
+#pragma unroll
+    for (int c = 0; c < STEP; ++c) k[c] = lds_read16(tile + KeyTile<D>::k_step(k0, c0 + c));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < STEP; ++c) s = mfma_32x32(k[c], q[c0 + c], s);
+  }
+  return s;
+}
+
+// Fragments of V of 64 elements, and O^T += V^T P^T for them
+struct ValueFrags {
+  v4s v[2][2][2];
+};
+template <int D>
+__device__ __forceinline__ ValueFrags read_values(const lds_byte* tile, const uint32_t (&v0)[2], int pair) {
+  ValueFrags f;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) f.v[b][c][e] = lds_read_tr(tile + KeyTile<D>::v_step(v0[e], 2 * pair + b, c));
+  return f;
+}
+template <int D>
+__device__ __forceinline__ void add_values(const ValueFrags& f, int pair, RowState<D>& st, const v8s (&p)[2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      st.o[2 * pair + b] = mfma_32x32(__builtin_shufflevector(f.v[b][c][0], f.v[b][c][1], 0, 1, 2, 3, 4, 5, 6, 7),
+                                      p[c], st.o[2 * pair + b]);
 }
 
 // Values that are not finite, in tiles that some rows do not see whole: a

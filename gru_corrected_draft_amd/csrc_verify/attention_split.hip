@@ -364,11 +364,9 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       if (R > 1 && (key > seen.pmax ||
                     (a.window && key + 31 <= seen.pmin - a.window && key >= a.sinks)))
         continue;  // none of this wave's rows sees it
-      v16f s;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] = 0.f;
-#pragma unroll
-      for (int kc = 0; kc < D / 16; ++kc) s = mfma_32x32(lds_read16(tile + T::k_step(k0_off, kc)), Q[kc], s);
+      v16f s = scores<D>(tile, k0_off, Q);
+      ValueFrags v = read_values<D>(tile, v0_off, 0);
+      __builtin_amdgcn_sched_barrier(0);
       if (!all_visible(seen, key, 32, a.window, a.sinks)) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -376,7 +374,15 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       }
       v8s p[2];
       softmax_step<D>(s, st, p, a.scale_log2);
-      weighted_values<D>(tile, v0_off, st, p);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        // the next fragments are read under these products
+        ValueFrags after;
+        if (x + 1 < D / 64) after = read_values<D>(tile, v0_off, x + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        add_values<D>(v, x, st, p);
+        v = after;
+      }
     }
 
     // join the streams of a row group: each wave writes JOIN rows at a time to
