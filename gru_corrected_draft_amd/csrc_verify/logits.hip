@@ -67,7 +67,7 @@ struct LogitsArgs {
   float* out_logprob;
 };
 
-// What one wave knows of a row: the largest logit, sum of e^((x - m) / T), and
+// What one wave knows of a row: a reference m, the sum of e^((x - m) / T), and
 // the best candidate with its id (kNone: no candidate).
 struct RowPart {
   float m, s, best;
@@ -92,48 +92,63 @@ struct Elem<bf16_t> {
   static constexpr int kVec = 8;
 };
 
-// kVec consecutive logits.  Rows of an odd vocabulary are aligned to the
-// element only; the copy still compiles to one 16-byte load, which the memory
-// path takes at any alignment.
+// kVec consecutive logits as they lie in memory.  Rows of an odd vocabulary are
+// aligned to the element only; the copy still compiles to one 16-byte load,
+// which the memory path takes at any alignment.  Past the n that there are, -inf.
 template <typename T>
-struct Vec {
-  T e[Elem<T>::kVec];
-};
-template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, int n, float* x) {
+__device__ __forceinline__ u32x4 load_raw(const T* p, int n) {
   constexpr int V = Elem<T>::kVec;
+  u32x4 raw;
   if (n >= V) {
-    Vec<T> v;
-    __builtin_memcpy(&v, p, 16);
+    __builtin_memcpy(&raw, p, 16);
+    return raw;
+  }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if constexpr (sizeof(T) == 2)
-        x[j] = bf16_to_f32(v.e[j]);
-      else
-        x[j] = v.e[j];
+  for (int w = 0; w < 4; ++w) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t lo = 2 * w < n ? p[2 * w] : 0xFF80u, hi = 2 * w + 1 < n ? p[2 * w + 1] : 0xFF80u;
+      raw[w] = lo | hi << 16;
+    } else {
+      raw[w] = w < n ? __float_as_uint(p[w]) : 0xFF800000u;
     }
-  } else {
+  }
+  return raw;
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const u32x4& raw, float* x) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      x[j] = -INFINITY;
-      if (j < n) {
-        if constexpr (sizeof(T) == 2)
-          x[j] = bf16_to_f32(p[j]);
-        else
-          x[j] = p[j];
-      }
+  for (int w = 0; w < 4; ++w) {
+    if constexpr (sizeof(T) == 2) {
+      x[2 * w] = __uint_as_float(raw[w] << 16);
+      x[2 * w + 1] = __uint_as_float(raw[w] & 0xFFFF0000u);
+    } else {
+      x[w] = __uint_as_float(raw[w]);
     }
   }
 }
+__device__ __forceinline__ float load_one(const bf16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
 
 __device__ __forceinline__ bf16_t to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+__device__ __forceinline__ void store_one(bf16_t* p, float x) { *p = to_bf16(x); }
+__device__ __forceinline__ void store_one(float* p, float x) { *p = x; }
+
 // the largest fp32 number for +inf, -inf for NaN
 __device__ __forceinline__ float tame(float x) {
   return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);
 }
+
+// -inf where bit j of `out` is set
+__device__ __forceinline__ float masked(float x, uint32_t out, int j) {
+  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)out, j, 1);  // all ones or none
+  return __uint_as_float((m & 0xFF800000u) | (~m & __float_as_uint(x)));
+}
+
+// e^x's power of two; results below 2^-126 become zero
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ float temperature_of(const LogitsArgs& a, int b) {
   const float t = a.temperature ? a.temperature[b] : 0.f;
@@ -162,13 +177,19 @@ __device__ __forceinline__ void build_touched(const LogitsArgs& a, int b, int lo
     const int len = clip_len(a.history_len, b, a.history_width);
     const int prompt = a.prompt_len ? clip_len(a.prompt_len, b, a.history_width) : 0;
     const int32_t* h = a.history + b * a.history_stride;
-    for (int i = tid; i < len; i += kThreads) {
-      const uint32_t off = (uint32_t)h[i] - (uint32_t)lo;
-      if (off < (uint32_t)ids) {
-        if (i < prompt)
-          atomicOr(&t.count[off], kPrompt);
-        else
-          atomicAdd(&t.count[off], 1u);
+    for (int i0 = tid; i0 < len; i0 += 4 * kThreads) {
+      uint32_t id[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) id[u] = i0 + u * kThreads < len ? (uint32_t)h[i0 + u * kThreads] : ~0u;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t off = id[u] - (uint32_t)lo;
+        if (i0 + u * kThreads < len && off < (uint32_t)ids) {
+          if (i0 + u * kThreads < prompt)
+            atomicOr(&t.count[off], kPrompt);
+          else
+            atomicAdd(&t.count[off], 1u);
+        }
       }
     }
   }
@@ -239,7 +260,7 @@ __device__ __forceinline__ float touched_logit(float x, uint32_t c, uint32_t ent
 // Reads logits once; writes them (process) or keeps each row's statistics
 // (verify).  Bound by memory at the larger sizes.
 template <typename T, bool VERIFY, bool TOUCH>
-__global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   constexpr int V = Elem<T>::kVec;
   extern __shared__ uint32_t dyn[];
   __shared__ int s_draft[kMaxRows];
@@ -286,136 +307,206 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
   rules.draft = s_draft;
   rules.n_draft = n_draft;
 
+  // A wave takes one row at a time, or one of `parts` contiguous pieces of it.
   const int slot = w / a.parts, part = w - slot * a.parts;
   const int rows = VERIFY ? n_draft + 1 : a.rows;
   const float c = VERIFY ? 1.44269504088896340736f / (temp > 0.f ? temp : 1.f) : 0.f;
-  const int first = part * 64 + lane, step = a.parts * 64;
-  const int row0 = slot < a.row_slots ? slot : rows;  // waves beyond the slots have no row
-  for (int row = row0; row < rows; row += a.row_slots) {
+  const bool sums = VERIFY && (temp > 0.f || a.out_logprob);
+  if (slot >= a.row_slots) return;
+  const int piece = ((ids + a.parts - 1) / a.parts + 63) / 64 * 64;
+  const int begin = min(part * piece, ids), end = min(begin + piece, ids);
+  // the piece's touched ids
+  int e0 = 0, e1 = t.n;
+  if (TOUCH && a.parts > 1) {
+    for (int hi = t.n; e0 < hi;) {
+      const int mid = (e0 + hi) >> 1;
+      if (t.list[mid] < begin)
+        e0 = mid + 1;
+      else
+        hi = mid;
+    }
+    e1 = e0;
+    for (int hi = t.n; e1 < hi;) {
+      const int mid = (e1 + hi) >> 1;
+      if (t.list[mid] < end)
+        e1 = mid + 1;
+      else
+        hi = mid;
+    }
+  }
+  constexpr int AHEAD = 4;  // loads in flight for a lane
+  for (int row = slot; row < rows; row += a.row_slots) {
     const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
     const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
     T* dst = VERIFY ? nullptr : (T*)a.out + b * a.out_req + row * a.out_row + lo;
     const int proposal = VERIFY && row < n_draft ? s_draft[row] : -1;
     const int own = proposal >= lo && proposal < lo + ids ? proposal - lo : -1;
+    float* const own_logit = VERIFY ? a.drafted + b * a.rows + row : nullptr;
+    // Reference of the exponents: a logit met, at most 16 powers of two below
+    // the largest, so that the sum is seldom rescaled.
     float m = -INFINITY, s = 0.f, best = -INFINITY;
     int where = -1;  // vector of the best candidate
-    for (int i = first * V; i < ids; i += step * V) {
-      float x[V];
-      load_vec<T>(src + i, ids - i, x);
-      uint32_t allow = mask ? mask[i / 32] >> (i % 32) : ~0u;
-      if constexpr (!VERIFY) {
-        // touched ids keep their logit here and are written again below
+    for (int i0 = begin + lane * V; i0 < end; i0 += AHEAD * 64 * V) {
+      u32x4 raw[AHEAD];
+      uint32_t out[AHEAD];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (!((allow >> j) & 1)) x[j] = -INFINITY;
-        if (i + V <= ids) {
-          Vec<T> v;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * 64 * V;
+        if (i < end) {
+          raw[u] = load_raw<T>(src + i, ids - i);
+          out[u] = mask ? ~(mask[i / 32] >> (i % 32)) : 0u;
+        }
+      }
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            if constexpr (sizeof(T) == 2)
-              v.e[j] = to_bf16(x[j]);
-            else
-              v.e[j] = x[j];
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * 64 * V;
+        if (i >= end) break;
+        if constexpr (!VERIFY) {
+          // touched ids keep their logit here and are written again below
+          if (out[u] & ((1u << V) - 1)) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t lo_ = (uint32_t)__builtin_amdgcn_sbfe((int)out[u], 2 * w, 1) & 0xFFFFu;
+                const uint32_t hi_ = (uint32_t)__builtin_amdgcn_sbfe((int)out[u], 2 * w + 1, 1) << 16;
+                const uint32_t m = lo_ | hi_;
+                raw[u][w] = (m & 0xFF80FF80u) | (~m & raw[u][w]);
+              } else {
+                raw[u][w] = __float_as_uint(masked(__uint_as_float(raw[u][w]), out[u], w));
+              }
+            }
           }
-          __builtin_memcpy(dst + i, &v, 16);
+          if (i + V <= ids) {
+            __builtin_memcpy(dst + i, &raw[u], 16);
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+              if (i + j < ids) {
+                if constexpr (sizeof(T) == 2)
+                  dst[i + j] = (bf16_t)(raw[u][j / 2] >> (16 * (j & 1)));
+                else
+                  dst[i + j] = __uint_as_float(raw[u][j]);
+              }
+          }
         } else {
+          uint32_t touched = 0;
+          if (TOUCH) touched = t.bits[i / 32] >> (i % 32);
+          float x[V];
+          unpack<T>(raw[u], x);
 #pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (i + j < ids) {
-              if constexpr (sizeof(T) == 2)
-                dst[i + j] = to_bf16(x[j]);
-              else
-                dst[i + j] = x[j];
+          for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
+          if ((out[u] | touched) & ((1u << V) - 1)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = masked(x[j], out[u] | touched, j);
+          }
+          float top = x[0];
+#pragma unroll
+          for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
+          if (sums) {
+            if ((top - m) * c > 16.f) {  // also the first time, where m is -inf
+              s *= exp2_fast((m - top) * c);
+              m = top;
             }
-        }
-      } else {
-        if (TOUCH) allow &= ~(t.bits[i / 32] >> (i % 32));
-        float top = -INFINITY;
+            if (m > -INFINITY) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[j] = ((allow >> j) & 1) ? tame(x[j]) : -INFINITY;
-          top = fmaxf(top, x[j]);
-        }
-        if (top > -INFINITY) {
-          const float mn = fmaxf(m, top);
-          s *= exp2f((m - mn) * c);
-#pragma unroll
-          for (int j = 0; j < V; ++j) s += exp2f((x[j] - mn) * c);
-          m = mn;
-        }
-        if ((uint32_t)(own - i) < (uint32_t)V) {
-#pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (own - i == j) {
-              // a touched proposal is written from the list below
-              if (!TOUCH || !((t.bits[own / 32] >> (own % 32)) & 1)) a.drafted[b * a.rows + row] = x[j];
-              x[j] = -INFINITY;
+              for (int j = 0; j < V; ++j) s += exp2_fast((x[j] - m) * c);
             }
-        }
-        if (temp > 0.f) {
+          }
+          if ((uint32_t)(own - i) < (uint32_t)V) {
 #pragma unroll
-          for (int j = 0; j < V; ++j)
-            if (x[j] > -INFINITY) x[j] -= noise[i + j];
-        }
-        top = -INFINITY;
+            for (int j = 0; j < V; ++j)
+              if (own - i == j) {
+                // a touched proposal is written from the list below
+                if (!((touched >> j) & 1)) *own_logit = x[j];
+                x[j] = -INFINITY;
+              }
+          }
+          if (temp > 0.f) {
+            // -inf stays -inf, and a NaN is passed over by the maximum
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = fmaxf(top, x[j]);
-        if (top > best) {
-          best = top;
-          where = i;
+            for (int j = 0; j < V; ++j) x[j] -= noise[i + j];
+          }
+          top = fmaxf(x[0], -INFINITY);
+#pragma unroll
+          for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
+          if (top > best) {
+            best = top;
+            where = i;
+          }
         }
       }
     }
+    int id = kNone;
     if constexpr (VERIFY) {
       // exact id of this lane's best candidate: the first of its vector
-      int id = kNone;
       if (where >= 0) {
         float x[V];
-        load_vec<T>(src + where, ids - where, x);
-        uint32_t allow = mask ? mask[where / 32] >> (where % 32) : ~0u;
-        if (TOUCH) allow &= ~(t.bits[where / 32] >> (where % 32));
+        unpack<T>(load_raw<T>(src + where, ids - where), x);
+        uint32_t gone = mask ? ~(mask[where / 32] >> (where % 32)) : 0u;
+        if (TOUCH) gone |= t.bits[where / 32] >> (where % 32);
 #pragma unroll
         for (int j = V - 1; j >= 0; --j) {
           float y = tame(x[j]);
-          if (!((allow >> j) & 1) || where + j == own || y == -INFINITY) continue;
+          if (((gone >> j) & 1) || where + j == own) continue;
           if (temp > 0.f) y -= noise[where + j];
           if (y == best) id = lo + where + j;
         }
       }
-      if (TOUCH) {
-        for (int e = first; e < t.n; e += step) {
-          const int off = t.list[e];
-          if (mask && !((mask[off / 32] >> (off % 32)) & 1)) {
-            if (off == own) a.drafted[b * a.rows + row] = -INFINITY;
-            continue;
+    }
+    if (TOUCH) {
+      // the same wave has written these ids' places above, in order
+      for (int k0 = e0 + lane; k0 < e1; k0 += AHEAD * 64) {
+        int off[AHEAD];
+        float x[AHEAD];
+        bool in[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          in[u] = k0 + u * 64 < e1;
+          if (in[u]) {
+            off[u] = t.list[k0 + u * 64];
+            x[u] = load_one(src + off[u]);
+            if (mask) in[u] = (mask[off[u] / 32] >> (off[u] % 32)) & 1;
+            if (VERIFY && !in[u] && off[u] == own) *own_logit = -INFINITY;
           }
-          float x;
-          if constexpr (sizeof(T) == 2)
-            x = bf16_to_f32(src[off]);
-          else
-            x = src[off];
-          x = tame(touched_logit(x, t.count[off], biases ? t.bias[off] : 0u, lo + off, row, rules));
-          if (off == own) a.drafted[b * a.rows + row] = x;
-          if (x == -INFINITY) continue;
-          const float mn = fmaxf(m, x);
-          s = s * exp2f((m - mn) * c) + exp2f((x - mn) * c);
-          m = mn;
-          if (off == own) continue;
-          if (temp > 0.f) x -= noise[off];
-          if (x > best || (x == best && lo + off < id)) {
-            best = x;
-            id = lo + off;
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          if (!in[u]) continue;
+          float y = touched_logit(x[u], t.count[off[u]], biases ? t.bias[off[u]] : 0u, lo + off[u], row, rules);
+          if constexpr (!VERIFY) {
+            store_one(dst + off[u], y);
+          } else {
+            y = tame(y);
+            if (off[u] == own) *own_logit = y;
+            if (y == -INFINITY) continue;
+            if (sums) {
+              if ((y - m) * c > 16.f) {
+                s *= exp2_fast((m - y) * c);
+                m = y;
+              }
+              s += exp2_fast((y - m) * c);
+            }
+            if (off[u] == own) continue;
+            if (temp > 0.f) y -= noise[off[u]];
+            if (y > best || (y == best && lo + off[u] < id)) {
+              best = y;
+              id = lo + off[u];
+            }
           }
         }
       }
+    }
+    if constexpr (VERIFY) {
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) {
-        const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
+        if (sums) {
+          const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
+          const float mn = fmaxf(m, om);
+          if (mn > -INFINITY) s = s * exp2_fast((m - mn) * c) + os * exp2_fast((om - mn) * c);
+          m = mn;
+        }
         const float ob = __shfl_xor(best, d, 64);
         const int oi = __shfl_xor(id, d, 64);
-        const float mn = fmaxf(m, om);
-        if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + os * exp2f((om - mn) * c);
-        m = mn;
         if (ob > best || (ob == best && oi < id)) {
           best = ob;
           id = oi;
@@ -426,47 +517,25 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a) {
                   (int64_t)blockIdx.x * a.parts + part] = RowPart{m, s, best, id};
     }
   }
-  if constexpr (!VERIFY && TOUCH) {
-    __syncthreads();
-    for (int row = row0; row < rows; row += a.row_slots) {
-      const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
-      const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
-      T* dst = (T*)a.out + b * a.out_req + row * a.out_row + lo;
-      for (int e = first; e < t.n; e += step) {
-        const int off = t.list[e];
-        if (mask && !((mask[off / 32] >> (off % 32)) & 1)) continue;
-        float x;
-        if constexpr (sizeof(T) == 2)
-          x = bf16_to_f32(src[off]);
-        else
-          x = src[off];
-        x = touched_logit(x, t.count[off], biases ? t.bias[off] : 0u, lo + off, row, rules);
-        if constexpr (sizeof(T) == 2)
-          dst[off] = to_bf16(x);
-        else
-          dst[off] = x;
-      }
-    }
-  }
 }
 
 // One workgroup per request joins the parts of its rows, walks the proposals
 // and writes the outputs.
-__global__ __launch_bounds__(256) void accept_kernel(LogitsArgs a, int parts) {
+__global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
   __shared__ float s_lse[kMaxRows], s_m[kMaxRows], s_best[kMaxRows];
   __shared__ int s_id[kMaxRows], s_stands[kMaxRows];
   const int b = blockIdx.x, lane = threadIdx.x & 63, w = wave_index();
   const int n = a.draft ? clip_len(a.draft_len, b, a.rows - 1) : 0;
   const float temp = temperature_of(a, b);
   const float scale = temp > 0.f ? temp : 1.f, c = 1.44269504088896340736f / scale;
-  for (int row = w; row <= n; row += 4) {
+  for (int row = w; row <= n; row += (int)(blockDim.x >> 6)) {
     const RowPart* p = a.partial + ((int64_t)b * a.rows + row) * parts;
     float m = -INFINITY, s = 0.f, best = -INFINITY;
     int id = kNone;
     for (int i = lane; i < parts; i += 64) {
       const RowPart o = p[i];
       const float mn = fmaxf(m, o.m);
-      if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + o.s * exp2f((o.m - mn) * c);
+      if (mn > -INFINITY) s = s * exp2_fast((m - mn) * c) + o.s * exp2_fast((o.m - mn) * c);
       m = mn;
       if (o.best > best || (o.best == best && o.id < id)) {
         best = o.best;
@@ -479,7 +548,7 @@ __global__ __launch_bounds__(256) void accept_kernel(LogitsArgs a, int parts) {
       const float ob = __shfl_xor(best, d, 64);
       const int oi = __shfl_xor(id, d, 64);
       const float mn = fmaxf(m, om);
-      if (mn > -INFINITY) s = s * exp2f((m - mn) * c) + os * exp2f((om - mn) * c);
+      if (mn > -INFINITY) s = s * exp2_fast((m - mn) * c) + os * exp2_fast((om - mn) * c);
       m = mn;
       if (ob > best || (ob == best && oi < id)) {
         best = ob;
@@ -573,7 +642,7 @@ static int longest_range(size_t per_id) {
 // the cuts that fill one to four rounds more than the longest ranges need,
 // the one with the least rounds x (range + 512) is taken.  requests * ranges
 // is at most requests * (ranges of the longest) + 4 rounds.
-static Cut cut_vocab(int vocab, int cus, int requests, int rows, size_t per_id, bool touch) {
+static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t per_id, bool touch) {
   Cut k;
   const int most = longest_range(per_id), slots = 2 * cus;
   const int least = (vocab + most - 1) / most;
@@ -595,7 +664,9 @@ static Cut cut_vocab(int vocab, int cus, int requests, int rows, size_t per_id, 
   }
   k.ranges = (vocab + k.range - 1) / k.range;
   k.row_slots = rows < kWaves ? rows : kWaves;
-  k.parts = kWaves / k.row_slots;
+  // waves to a row, each with at least one vector for most of its lanes
+  const int pieces = (k.range + 64 * vec - 1) / (64 * vec);
+  k.parts = kWaves / k.row_slots < pieces ? kWaves / k.row_slots : pieces;
   k.lds = per_id * k.range + (touch ? k.range / 8 : 0) + 64;
   return k;
 }
@@ -709,7 +780,7 @@ template <bool VERIFY>
 static void launch_logits(const domino_verify_t* h, LogitsArgs& a, Cut& k, hipStream_t st) {
   const bool penalties = a.repetition || a.frequency || a.presence;
   const bool touch = penalties || a.bias_ids;
-  k = cut_vocab(h->cfg.vocab, h->cus, a.requests, a.rows,
+  k = cut_vocab(h->cfg.vocab, h->cus, a.requests, a.rows, h->cfg.dtype == DOMINO_DTYPE_BF16 ? 8 : 4,
                 lds_per_id(VERIFY && a.noise, touch, a.bias_ids != nullptr), touch);
   a.range = k.range;
   a.row_slots = k.row_slots;
@@ -790,6 +861,6 @@ extern "C" domino_status_t domino_verify_run(domino_verify_t* h, const domino_lo
   (void)hipGetLastError();
   Cut k;
   launch_logits<true>(h, a, k, (hipStream_t)stream);
-  hipLaunchKernelGGL(accept_kernel, dim3(a.requests), dim3(256), 0, (hipStream_t)stream, a, k.ranges * k.parts);
+  hipLaunchKernelGGL(accept_kernel, dim3(a.requests), dim3(a.rows < 16 ? 64 * a.rows : 1024), 0, (hipStream_t)stream, a, k.ranges * k.parts);
   return launched(h, "run");
 }
