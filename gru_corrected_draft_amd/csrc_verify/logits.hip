@@ -5,13 +5,17 @@
 // request for all of the request's rows, so that what the rows share (the
 // history's counts, the biases, the noise) is put into LDS once.
 //
-// Few ids of a range are touched by a penalty or a bias.  A bitmap tells which,
-// and a lane takes the touched ones of its vector one by one, so that the
-// division of the repetition penalty and the look-ups are paid for them alone,
-// while the logits are in registers (going back for them from a list wrote
-// their lines to memory twice: 64 blocks of 151936 ids with 4096 tokens of
-// history took 212 us against 127 us without one).  Counting uses integer
-// atomics in LDS, so nothing depends on the order of arrival.
+// Few ids of a range are touched by a penalty or a bias, and the division of the
+// repetition penalty and the look-ups are paid for them alone.  A bitmap tells
+// which they are.  Where logits are written (bound by memory), a lane takes the
+// touched ones of its vector one by one while they are in registers: going back
+// for them wrote their lines twice, and 64 blocks of 151936 ids with 4096 tokens
+// of history took 212 us against 137.  Where they are not (bound by arithmetic),
+// the pass leaves touched ids out and each row takes them afterwards from a list,
+// a lane to each: taken in the pass, for a lane or two of a wave at a time, they
+// made 64 greedy blocks with that history take 188 us against 137.  Counting uses
+// integer atomics in LDS and the list is in the order of the ids, so nothing
+// depends on the order of arrival.
 #include <cmath>
 #include <new>
 
@@ -127,6 +131,9 @@ __device__ __forceinline__ void unpack(const u32x4& raw, float* x) {
     }
   }
 }
+__device__ __forceinline__ float load_one(const bf16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
+
 // element j of a vector that stays in registers
 template <typename T>
 __device__ __forceinline__ float element(const u32x4& raw, int j) {
@@ -154,6 +161,7 @@ __device__ __forceinline__ void replace(u32x4& raw, int j, float x) {
   for (int w = 0; w < 4; ++w) raw[w] = word == w ? (raw[w] & keep) | put : raw[w];
 }
 
+
 // the largest fp32 number for +inf, -inf for NaN
 __device__ __forceinline__ float tame(float x) {
   return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);
@@ -173,16 +181,19 @@ __device__ __forceinline__ float temperature_of(const LogitsArgs& a, int b) {
   return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;
 }
 
-// LDS of a workgroup: counts, last bias entry and bitmap of touched ids
+// LDS of a workgroup: counts, last bias entry, list and bitmap of touched ids
 struct Touched {
   uint32_t* count;   // [range]
   uint32_t* bias;    // [range] entry + 1
   uint32_t* bits;    // [range / 32]
+  uint16_t* list;    // [range] offsets, ascending
+  int n;
 };
 
+template <bool LIST>
 __device__ __forceinline__ void build_touched(const LogitsArgs& a, int b, int lo, int ids,
                                               bool counts, bool biases, int n_draft,
-                                              const int* s_draft, Touched& t) {
+                                              const int* s_draft, int* s_wave, Touched& t) {
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index();
   for (int i = tid; i < a.range; i += kThreads) {
     t.count[i] = 0;
@@ -222,11 +233,35 @@ __device__ __forceinline__ void build_touched(const LogitsArgs& a, int b, int lo
     }
   }
   __syncthreads();
-  for (int g = w; g < a.range / 64; g += kWaves) {
+  // each wave compacts a run of 64-id groups; the runs follow one another
+  const int groups = a.range / 64, per = (groups + kWaves - 1) / kWaves;
+  const int g0 = w * per, g1 = min(g0 + per, groups);
+  int total = 0;
+  for (int g = g0; g < g1; ++g) {
     const int i = g * 64 + lane;
     const uint64_t hit = __ballot(t.count[i] != 0 || (biases && t.bias[i] != 0));
     if (lane < 2) t.bits[2 * g + lane] = (uint32_t)(hit >> (32 * lane));
+    total += __popcll(hit);
   }
+  if (!LIST) {
+    __syncthreads();
+    return;
+  }
+  if (lane == 0) s_wave[w] = total;
+  __syncthreads();
+  int at = 0, all = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < w) at += s_wave[i];
+    all += s_wave[i];
+  }
+  for (int g = g0; g < g1; ++g) {
+    const int i = g * 64 + lane;
+    const bool hit = t.count[i] != 0 || (biases && t.bias[i] != 0);
+    const uint64_t m = __ballot(hit);
+    if (hit) t.list[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)i;
+    at += __popcll(m);
+  }
+  t.n = all;
   __syncthreads();
 }
 
@@ -260,6 +295,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   constexpr int V = Elem<T>::kVec;
   extern __shared__ uint32_t dyn[];
   __shared__ int s_draft[kMaxRows];
+  __shared__ int s_wave[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index();
   const int b = blockIdx.y, lo = blockIdx.x * a.range;
   const int ids = min(a.range, a.vocab - lo);
@@ -282,13 +318,16 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
     t.bias = at;
     if (biases) at += a.range;
     t.bits = at;
+    at += a.range / 32;
+    t.list = (uint16_t*)at;
   }
+  t.n = 0;
   if (VERIFY && temp > 0.f) {
     const float* e = a.noise + b * a.noise_stride + lo;
     for (int i = tid; i < ids; i += kThreads) noise[i] = temp * logf(e[i]);
   }
   __syncthreads();
-  if (TOUCH) build_touched(a, b, lo, ids, counts, biases, n_draft, s_draft, t);
+  if (TOUCH) build_touched<VERIFY>(a, b, lo, ids, counts, biases, n_draft, s_draft, s_wave, t);
 
   Rules rules;
   rules.has_repetition = a.repetition != nullptr;
@@ -307,6 +346,25 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   if (slot >= a.row_slots) return;
   const int piece = ((ids + a.parts - 1) / a.parts + 63) / 64 * 64;
   const int begin = min(part * piece, ids), end = min(begin + piece, ids);
+  // the piece's touched ids
+  int e0 = 0, e1 = t.n;
+  if (VERIFY && TOUCH && a.parts > 1) {
+    for (int hi = t.n; e0 < hi;) {
+      const int mid = (e0 + hi) >> 1;
+      if (t.list[mid] < begin)
+        e0 = mid + 1;
+      else
+        hi = mid;
+    }
+    e1 = e0;
+    for (int hi = t.n; e1 < hi;) {
+      const int mid = (e1 + hi) >> 1;
+      if (t.list[mid] < end)
+        e1 = mid + 1;
+      else
+        hi = mid;
+    }
+  }
   constexpr int AHEAD = 4;  // loads in flight for a lane
   for (int row = slot; row < rows; row += a.row_slots) {
     const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
@@ -319,8 +377,6 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
     // the largest, so that the sum is seldom rescaled.
     float m = -INFINITY, s = 0.f, best = -INFINITY;
     int where = -1;  // vector of the best candidate
-    float touched_best = -INFINITY;
-    int touched_id = kNone;
     for (int i0 = begin + lane * V; i0 < end; i0 += AHEAD * 64 * V) {
       u32x4 raw[AHEAD];
       uint32_t out[AHEAD];
@@ -372,39 +428,15 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
               }
           }
         } else {
-          uint32_t gone = out[u], hit0 = 0;
-          if (TOUCH) {
-            const uint32_t touched = t.bits[i / 32] >> (i % 32);
-            hit0 = touched & ~out[u] & ((1u << V) - 1);
-            gone |= touched;
-            for (uint32_t hit = hit0; hit; hit &= hit - 1) {
-              const int j = __builtin_ctz(hit), off = i + j;
-              float y = tame(touched_logit(element<T>(raw[u], j), t.count[off], biases ? t.bias[off] : 0u,
-                                           lo + off, row, rules));
-              if (off == own) *own_logit = y;
-              if (y == -INFINITY) continue;
-              if (sums) {
-                if ((y - m) * c > 16.f) {
-                  s *= exp2_fast((m - y) * c);
-                  m = y;
-                }
-                s += exp2_fast((y - m) * c);
-              }
-              if (off == own) continue;
-              if (temp > 0.f) y -= noise[off];
-              if (y > touched_best) {  // offsets ascend: the first of equals stays
-                touched_best = y;
-                touched_id = lo + off;
-              }
-            }
-          }
+          uint32_t touched = 0;
+          if (TOUCH) touched = t.bits[i / 32] >> (i % 32);
           float x[V];
           unpack<T>(raw[u], x);
 #pragma unroll
           for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
-          if (gone & ((1u << V) - 1)) {
+          if ((out[u] | touched) & ((1u << V) - 1)) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = masked(x[j], gone, j);
+            for (int j = 0; j < V; ++j) x[j] = masked(x[j], out[u] | touched, j);
           }
           float top = x[0];
 #pragma unroll
@@ -423,7 +455,8 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
               if (own - i == j) {
-                if (!((hit0 >> j) & 1)) *own_logit = x[j];
+                // a touched proposal is written from the list below
+                if (!((touched >> j) & 1)) *own_logit = x[j];
                 x[j] = -INFINITY;
               }
           }
@@ -458,9 +491,43 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           if (y == best) id = lo + where + j;
         }
       }
-      if (TOUCH && (touched_best > best || (touched_best == best && touched_id < id))) {
-        best = touched_best;
-        id = touched_id;
+    }
+    if (VERIFY && TOUCH) {
+      for (int k0 = e0 + lane; k0 < e1; k0 += AHEAD * 64) {
+        int off[AHEAD];
+        float x[AHEAD];
+        bool in[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          in[u] = k0 + u * 64 < e1;
+          if (in[u]) {
+            off[u] = t.list[k0 + u * 64];
+            x[u] = load_one(src + off[u]);
+            if (mask) in[u] = (mask[off[u] / 32] >> (off[u] % 32)) & 1;
+            if (!in[u] && off[u] == own) *own_logit = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          if (!in[u]) continue;
+          float y = touched_logit(x[u], t.count[off[u]], biases ? t.bias[off[u]] : 0u, lo + off[u], row, rules);
+          y = tame(y);
+          if (off[u] == own) *own_logit = y;
+          if (y == -INFINITY) continue;
+          if (sums) {
+            if ((y - m) * c > 16.f) {
+              s *= exp2_fast((m - y) * c);
+              m = y;
+            }
+            s += exp2_fast((y - m) * c);
+          }
+          if (off[u] == own) continue;
+          if (temp > 0.f) y -= noise[off[u]];
+          if (y > best || (y == best && lo + off[u] < id)) {
+            best = y;
+            id = lo + off[u];
+          }
+        }
       }
     }
     if constexpr (VERIFY) {
@@ -593,8 +660,8 @@ struct Cut {
   size_t lds;
 };
 
-static size_t lds_per_id(bool noise, bool touch, bool biases) {
-  return (noise ? 4 : 0) + (touch ? 4 : 0) + (biases ? 4 : 0);
+static size_t lds_per_id(bool noise, bool touch, bool list, bool biases) {
+  return (noise ? 4 : 0) + (touch ? 4 : 0) + (list ? 2 : 0) + (biases ? 4 : 0);
 }
 
 // longest range: what LDS for two workgroups to a CU holds (its bitmap is
@@ -664,7 +731,7 @@ extern "C" domino_status_t domino_verify_create(const domino_verify_config_t* cf
     h->cus = 256;
   }
   // bound of cut_vocab's requests * ranges, times the waves of a row
-  const int shortest = longest_range(lds_per_id(true, true, true));
+  const int shortest = longest_range(lds_per_id(true, true, true, true));
   const size_t words = ((size_t)cfg->max_requests * ((cfg->vocab + shortest - 1) / shortest) + 8 * h->cus) *
                        (cfg->max_rows > kWaves ? cfg->max_rows : kWaves);
   h->partial = (RowPart*)h->take(words * sizeof(RowPart));
@@ -748,7 +815,7 @@ static void launch_logits(const domino_verify_t* h, LogitsArgs& a, Cut& k, hipSt
   const bool penalties = a.repetition || a.frequency || a.presence;
   const bool touch = penalties || a.bias_ids;
   k = cut_vocab(h->cfg.vocab, h->cus, a.requests, a.rows, h->cfg.dtype == DOMINO_DTYPE_BF16 ? 8 : 4,
-                lds_per_id(VERIFY && a.noise, touch, a.bias_ids != nullptr), touch);
+                lds_per_id(VERIFY && a.noise, touch, VERIFY && touch, a.bias_ids != nullptr), touch);
   a.range = k.range;
   a.row_slots = k.row_slots;
   a.parts = k.parts;
