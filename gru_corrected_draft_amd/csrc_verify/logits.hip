@@ -181,6 +181,68 @@ __device__ __forceinline__ float temperature_of(const LogitsArgs& a, int b) {
   return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;
 }
 
+// whether a vector holds an infinity or NaN: an exponent of all ones carries
+// into the bit above it
+template <typename T>
+__device__ __forceinline__ bool odd(const u32x4& raw) {
+  constexpr uint32_t kExp = sizeof(T) == 2 ? 0x7F807F80u : 0x7F800000u;
+  constexpr uint32_t kOne = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
+  uint32_t carry = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) carry |= (raw[w] & kExp) + kOne;
+  return carry & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u);
+}
+
+// The largest of n; a NaN is passed over.  Written out because fmaxf first
+// makes each operand canonical, one more instruction apiece.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N]) {
+  float top = max3(x[0], x[1], x[2]);
+#pragma unroll
+  for (int j = 3; j + 1 < N; j += 2) top = max3(top, x[j], x[j + 1]);
+  return max3(top, x[N - 1], x[N - 1]);
+}
+
+// Lane exchange for reductions over a wave: neighbours, pairs, halves of eight
+// and sixteen by data-parallel moves, then halves of 32 and 64 by swaps.
+template <int STEP>
+__device__ __forceinline__ uint32_t other(uint32_t x) {
+  if constexpr (STEP == 0) return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false);   // quad_perm 1 0 3 2
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false);   // quad_perm 2 3 0 1
+  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false);  // row_half_mirror
+  if constexpr (STEP == 3) return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false);  // row_mirror
+  return x;
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, F f) {
+  x = f(x, other<0>(x));
+  x = f(x, other<1>(x));
+  x = f(x, other<2>(x));
+  x = f(x, other<3>(x));
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = f(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return f(b[0], b[1]);
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return __uint_as_float(wave_reduce(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  return __uint_as_float(wave_reduce(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+__device__ __forceinline__ int wave_min(int x) {
+  return (int)wave_reduce((uint32_t)x, [](uint32_t a, uint32_t b) { return (uint32_t)min((int)a, (int)b); });
+}
+
 // LDS of a workgroup: counts, last bias entry, list and bitmap of touched ids
 struct Touched {
   uint32_t* count;   // [range]
@@ -380,12 +442,23 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
     for (int i0 = begin + lane * V; i0 < end; i0 += AHEAD * 64 * V) {
       u32x4 raw[AHEAD];
       uint32_t out[AHEAD];
+      // the wave's last vector of this turn is whole: no lane needs a check
+      if (i0 - lane * V + AHEAD * 64 * V <= min(end, ids)) {
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int i = i0 + u * 64 * V;
-        if (i < end) {
-          raw[u] = load_raw<T>(src + i, ids - i);
+        for (int u = 0; u < AHEAD; ++u) __builtin_memcpy(&raw[u], src + i0 + u * 64 * V, 16);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int i = i0 + u * 64 * V;
           out[u] = mask ? ~(mask[i / 32] >> (i % 32)) : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int i = i0 + u * 64 * V;
+          if (i < end) {
+            raw[u] = load_raw<T>(src + i, ids - i);
+            out[u] = mask ? ~(mask[i / 32] >> (i % 32)) : 0u;
+          }
         }
       }
 #pragma unroll
@@ -432,23 +505,29 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           if (TOUCH) touched = t.bits[i / 32] >> (i % 32);
           float x[V];
           unpack<T>(raw[u], x);
+          if (odd<T>(raw[u])) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
+            for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
+          }
           if ((out[u] | touched) & ((1u << V) - 1)) {
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = masked(x[j], out[u] | touched, j);
           }
-          float top = x[0];
-#pragma unroll
-          for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
           if (sums) {
+            const float top = largest<V>(x);
             if ((top - m) * c > 16.f) {  // also the first time, where m is -inf
               s *= exp2_fast((m - top) * c);
               m = top;
             }
             if (m > -INFINITY) {
+              float e[V];
 #pragma unroll
-              for (int j = 0; j < V; ++j) s += exp2_fast((x[j] - m) * c);
+              for (int j = 0; j < V; ++j) e[j] = exp2_fast((x[j] - m) * c);
+#pragma unroll
+              for (int n = V / 2; n; n /= 2)
+#pragma unroll
+                for (int j = 0; j < n; ++j) e[j] += e[j + n];
+              s += e[0];
             }
           }
           if ((uint32_t)(own - i) < (uint32_t)V) {
@@ -463,11 +542,15 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           if (temp > 0.f) {
             // -inf stays -inf, and a NaN is passed over by the maximum
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[j] -= noise[i + j];
+            for (int j = 0; j < V; j += 4) {
+              const float4 g = *reinterpret_cast<const float4*>(noise + i + j);
+              x[j] -= g.x;
+              x[j + 1] -= g.y;
+              x[j + 2] -= g.z;
+              x[j + 3] -= g.w;
+            }
           }
-          top = fmaxf(x[0], -INFINITY);
-#pragma unroll
-          for (int j = 1; j < V; ++j) top = fmaxf(top, x[j]);
+          const float top = largest<V>(x);
           if (top > best) {
             best = top;
             where = i;
@@ -531,21 +614,14 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
       }
     }
     if constexpr (VERIFY) {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) {
-        if (sums) {
-          const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
-          const float mn = fmaxf(m, om);
-          if (mn > -INFINITY) s = s * exp2_fast((m - mn) * c) + os * exp2_fast((om - mn) * c);
-          m = mn;
-        }
-        const float ob = __shfl_xor(best, d, 64);
-        const int oi = __shfl_xor(id, d, 64);
-        if (ob > best || (ob == best && oi < id)) {
-          best = ob;
-          id = oi;
-        }
+      if (sums) {
+        const float all = wave_max(m);
+        if (all > -INFINITY) s = wave_sum(s * exp2_fast((m - all) * c));
+        m = all;
       }
+      const float most = wave_max(best);
+      id = wave_min(best == most ? id : kNone);
+      best = most;
       if (lane == 0)
         a.partial[((int64_t)b * a.rows + row) * ((int64_t)gridDim.x * a.parts) +
                   (int64_t)blockIdx.x * a.parts + part] = RowPart{m, s, best, id};
@@ -576,19 +652,12 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
         id = o.id;
       }
     }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const float om = __shfl_xor(m, d, 64), os = __shfl_xor(s, d, 64);
-      const float ob = __shfl_xor(best, d, 64);
-      const int oi = __shfl_xor(id, d, 64);
-      const float mn = fmaxf(m, om);
-      if (mn > -INFINITY) s = s * exp2_fast((m - mn) * c) + os * exp2_fast((om - mn) * c);
-      m = mn;
-      if (ob > best || (ob == best && oi < id)) {
-        best = ob;
-        id = oi;
-      }
-    }
+    const float all = wave_max(m);
+    if (all > -INFINITY) s = wave_sum(s * exp2_fast((m - all) * c));
+    m = all;
+    const float most = wave_max(best);
+    id = wave_min(best == most ? id : kNone);
+    best = most;
     if (lane == 0) {
       int stands = 0;
       float lp = -INFINITY;
