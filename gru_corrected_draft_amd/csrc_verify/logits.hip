@@ -181,20 +181,9 @@ __device__ __forceinline__ float temperature_of(const LogitsArgs& a, int b) {
   return t > 0.f ? fminf(fmaxf(t, 1e-30f), 1e30f) : 0.f;
 }
 
-// whether a vector holds an infinity or NaN: an exponent of all ones carries
-// into the bit above it
-template <typename T>
-__device__ __forceinline__ bool odd(const u32x4& raw) {
-  constexpr uint32_t kExp = sizeof(T) == 2 ? 0x7F807F80u : 0x7F800000u;
-  constexpr uint32_t kOne = sizeof(T) == 2 ? 0x00800080u : 0x00800000u;
-  uint32_t carry = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) carry |= (raw[w] & kExp) + kOne;
-  return carry & (sizeof(T) == 2 ? 0x80008000u : 0x80000000u);
-}
-
-// The largest of n; a NaN is passed over.  Written out because fmaxf first
-// makes each operand canonical, one more instruction apiece.
+// The largest of n; a quiet NaN is passed over, a signaling one takes its two
+// neighbours with it.  Written out because fmaxf first makes each operand
+// canonical, one more instruction apiece.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -206,6 +195,21 @@ __device__ __forceinline__ float largest(const float (&x)[N]) {
 #pragma unroll
   for (int j = 3; j + 1 < N; j += 2) top = max3(top, x[j], x[j + 1]);
   return max3(top, x[N - 1], x[N - 1]);
+}
+
+// Sum of the exponentials 2^((x - m) c).  From the difference: m c taken out of
+// a fused product would be one instruction less apiece, but its rounding leaves
+// the only candidate of a row a log-probability of not quite 0.
+template <int N>
+__device__ __forceinline__ float sum_exp(const float (&x)[N], float m, float c) {
+  float e[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = exp2_fast((x[j] - m) * c);
+#pragma unroll
+  for (int n = N / 2; n; n /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) e[j] += e[j + n];
+  return e[0];
 }
 
 // Lane exchange for reductions over a wave: neighbours, pairs, halves of eight
@@ -505,30 +509,25 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           if (TOUCH) touched = t.bits[i / 32] >> (i % 32);
           float x[V];
           unpack<T>(raw[u], x);
-          if (odd<T>(raw[u])) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
-          }
           if ((out[u] | touched) & ((1u << V) - 1)) {
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = masked(x[j], out[u] | touched, j);
           }
+          bool nan = false;
+#pragma unroll
+          for (int j = 0; j < V; j += 2) nan |= __builtin_isunordered(x[j], x[j + 1]);
+          float top = largest<V>(x);
+          if (nan || top == INFINITY) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = tame(x[j]);
+            top = largest<V>(x);
+          }
           if (sums) {
-            const float top = largest<V>(x);
             if ((top - m) * c > 16.f) {  // also the first time, where m is -inf
               s *= exp2_fast((m - top) * c);
               m = top;
             }
-            if (m > -INFINITY) {
-              float e[V];
-#pragma unroll
-              for (int j = 0; j < V; ++j) e[j] = exp2_fast((x[j] - m) * c);
-#pragma unroll
-              for (int n = V / 2; n; n /= 2)
-#pragma unroll
-                for (int j = 0; j < n; ++j) e[j] += e[j + n];
-              s += e[0];
-            }
+            if (m > -INFINITY) s += sum_exp<V>(x, m, c);
           }
           if ((uint32_t)(own - i) < (uint32_t)V) {
 #pragma unroll
@@ -538,6 +537,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
                 if (!((touched >> j) & 1)) *own_logit = x[j];
                 x[j] = -INFINITY;
               }
+            top = largest<V>(x);
           }
           if (temp > 0.f) {
             // -inf stays -inf, and a NaN is passed over by the maximum
@@ -549,8 +549,8 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
               x[j + 2] -= g.z;
               x[j + 3] -= g.w;
             }
+            top = largest<V>(x);
           }
-          const float top = largest<V>(x);
           if (top > best) {
             best = top;
             where = i;

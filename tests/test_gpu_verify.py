@@ -283,6 +283,28 @@ def test_verify_empty_rows_and_odd_values():
         assert abs(logprob[6, 0] + np.log(vocab)) < 1e-5
 
 
+@pytest.mark.parametrize("temp", [0.0, 0.7])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_verify_passes_over_every_nan(dtype, temp):
+    """NaN of both kinds and signs in every place of a row, next to the largest logit and away from it."""
+    import torch
+    log(f"[gpu-test] verify NaN {dtype} {temp}")
+    vocab = 2050
+    logits, rules, more = make(4, 3, vocab, dtype, 77, temperature=temp, agree=1.0)
+    kinds = (0x7FC0, 0x7F81, 0xFFC0, 0xFF81) if dtype == "bf16" else (0x7FC00000, 0x7F800001, 0xFFC00000, 0xFF800001)
+    raw = logits.view(torch.int16 if dtype == "bf16" else torch.int32).numpy()
+    rng = np.random.default_rng(78)
+    for b in range(4):
+        for t in range(3):
+            at = rng.permutation(vocab)[:600]
+            top = int(np.nanargmax(logits[b, t].float().numpy()))
+            at = np.concatenate([at, [top - 1, top + 1] if 0 < top < vocab - 1 else []]).astype(int)
+            at = at[at != top]
+            raw[b, t, at] = np.array(kinds, np.uint16 if dtype == "bf16" else np.uint32)[at % 4].view(raw.dtype)
+    got = op(vocab, dtype).run(logits.cuda(), return_logprob=True, **dev(rules), **dev(more))
+    check_verify(got, logits, rules, more, vocab)
+
+
 def test_sampling_follows_the_distribution():
     """With one proposal and fresh noise, the first token's frequencies are the target's: 60000 draws over
     five ids, each within five standard deviations."""
