@@ -363,7 +363,9 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   __shared__ int s_draft[kMaxRows];
   __shared__ int s_wave[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index();
-  const int b = blockIdx.y, lo = blockIdx.x * a.range;
+  // requests vary fastest: low ids are the frequent ones in most vocabularies,
+  // so the ranges with the most touched ids start first
+  const int b = blockIdx.x, lo = blockIdx.y * a.range;
   const int ids = min(a.range, a.vocab - lo);
   const bool counts = TOUCH && (a.repetition || a.frequency || a.presence);
   const bool biases = TOUCH && a.bias_ids;
@@ -623,8 +625,8 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
       id = wave_min(best == most ? id : kNone);
       best = most;
       if (lane == 0)
-        a.partial[((int64_t)b * a.rows + row) * ((int64_t)gridDim.x * a.parts) +
-                  (int64_t)blockIdx.x * a.parts + part] = RowPart{m, s, best, id};
+        a.partial[((int64_t)b * a.rows + row) * ((int64_t)gridDim.y * a.parts) +
+                  (int64_t)blockIdx.y * a.parts + part] = RowPart{m, s, best, id};
     }
   }
 }
@@ -888,7 +890,7 @@ static void launch_logits(const domino_verify_t* h, LogitsArgs& a, Cut& k, hipSt
   a.range = k.range;
   a.row_slots = k.row_slots;
   a.parts = k.parts;
-  const dim3 grid(k.ranges, a.requests), block(kThreads);
+  const dim3 grid(a.requests, k.ranges), block(kThreads);
   if (h->cfg.dtype == DOMINO_DTYPE_BF16) {
     if (touch)
       hipLaunchKernelGGL((logits_kernel<bf16_t, VERIFY, true>), grid, block, k.lds, st, a);
