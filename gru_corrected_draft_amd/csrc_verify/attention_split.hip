@@ -29,12 +29,12 @@ namespace {
 
 template <int D, int R>
 struct Shape {
-  static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : 8 / R);  // streams
+  static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : R == 2 ? 2 : 8 / R);  // streams
   static constexpr int W = R * S;                                                // waves
   static constexpr int kThreads = 64 * W;
   static constexpr int kRows = 32 * R;
   // tiles of a stream in LDS: 128 KB in all at D = 128 and 256 up to R = 4
-  static constexpr int kRing = D == 64 ? 4 : (R <= 2 ? 2 : 4);
+  static constexpr int kRing = D == 64 ? 4 : (R == 1 ? 2 : 4);
   static constexpr int kLds = S * kRing * KeyTile<D>::kBytes;
   static constexpr int kJoin = kLds / (W * D * 4) < 32 ? kLds / (W * D * 4) : 32;  // rows joined at a time
   static constexpr int kLoads = KeyTile<D>::kLoads / R;  // copies of a tile by one wave

@@ -724,7 +724,7 @@ struct domino_verify : HandleBase {
 static thread_local char t_err[256] = "";
 
 constexpr int kMinRange = 512;
-constexpr size_t kLdsBytes = 78 * 1024;  // two workgroups to a CU
+constexpr size_t kLdsBytes = 79 * 1024;  // two workgroups to a CU, beside their static LDS
 
 struct Cut {
   int range, ranges, row_slots, parts;
@@ -735,24 +735,29 @@ static size_t lds_per_id(bool noise, bool touch, bool list, bool biases) {
   return (noise ? 4 : 0) + (touch ? 4 : 0) + (list ? 2 : 0) + (biases ? 4 : 0);
 }
 
-// longest range: what LDS for two workgroups to a CU holds (its bitmap is
-// counted as a byte per id, an overestimate)
+// longest range: what LDS for two workgroups to a CU holds, with a bit of the
+// bitmap to each id
 static int longest_range(size_t per_id) {
-  const int fit = per_id ? (int)((kLdsBytes - 1024) / (per_id + 1)) / 64 * 64 : 16384;
+  const int fit = per_id ? (int)((kLdsBytes - 64) * 8 / (per_id * 8 + 1)) / 64 * 64 : 16384;
   return fit < 16384 ? fit : 16384;
 }
 
 // Ranges of a launch.  Workgroups run in rounds of two to a CU, and a range
 // costs its ids plus what its start takes (about the time of 512 ids), so of
 // the cuts that fill one to four rounds more than the longest ranges need,
-// the one with the least rounds x (range + 512) is taken.  requests * ranges
-// is at most requests * (ranges of the longest) + 4 rounds.
-static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t per_id, bool touch) {
+// the one with the least rounds x (range + 512) is taken.  Where touched ids
+// are taken in the pass, ranges differ in work and at least four rounds even
+// it out: 64 blocks of 151936 ids with 4096 tokens of history, 300 biases and
+// masks took 171 us in two rounds, 164 in three, 160 in four and six; the
+// verification of 64 blocks, whose start takes longer, 144, 144, 151 and 170.
+// requests * ranges is at most requests * (ranges of the longest) + 8 rounds.
+static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t per_id, bool touch, bool verify) {
   Cut k;
   const int most = longest_range(per_id), slots = 2 * cus;
   const int least = (vocab + most - 1) / most;
   int64_t best = -1;
-  const int64_t from = ((int64_t)least * requests + slots - 1) / slots;
+  int64_t from = ((int64_t)least * requests + slots - 1) / slots;
+  if (touch && !verify && from < 4) from = 4;
   k.range = most;
   for (int64_t rounds = from; rounds < from + 4; ++rounds) {
     int64_t r = rounds * slots / requests;
@@ -886,7 +891,7 @@ static void launch_logits(const domino_verify_t* h, LogitsArgs& a, Cut& k, hipSt
   const bool penalties = a.repetition || a.frequency || a.presence;
   const bool touch = penalties || a.bias_ids;
   k = cut_vocab(h->cfg.vocab, h->cus, a.requests, a.rows, h->cfg.dtype == DOMINO_DTYPE_BF16 ? 8 : 4,
-                lds_per_id(VERIFY && a.noise, touch, VERIFY && touch, a.bias_ids != nullptr), touch);
+                lds_per_id(VERIFY && a.noise, touch, VERIFY && touch, a.bias_ids != nullptr), touch, VERIFY);
   a.range = k.range;
   a.row_slots = k.row_slots;
   a.parts = k.parts;
