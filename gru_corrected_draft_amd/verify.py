@@ -76,18 +76,26 @@ def load_library():
     return lib
 
 
-def _want(name, t, dtype, shape, device):
-    """A tensor of exactly this type and shape on the device, its last dimension contiguous."""
+def _fits(t, dtype, shape, index):
+    """The quick check of a call that is in order: type, shape and GPU of a tensor."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index
+
+
+def _want(name, t, dtype, shape, index):
+    """Refuses a tensor that is not of this type and shape on GPU ``index``, its last dimension contiguous."""
     if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if index < 0:
+        raise ValueError("tensors must be on a GPU")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if shape and shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# the current stream's address without a Stream object around it (a call's checks and arguments take
+# about as long on the host as its kernel on the GPU, so each microsecond shows)
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Handle:
@@ -136,40 +144,46 @@ class PagedAttention(_Handle):
                                                       max_requests, _DTYPES[dtype]))
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype = page_size, dtype
+        self._scale = 1.0 / math.sqrt(head_dim)
 
-    def _cache(self, k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, device):
-        n = k_cache.shape[0] if k_cache.dim() == 4 else 0
-        shape = (n, self.kv_heads, self.page_size, self.head_dim)
-        _want("k_cache", k_cache, self.dtype, shape, device)
-        _want("v_cache", v_cache, self.dtype, shape, device)
+    def _cache(self, k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index):
+        shape = (k_cache.shape[0] if k_cache.dim() else 0, self.kv_heads, self.page_size, self.head_dim)
         strides = k_cache.stride()
-        if v_cache.stride() != strides:
-            raise ValueError("k_cache and v_cache must have the same strides")
-        b = kv_len.shape[0] if kv_len.dim() == 1 else -1
-        width = page_table.shape[1] if page_table.dim() == 2 else -1
-        _want("kv_len", kv_len, torch.int32, (b,), device)
-        _want("q_start", q_start, torch.int32, (b + 1,), device)
-        _want("page_table", page_table, torch.int32, (b, width), device)
-        if not device.type == "cuda":
-            raise ValueError("tensors must be on a GPU")
+        b, width = page_table.shape if page_table.dim() == 2 else (-1, -1)
+        if not (_fits(k_cache, self.dtype, shape, index) and _fits(v_cache, self.dtype, shape, index)
+                and v_cache.stride() == strides and strides[3] == 1 and index >= 0
+                and _fits(page_table, torch.int32, (b, width), index) and _fits(kv_len, torch.int32, (b,), index)
+                and _fits(q_start, torch.int32, (b + 1,), index) and page_table.stride(1) == 1
+                and kv_len.stride(0) == 1 and q_start.stride(0) == 1):
+            _want("k_cache", k_cache, self.dtype, shape, index)
+            _want("v_cache", v_cache, self.dtype, shape, index)
+            if v_cache.stride() != strides:
+                raise ValueError("k_cache and v_cache must have the same strides")
+            _want("page_table", page_table, torch.int32, (b, width), index)
+            _want("kv_len", kv_len, torch.int32, (b,), index)
+            _want("q_start", q_start, torch.int32, (b + 1,), index)
         if max_new is None:
             max_new = tokens
         if max_kv is None:
             max_kv = min(width * self.page_size, 2 ** 31 - 1)
-        return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], n,
+        return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
                          page_table.data_ptr(), page_table.stride(0), width, kv_len.data_ptr(),
                          q_start.data_ptr(), b, tokens, max_new, max_kv)
 
     def append(self, k, v, k_cache, v_cache, page_table, kv_len, q_start, max_new=None, max_kv=None):
         """Write the new tokens' ``k`` and ``v`` ([tokens, kv_heads, head_dim]) into the cache."""
-        tokens, dev = k.shape[0], k.device
+        tokens, index = k.shape[0], k.get_device()
         shape = (tokens, self.kv_heads, self.head_dim)
-        _want("k", k, self.dtype, shape, dev)
-        _want("v", v, self.dtype, shape, dev)
-        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, dev)
-        self._check(self.lib.domino_attention_append(
-            self.handle, ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-            v.stride(0), v.stride(1), _stream(dev)))
+        ks, vs = k.stride(), v.stride()
+        if not (_fits(k, self.dtype, shape, index) and _fits(v, self.dtype, shape, index)
+                and ks[2] == 1 and vs[2] == 1):
+            _want("k", k, self.dtype, shape, index)
+            _want("v", v, self.dtype, shape, index)
+        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index)
+        st = self.lib.domino_attention_append(self.handle, ctypes.byref(c), k.data_ptr(), ks[0], ks[1],
+                                              v.data_ptr(), vs[0], vs[1], _stream(index))
+        if st:
+            self._check(st)
 
     def run(self, q, k_cache, v_cache, page_table, kv_len, q_start, max_new=None, max_kv=None, window=0,
             sinks=0, scale=None, out=None, return_lse=False):
@@ -178,19 +192,24 @@ class PagedAttention(_Handle):
         cache; otherwise a token sees the last ``window`` positions up to its own and the first
         ``sinks``.  ``scale`` defaults to head_dim ** -0.5.  Rows of ``out`` that belong to no request
         are left as they are."""
-        tokens, dev = q.shape[0], q.device
+        tokens, index = q.shape[0], q.get_device()
         shape = (tokens, self.q_heads, self.head_dim)
-        _want("q", q, self.dtype, shape, dev)
+        qs = q.stride()
+        if not (_fits(q, self.dtype, shape, index) and qs[2] == 1):
+            _want("q", q, self.dtype, shape, index)
+        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index)
         if out is None:
-            out = torch.empty(shape, dtype=self.dtype, device=dev)
+            out = torch.empty(shape, dtype=self.dtype, device=q.device)
         else:
-            _want("out", out, self.dtype, shape, dev)
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev) if return_lse else None
-        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, dev)
-        self._check(self.lib.domino_attention_run(
-            self.handle, ctypes.byref(c), q.data_ptr(), q.stride(0), q.stride(1), window, sinks,
-            1.0 / math.sqrt(self.head_dim) if scale is None else scale, out.data_ptr(), out.stride(0),
-            out.stride(1), lse.data_ptr() if return_lse else None, _stream(dev)))
+            _want("out", out, self.dtype, shape, index)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device) if return_lse else None
+        os = out.stride()
+        st = self.lib.domino_attention_run(
+            self.handle, ctypes.byref(c), q.data_ptr(), qs[0], qs[1], window, sinks,
+            self._scale if scale is None else scale, out.data_ptr(), os[0], os[1],
+            lse.data_ptr() if return_lse else None, _stream(index))
+        if st:
+            self._check(st)
         return (out, lse) if return_lse else out
 
 
@@ -218,42 +237,50 @@ class DraftVerifier(_Handle):
         if logits.dim() != 3:
             raise ValueError("logits must be [requests, rows, vocab]")
         b, rows, _ = logits.shape
-        dev = logits.device
-        _want("logits", logits, self.dtype, (b, rows, self.vocab), dev)
-        if dev.type != "cuda":
+        ls, index, i32, f32 = logits.stride(), logits.get_device(), torch.int32, torch.float32
+
+        def take(name, t, dtype, shape):
+            if not (_fits(t, dtype, shape, index) and t.stride(-1) == 1):
+                _want(name, t, dtype, shape, index)
+            return t.data_ptr()
+
+        take("logits", logits, self.dtype, (b, rows, self.vocab))
+        a = LogitsArgs(logits.data_ptr(), ls[0], ls[1], b, rows)
+        if index < 0:
             raise ValueError("tensors must be on a GPU")
-        a = LogitsArgs(logits=logits.data_ptr(), request_stride=logits.stride(0),
-                       row_stride=logits.stride(1), requests=b, rows=rows)
         if draft is not None and rows > 1:
-            _want("draft", draft, torch.int32, (b, rows - 1), dev)
-            a.draft, a.draft_stride = draft.data_ptr(), draft.stride(0)
+            a.draft, a.draft_stride = take("draft", draft, i32, (b, rows - 1)), draft.stride(0)
         if history is not None:
             width = history.shape[1] if history.dim() == 2 else -1
-            _want("history", history, torch.int32, (b, width), dev)
-            a.history, a.history_stride, a.history_width = history.data_ptr(), history.stride(0), width
+            a.history, a.history_stride = take("history", history, i32, (b, width)), history.stride(0)
+            a.history_width = width
         if (bias_ids is None) != (bias_values is None):
             raise ValueError("bias_ids and bias_values must be given together")
         if bias_ids is not None:
             width = bias_ids.shape[1] if bias_ids.dim() == 2 else -1
-            _want("bias_ids", bias_ids, torch.int32, (b, width), dev)
-            _want("bias_values", bias_values, torch.float32, (b, width), dev)
+            a.bias_ids = take("bias_ids", bias_ids, i32, (b, width))
+            a.bias_values = take("bias_values", bias_values, f32, (b, width))
             if b > 1 and bias_ids.stride(0) != bias_values.stride(0):
                 raise ValueError("bias_ids and bias_values must have the same strides")
-            a.bias_ids, a.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
             a.bias_stride, a.bias_width = bias_ids.stride(0), width
-        for name, t, dtype in (("draft_len", draft_len, torch.int32),
-                               ("history_len", history_len, torch.int32),
-                               ("prompt_len", prompt_len, torch.int32),
-                               ("bias_len", bias_len, torch.int32),
-                               ("repetition", repetition, torch.float32),
-                               ("frequency", frequency, torch.float32),
-                               ("presence", presence, torch.float32)):
-            if t is not None:
-                _want(name, t, dtype, (b,), dev)
-                setattr(a, name, t.data_ptr())
+        per_request = (b,)
+        if draft_len is not None:
+            a.draft_len = take("draft_len", draft_len, i32, per_request)
+        if history_len is not None:
+            a.history_len = take("history_len", history_len, i32, per_request)
+        if prompt_len is not None:
+            a.prompt_len = take("prompt_len", prompt_len, i32, per_request)
+        if bias_len is not None:
+            a.bias_len = take("bias_len", bias_len, i32, per_request)
+        if repetition is not None:
+            a.repetition = take("repetition", repetition, f32, per_request)
+        if frequency is not None:
+            a.frequency = take("frequency", frequency, f32, per_request)
+        if presence is not None:
+            a.presence = take("presence", presence, f32, per_request)
         if mask is not None:
-            _want("mask", mask, torch.int32, (b, rows, (self.vocab + 31) // 32), dev)
-            a.mask, a.mask_request_stride, a.mask_row_stride = mask.data_ptr(), mask.stride(0), mask.stride(1)
+            a.mask = take("mask", mask, i32, (b, rows, (self.vocab + 31) // 32))
+            a.mask_request_stride, a.mask_row_stride = mask.stride(0), mask.stride(1)
         return a
 
     def process(self, logits, draft=None, draft_len=None, history=None, history_len=None, prompt_len=None,
@@ -262,14 +289,18 @@ class DraftVerifier(_Handle):
         """The processed logits, rounded once to the handle's dtype.  ``out`` may be ``logits``."""
         a = self._args(logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
                        presence, bias_ids, bias_values, bias_len, mask)
+        index = logits.get_device()
         if out is None:
             out = torch.empty(logits.shape, dtype=self.dtype, device=logits.device)
         else:
-            _want("out", out, self.dtype, tuple(logits.shape), logits.device)
+            _want("out", out, self.dtype, tuple(logits.shape), index)
             if out.data_ptr() == logits.data_ptr() and out.stride() != logits.stride():
                 raise ValueError("out over the logits must have their strides")
-        self._check(self.lib.domino_verify_process(self.handle, ctypes.byref(a), out.data_ptr(),
-                                                   out.stride(0), out.stride(1), _stream(logits.device)))
+        os = out.stride()
+        st = self.lib.domino_verify_process(self.handle, ctypes.byref(a), out.data_ptr(), os[0], os[1],
+                                            _stream(index))
+        if st:
+            self._check(st)
         return out
 
     def run(self, logits, draft=None, draft_len=None, temperature=None, accept_u=None, noise=None,
@@ -282,23 +313,25 @@ class DraftVerifier(_Handle):
         exponential and, with proposals, ``accept_u`` [requests, rows - 1] fp32 uniform in [0, 1)."""
         a = self._args(logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
                        presence, bias_ids, bias_values, bias_len, mask)
-        b, rows, dev = a.requests, a.rows, logits.device
-        u = n = None
+        b, rows, index, dev = a.requests, a.rows, logits.get_device(), logits.device
+        temp = u = n = None
         u_stride = n_stride = 0
         if temperature is not None:
-            _want("temperature", temperature, torch.float32, (b,), dev)
+            _want("temperature", temperature, torch.float32, (b,), index)
+            temp = temperature.data_ptr()
             if noise is None or (accept_u is None and a.draft):
                 raise ValueError("temperature needs noise, and accept_u where there are proposals")
-            _want("noise", noise, torch.float32, (b, self.vocab), dev)
+            _want("noise", noise, torch.float32, (b, self.vocab), index)
             n, n_stride = noise.data_ptr(), noise.stride(0)
             if a.draft:
-                _want("accept_u", accept_u, torch.float32, (b, rows - 1), dev)
+                _want("accept_u", accept_u, torch.float32, (b, rows - 1), index)
                 u, u_stride = accept_u.data_ptr(), accept_u.stride(0)
         tokens = torch.empty((b, rows), dtype=torch.int32, device=dev)
         accepted = torch.empty((b,), dtype=torch.int32, device=dev)
         logprob = torch.empty((b, rows), dtype=torch.float32, device=dev) if return_logprob else None
-        self._check(self.lib.domino_verify_run(
-            self.handle, ctypes.byref(a), None if temperature is None else temperature.data_ptr(),
-            u, u_stride, n, n_stride, tokens.data_ptr(), accepted.data_ptr(),
-            logprob.data_ptr() if return_logprob else None, _stream(dev)))
+        st = self.lib.domino_verify_run(self.handle, ctypes.byref(a), temp, u, u_stride, n, n_stride,
+                                        tokens.data_ptr(), accepted.data_ptr(),
+                                        logprob.data_ptr() if return_logprob else None, _stream(index))
+        if st:
+            self._check(st)
         return (tokens, accepted, logprob) if return_logprob else (tokens, accepted)
