@@ -123,6 +123,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const v2bf r = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, r);
 }
+// x f, an infinity kept where f has underflowed
+__device__ __forceinline__ float scaled(float x, float f) { return __builtin_isinf(x) ? x : x * f; }
+
 __device__ __forceinline__ bool nonfinite(float x) {
   return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u;
 }

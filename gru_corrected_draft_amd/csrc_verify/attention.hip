@@ -50,6 +50,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------- fp32 attention
 // Four waves share a tile of 16 rows and take 16-key tiles in turn, each with
 // its own running maximum and sum; the four are joined in LDS at the end.
+// Where few row tiles would leave the chip idle, the keys of each are dealt to
+// several workgroups, whose outputs a second launch joins.
 // The scores are computed transposed (keys x rows), so the row's maximum and
 // sum stay in the row's lanes and the accumulator registers of the scores are
 // the second product's operand as they are: lane (n = l % 16, q = l / 16)
@@ -61,12 +63,12 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 template <int D>
-__global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a, int splits) {
   constexpr int KT = 16, ROWS = 16, C = D / 16, NB = D / 64;
   __shared__ float s_o[4][ROWS][D + 4];
   __shared__ float s_m[4][ROWS], s_l[4][ROWS];
   __shared__ int s_bad[4];
-  const int b = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * ROWS;
+  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x % splits, r0 = blockIdx.x / splits * ROWS;
   const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
   const int rows = req.n * a.group;
   if (r0 >= rows) return;
@@ -87,7 +89,7 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
     for (int j = 0; j < 4; ++j) O[i][j] = zero4();
   float m = -INFINITY, l = 0.f;
   bool bad = req.bad;
-  for (int i = w; i < span.count; i += 4) {
+  for (int i = split * 4 + w; i < span.count; i += 4 * splits) {
     const int k0 = tile_of(span, i) * KT;
     int page = a.table[b * a.table_stride + (k0 >> a.page_shift)];
     if (page < 0 || page >= a.num_pages) {
@@ -198,15 +200,60 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a) {
       // a wave that saw no key of this row holds only zeros
       if (s_m[x][rr] != -INFINITY) num += f * s_o[x][rr][d];
     }
-    float o = den == 0.f && top == -INFINITY ? 0.f : num / den;
-    if (spoilt) o = NAN;
+    if (spoilt) den = NAN;
+    if (splits > 1) {
+      const int64_t part = ((int64_t)b * a.kv_heads + h) * gridDim.x + blockIdx.x;
+      a.part_o[(part * ROWS + rr) * D + d] = num;
+      if (d == 0) {
+        a.part_ml[(part * ROWS + rr) * 2] = top;
+        a.part_ml[(part * ROWS + rr) * 2 + 1] = den;
+      }
+      continue;
+    }
+    const float o = den == 0.f && top == -INFINITY ? 0.f : num / den;
     const int tk = (r0 + rr) / a.group, hd = h * a.group + (r0 + rr) - tk * a.group;
     ((float*)a.out)[(req.q0 + tk) * a.o_tok + hd * a.o_head + d] = o;
     if (d == 0 && a.lse)
       a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] =
-          spoilt ? NAN : (den == 0.f && top == -INFINITY ? -INFINITY : top * a.scale + logf(den));
+          den == 0.f && top == -INFINITY ? -INFINITY : top * a.scale + logf(den);
   }
 }
+
+// Joins the parts of each row: a thread takes four elements of one.
+template <int D>
+__global__ __launch_bounds__(256) void join_f32_kernel(AttendArgs a, int splits, int row_tiles) {
+  constexpr int ROWS = 16;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  const int i = blockIdx.x * 256 + threadIdx.x, r = i / (D / 4), piece = i - r * (D / 4);
+  if (r >= req.n * a.group) return;
+  const int tile = r / ROWS, row = r - tile * ROWS;
+  const int64_t first = (((int64_t)b * a.kv_heads + h) * row_tiles + tile) * splits;
+  float top = -INFINITY, den = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = *(const float2*)(a.part_ml + ((first + s) * ROWS + row) * 2);
+    const float4 y = load4(a.part_o + ((first + s) * ROWS + row) * D + 4 * piece);
+    const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float fo = exp2f((top - ref) * a.scale_log2), fn = exp2f((ml.x - ref) * a.scale_log2);
+    den = den * fo + ml.y * fn;
+    o.x = scaled(o.x, fo) + scaled(y.x, fn);
+    o.y = scaled(o.y, fo) + scaled(y.y, fn);
+    o.z = scaled(o.z, fo) + scaled(y.z, fn);
+    o.w = scaled(o.w, fo) + scaled(y.w, fn);
+    top = mn;
+  }
+  const bool none = den == 0.f && top == -INFINITY;
+  const int tk = r / a.group, hd = h * a.group + r - tk * a.group;
+  *(float4*)((float*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + 4 * piece) =
+      none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / den, o.y / den, o.z / den, o.w / den);
+  if (piece == 0 && a.lse)
+    a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] = none ? -INFINITY : top * a.scale + logf(den);
+}
+
+// workspace of split fp32 attention: 2 parts of 16 rows to a CU
+static size_t attend_f32_floats(int head_dim, int cus) { return (size_t)2 * cus * 16 * (head_dim + 2); }
 
 // ---------------------------------------------------------------- handle
 struct domino_attention : HandleBase {
@@ -251,14 +298,14 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
     (void)hipGetLastError();
     h->cus = 256;
   }
-  if (cfg->dtype == DOMINO_DTYPE_BF16) {
-    h->part = (float*)h->take(attend_split_floats(cfg->head_dim, h->cus) * sizeof(float));
-    h->plan = (int32_t*)h->take((size_t)(cfg->max_requests + 1) * sizeof(int32_t));
-    if (!h->part || !h->plan) {
-      h->release();
-      delete h;
-      return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: workspace allocation failed");
-    }
+  const size_t floats = cfg->dtype == DOMINO_DTYPE_BF16 ? attend_split_floats(cfg->head_dim, h->cus)
+                                                        : attend_f32_floats(cfg->head_dim, h->cus);
+  h->part = (float*)h->take(floats * sizeof(float));
+  h->plan = (int32_t*)h->take((size_t)(cfg->max_requests + 1) * sizeof(int32_t));
+  if (!h->part || !h->plan) {
+    h->release();
+    delete h;
+    return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: workspace allocation failed");
   }
   *out = h;
   return DOMINO_OK;
@@ -368,15 +415,19 @@ extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const 
   return launched(h, "append");
 }
 
-static void launch_attend_f32(int D, const AttendArgs& a, hipStream_t st) {
-  const int64_t rows = (int64_t)a.max_new * a.group;
-  const dim3 grid((unsigned)((rows + 15) / 16), a.kv_heads, a.requests);
-  if (D == 64)
-    hipLaunchKernelGGL((attend_f32_kernel<64>), grid, dim3(256), 0, st, a);
-  else if (D == 128)
-    hipLaunchKernelGGL((attend_f32_kernel<128>), grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((attend_f32_kernel<256>), grid, dim3(256), 0, st, a);
+template <int D>
+static void launch_attend_f32(const AttendArgs& a, int cus, hipStream_t st) {
+  const int64_t rows = (int64_t)a.max_new * a.group, tiles = (rows + 15) / 16;
+  const int64_t segments = tiles * a.kv_heads * a.requests, keys = (a.max_kv + 63) / 64;
+  // a workgroup to each half of a CU, with at least 64 keys
+  int64_t splits = 2 * cus / segments;
+  if (splits > keys) splits = keys;
+  if (splits < 1) splits = 1;
+  hipLaunchKernelGGL((attend_f32_kernel<D>), dim3((unsigned)(tiles * splits), a.kv_heads, a.requests), dim3(256), 0, st,
+                     a, (int)splits);
+  if (splits > 1)
+    hipLaunchKernelGGL((join_f32_kernel<D>), dim3((unsigned)((rows * (D / 4) + 255) / 256), a.kv_heads, a.requests),
+                       dim3(256), 0, st, a, (int)splits, (int)tiles);
 }
 
 extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t* c,
@@ -445,7 +496,14 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
     a.min_share = 2;
     launch_attend_split(f.head_dim, a, h->cus, (hipStream_t)stream);
   } else {
-    launch_attend_f32(f.head_dim, a, (hipStream_t)stream);
+    a.part_o = h->part;
+    a.part_ml = h->part + attend_f32_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;
+    if (f.head_dim == 64)
+      launch_attend_f32<64>(a, h->cus, (hipStream_t)stream);
+    else if (f.head_dim == 128)
+      launch_attend_f32<128>(a, h->cus, (hipStream_t)stream);
+    else
+      launch_attend_f32<256>(a, h->cus, (hipStream_t)stream);
   }
   return launched(h, "run");
 }

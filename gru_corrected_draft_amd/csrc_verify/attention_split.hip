@@ -467,9 +467,6 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
   }
 }
 
-// x f, an infinity kept where f has underflowed
-__device__ __forceinline__ float scaled(float x, float f) { return __builtin_isinf(x) ? x : x * f; }
-
 // Joins the parts of split segments: 256 threads take 1024 / D rows of one
 // (request, row tile, key head).
 template <int D, int R>
