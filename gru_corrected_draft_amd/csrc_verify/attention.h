@@ -44,6 +44,7 @@ struct AttendArgs {
   float* part_ml;  // [slots][rows][2]
   int32_t* plan;   // [requests + 2]
   int32_t min_share;
+  bool pieces;  // segments cut for themselves
 };
 
 // A value that is the same in every lane, in a scalar register: branches and

@@ -22,7 +22,10 @@
 // whatever the lengths of the requests: each workgroup sums up the lengths
 // itself.  A share ends at most two segments inside; those leave their
 // unnormalised output, maximum and sum in the workspace, and a second launch
-// joins them.
+// joins them.  With no more segments than half the workgroups, each segment is
+// cut into pieces of its own instead, one to a workgroup: a share that straddles
+// two segments would pay for two starts and two ends (8 requests with 16 tokens
+// over 2 to 4 thousand keys took 35 us so).
 #include "attention_bf16.h"
 
 namespace {
@@ -66,14 +69,14 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
   constexpr int S = C::S, ROWS = C::kRows, RING = C::kRing, THREADS = C::kThreads, JOIN = C::kJoin;
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ int s_sum[C::W];
-  __shared__ float s_m[C::W][32], s_l[C::W][32];
+  __shared__ float s_m[C::W][32], s_l[C::W][32], s_f[C::W][32];
   __shared__ int s_bad;
   __shared__ uint16_t s_notes[C::W][32 * (D / 8)];
   __shared__ int s_noting[C::W];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 31, h2 = lane >> 5;
   const int rg = w / S, stream = w - rg * S;
 
-  int b = 0, begin = 0, at = 0, end = 1, upto = 0;
+  int b = 0, begin = 0, at = 0, end = 1, upto = 0, mine_pieces = 0;
   Request mine{0, 0, 0, false};
   const bool few = a.requests <= 64;
   if constexpr (!WHOLE) {
@@ -84,6 +87,22 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     if (few) {
       if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
       upto = lane < a.requests ? request_steps<ROWS, S>(a, mine) : 0;
+      if (a.pieces) {
+        // The shortest piece at which there are workgroups for all, each lane
+        // trying one between an even share and twice that, where there are.
+        int all = upto;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
+        const int even = max(a.min_share, (all + (int)gridDim.x - 1) / (int)gridDim.x);
+        const int steps = upto / a.kv_heads, size = even + lane + (int)((int64_t)even * lane / 63);
+        int need = 0;
+#pragma unroll 1
+        for (int i = 0; i < a.requests; ++i) need += (__builtin_amdgcn_readlane(steps, i) + size - 1) / size;
+        const uint64_t fits = __ballot(need * a.kv_heads <= (int)gridDim.x);
+        const int piece = __builtin_amdgcn_readlane(size, fits ? __builtin_ctzll(fits) : 63);
+        mine_pieces = (steps + piece - 1) / piece;
+        upto = mine_pieces * a.kv_heads;
+      }
   #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int y = __shfl_up(upto, d, 64);
@@ -115,7 +134,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       total = carry;
     }
     total = uniform(total);
-    const int share = max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const int share = a.pieces ? 1 : max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     at = blockIdx.x * share;
     end = min(at + share, total);
     if (at >= end) return;
@@ -195,16 +214,27 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       int off = at - begin;
       span = row_tile_span<ROWS>(a, req, 0);
       seg = steps_of(span.count, S);
-      while (uniform(off >= seg * a.kv_heads)) {
-        off -= seg * a.kv_heads;
-        span = row_tile_span<ROWS>(a, req, ++rt);
-        seg = steps_of(span.count, S);
+      if (a.pieces) {
+        const int pieces = __builtin_amdgcn_readlane(mine_pieces, b);
+        h = uniform(off / pieces);
+        const int x = off - h * pieces;
+        first = uniform((int)((int64_t)seg * x / pieces));
+        stop = uniform((int)((int64_t)seg * (x + 1) / pieces));
+      } else {
+        while (uniform(off >= seg * a.kv_heads)) {
+          off -= seg * a.kv_heads;
+          span = row_tile_span<ROWS>(a, req, ++rt);
+          seg = steps_of(span.count, S);
+        }
+        h = off / seg;
+        first = off - h * seg;
+        stop = min(seg, first + end - at);
       }
       rt = uniform(rt);
       seg = uniform(seg);
-      h = uniform(off / seg);
-      first = uniform(off - h * seg);
-      stop = min(seg, first + end - at);
+      h = uniform(h);
+      first = uniform(first);
+      stop = uniform(stop);
     }
     span = uniform(span);
     req = Request{uniform(req.q0), uniform(req.n), uniform(req.kv), (bool)uniform(req.bad)};
@@ -414,22 +444,49 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
                 st.o[blk][4 * x], st.o[blk][4 * x + 1], st.o[blk][4 * x + 2], st.o[blk][4 * x + 3]);
           }
       }
+      // a row's factors for its streams, the division by the sum in them where
+      // the row is complete
+      float top = -INFINITY, den = 0.f;
+      const int row_ = tid & 31, g_ = tid >> 5;
+      const bool joins = j0 == 0 && tid < 32 * R;
+      if (joins) {
+#pragma unroll
+        for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[g_ * S + x][row_]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float f[S];
+#pragma unroll
+        for (int x = 0; x < S; ++x) {
+          f[x] = __builtin_amdgcn_exp2f((s_m[g_ * S + x][row_] - ref) * a.scale_log2);
+          den += f[x] * s_l[g_ * S + x][row_];
+        }
+        const float inv = !whole ? 1.f : den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+        for (int x = 0; x < S; ++x) s_f[g_ * S + x][row_] = f[x] * inv;
+      }
       __syncthreads();
       const bool spoilt = s_bad != 0;
+      if (joins && r0 + g_ * 32 + row_ <= last) {
+        if (spoilt) den = NAN;
+        if (whole) {
+          const int r = r0 + g_ * 32 + row_, tok = r / a.group, hq = h * a.group + r - tok * a.group;
+          if (a.lse)
+            a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
+        } else {
+          *(float2*)(a.part_ml + (part * ROWS + g_ * 32 + row_) * 2) = make_float2(top, den);
+        }
+      }
+      int odd = 0;
+#pragma unroll
+      for (int x = 0; x < C::W; ++x) odd |= s_noting[x];
+#pragma unroll 4
       for (int i = tid; i < R * JOIN * (D / 4); i += THREADS) {
         const int piece = i % (D / 4), row = j0 + (i / (D / 4)) % JOIN, g = i / (D / 4) / JOIN;
         const int in_tile = g * 32 + row;  // row of the row tile
         if (r0 + in_tile > last) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[g * S + x][row]);
-        const float ref = top == -INFINITY ? 0.f : top;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = spoilt ? NAN : 0.f;
 #pragma unroll
         for (int x = 0; x < S; ++x) {
-          const float f = __builtin_amdgcn_exp2f((s_m[g * S + x][row] - ref) * a.scale_log2);
-          den += f * s_l[g * S + x][row];
+          const float f = s_f[g * S + x][row];
           const float4 y =
               *(const float4*)(so + (((g * S + x) * JOIN + row - j0) * D + (piece ^ (row & (D / 4 - 1))) * 4));
           o.x += f * y.x;
@@ -437,33 +494,29 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
           o.z += f * y.z;
           o.w += f * y.w;
         }
+        if (__builtin_expect(odd, 0)) {
 #pragma unroll 1
-        for (int x = 0; x < S; ++x)
-          if (s_noting[g * S + x]) {
-            const uint32_t note = s_notes[g * S + x][row * (D / 8) + piece / 2] >> (8 * (piece & 1));
-            o.x = noted(o.x, note & 3);
-            o.y = noted(o.y, note >> 2 & 3);
-            o.z = noted(o.z, note >> 4 & 3);
-            o.w = noted(o.w, note >> 6 & 3);
-          }
+          for (int x = 0; x < S; ++x)
+            if (s_noting[g * S + x]) {
+              const uint32_t note = s_notes[g * S + x][row * (D / 8) + piece / 2] >> (8 * (piece & 1));
+              o.x = noted(o.x, note & 3);
+              o.y = noted(o.y, note >> 2 & 3);
+              o.z = noted(o.z, note >> 4 & 3);
+              o.w = noted(o.w, note >> 6 & 3);
+            }
+        }
         if (whole) {
-          const float inv = den == 0.f ? 0.f : 1.f / den;
+          if (spoilt) o = make_float4(NAN, NAN, NAN, NAN);
           const int r = r0 + in_tile, tok = r / a.group, hq = h * a.group + r - tok * a.group;
           *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
-              u32x2{pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)};
-          if (piece == 0 && a.lse)
-            a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
+              u32x2{pack_bf16(o.x, o.y), pack_bf16(o.z, o.w)};
         } else {
           *(float4*)(a.part_o + (part * ROWS + in_tile) * D + 4 * piece) = o;
-          if (piece == 0) {
-            a.part_ml[(part * ROWS + in_tile) * 2] = top;
-            a.part_ml[(part * ROWS + in_tile) * 2 + 1] = den;
-          }
         }
       }
     }
     __syncthreads();
-    at = uniform(at + stop - first);
+    at = uniform(WHOLE || a.pieces ? end : at + stop - first);
   }
 }
 
@@ -477,13 +530,22 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
   const int rows = req.n * a.group, r0 = rt * ROWS;
   const int row = group * PER + threadIdx.x / (D / 4), piece = threadIdx.x % (D / 4);
   if (r0 + row >= rows || row >= ROWS) return;
-  const int total = a.plan[a.requests];
-  const int share = max(a.min_share, (total + workers - 1) / workers);
-  int from = a.plan[b];
-  for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, S) * a.kv_heads;
-  const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, S);
-  from += h * seg;
-  const int g0 = from / share, g1 = (from + seg - 1) / share;
+  const int from0 = a.plan[b];
+  int g0, g1;
+  if (a.pieces) {
+    const int pieces = (a.plan[b + 1] - from0) / a.kv_heads;
+    g0 = from0 + h * pieces;
+    g1 = g0 + pieces - 1;
+  } else {
+    const int total = a.plan[a.requests];
+    const int share = max(a.min_share, (total + workers - 1) / workers);
+    int from = from0;
+    for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, S) * a.kv_heads;
+    const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, S);
+    from += h * seg;
+    g0 = from / share;
+    g1 = (from + seg - 1) / share;
+  }
   if (g0 == g1) return;
   float top = -INFINITY, den = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -521,7 +583,7 @@ void launch_kernel(const AttendArgs& a, dim3 grid, hipStream_t st) {
 }
 
 template <int D, int R>
-void launch(const AttendArgs& a, int cus, hipStream_t st) {
+void launch(AttendArgs a, int cus, hipStream_t st) {
   using C = Shape<D, R>;
   constexpr int ROWS = C::kRows, PER = 1024 / D;
   const int64_t rows = (int64_t)a.max_new * a.group;
@@ -534,6 +596,7 @@ void launch(const AttendArgs& a, int cus, hipStream_t st) {
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
   const int workers = (int)(need < cus ? need : cus);
+  a.pieces = row_tiles == 1 && a.requests <= 64 && 2 * segments <= workers;
   launch_kernel<D, R, false>(a, dim3(workers), st);
   const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
   hipLaunchKernelGGL((attend_join_kernel<D, R>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests),
