@@ -114,6 +114,39 @@ __device__ __forceinline__ bool all_visible(const KeySpan& s, int k0, int n, int
   return k0 + n - 1 <= s.pmin && (window == 0 || k0 > s.pmax - window || k0 + n <= sinks);
 }
 
+// Ranges of tile indices: [whole_lo, whole_hi) are tiles that all rows see
+// whole, and of those from sink_hi on, which hold no sink, some row sees a key
+// of [some_lo, some_hi).
+struct TileRange {
+  int whole_lo, whole_hi, some_lo, some_hi, sink_hi;
+};
+
+__device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
+
+template <int KT>
+__device__ __forceinline__ TileRange tile_range(const KeySpan& s, int window, int sinks) {
+  const int shift = s.sink_tiles - s.first;  // index of a tile past the sinks, less the tile
+  TileRange r;
+  r.whole_hi = floor_div(s.pmin + 1, KT) + shift;
+  r.whole_lo = s.sink_tiles;
+  r.some_hi = floor_div(s.pmax, KT) + 1 + shift;
+  r.some_lo = s.sink_tiles;
+  r.sink_hi = (sinks + KT - 1) / KT + shift;
+  if (r.sink_hi < s.sink_tiles) r.sink_hi = s.sink_tiles;
+  if (window > 0) {
+    const int lo = floor_div(s.pmax - window, KT) + 1 + shift;      // first key > pmax - window
+    if (lo > r.whole_lo) r.whole_lo = lo;
+    const int some = floor_div(s.pmin - window + 1, KT) + shift;    // last key > pmin - window
+    if (some > r.some_lo) r.some_lo = some;
+  }
+  return r;
+}
+
+__device__ __forceinline__ TileRange uniform(const TileRange& r) {
+  return TileRange{uniform(r.whole_lo), uniform(r.whole_hi), uniform(r.some_lo), uniform(r.some_hi),
+                   uniform(r.sink_hi)};
+}
+
 __device__ __forceinline__ bool visible(int key, int p, int window, int sinks) {
   return key <= p && (window == 0 || key > p - window || key < sinks);
 }

@@ -241,7 +241,9 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     bool bad = req.bad;
 
     const_i32* const table = (const_i32*)(a.table + b * a.table_stride);
-    const int64_t head = h * a.head;
+    const uint64_t head = 2 * (uint64_t)h * (uint64_t)a.head, page_bytes = 2 * (uint64_t)a.page;
+    const uint32_t row_bytes = 2 * (uint32_t)a.row;
+    const TileRange range = uniform(tile_range<32>(span, a.window, a.sinks));
     const int page_mask = (1 << a.page_shift) - 1;
     const int tiles = min(stop * S, span.count);
     int next = first * S + stream, ahead = 0, slot_in = 0, slot_out = 0;
@@ -253,28 +255,30 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       const bool seen = key < span.hi && (key + 15 >= span.lo || key < a.sinks);
       return table[(seen ? key : other) >> a.page_shift];
     };
-    int page0 = 0, page1 = 0;
+    const int own_half = R >= 4 ? rg / (R / 4) % 2 : 0;  // of a tile's keys, R >= 4
+    int page0 = 0, page1 = 0, next_key = 0;
     auto look_up = [&]() {
-      const int key = tile_of(span, next) * 32;
-      if constexpr (R >= 4) {
-        const int c = rg / (R / 4) % 2;
-        page0 = page_of(key + 16 * c, key + 16 - 16 * c);
+      next_key = tile_of(span, next) * 32;
+      const int k0 = next_key + 16 * own_half, k1 = next_key + 16 - 16 * own_half;
+      if (next >= range.whole_lo && next < range.whole_hi) {
+        page0 = table[k0 >> a.page_shift];
+        if (R < 4) page1 = table[k1 >> a.page_shift];
       } else {
-        page0 = page_of(key, key + 16);
-        page1 = page_of(key + 16, key);
+        page0 = page_of(k0, k1);
+        if (R < 4) page1 = page_of(k1, k0);
       }
     };
     if (next < tiles) look_up();
-    // where 16 keys lie, in elements
+    // where 16 keys lie, in bytes
     auto chunk = [&](int key, int page) -> int64_t {
-      if (page < 0 || page >= a.num_pages) {
+      if ((uint32_t)page >= (uint32_t)a.num_pages) {
         bad = true;
         page = 0;
       }
-      return page * a.page + head + (int64_t)(key & page_mask) * a.row;
+      return (int64_t)((uint32_t)page * page_bytes + head) + (uint32_t)(key & page_mask) * row_bytes;
     };
     auto copy = [&](const void* cache, int64_t at16, const lds_byte* dst, int j0, int j1) {
-      const char* from = (const char*)cache + 2 * at16;
+      const char* from = (const char*)cache + at16;
 #pragma unroll
       for (int j = 0; j < T::kChunkLoads; ++j)
         if (j >= j0 && j < j1)
@@ -282,7 +286,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     };
     // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
-      const int key = tile_of(span, next) * 32, p0 = page0, p1 = page1;
+      const int key = next_key, p0 = page0, p1 = page1;
       next += S;
       ++ahead;
       if (next < tiles) look_up();
@@ -290,7 +294,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       slot_in = slot_in + 1 == RING ? 0 : slot_in + 1;
       if constexpr (R >= 4) {  // 16 rows of K or of V, or half the copies of them
         constexpr int PART = R / 4, LOADS = T::kChunkLoads / PART;
-        const int x = rg / (2 * PART), c = rg / PART % 2, j0 = rg % PART * LOADS;
+        const int x = rg / (2 * PART), c = own_half, j0 = rg % PART * LOADS;
         copy(x ? a.v : a.k, chunk(key + 16 * c, p0), dst + x * T::kHalf + c * (T::kHalf / 2), j0,
              j0 + LOADS);
       } else {
@@ -345,6 +349,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       seen.pmin = uniform(req.kv - req.n + min(w0, last) / a.group);
       seen.pmax = uniform(req.kv - req.n + min(w0 + 31, last) / a.group);
     }
+    const TileRange mine_range = R > 1 ? uniform(tile_range<32>(seen, a.window, a.sinks)) : range;
     RowState<D> st;
     st.clear();
     bool noting = false;
@@ -364,26 +369,33 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 #pragma unroll 1
     for (int i = first * S + stream; i - stream < tiles; i += S) {
       lds_byte* const tile = own + slot_out * T::kBytes;
-      const int key = tile_of(span, i) * 32;
       if constexpr (R == 1) {
         if (i >= tiles) break;
-        if (next < tiles) fetch();
-        land();
-        if (!all_visible(span, key, 32, a.window, a.sinks) && note(tile, key)) clear_odd_values<D>(tile, 0, 1, lane);
+        if (next < tiles) {
+          fetch();
+          --ahead;
+          wait_copies<(RING - 1) * C::kLoads>();
+        } else {
+          land();
+        }
+        if ((i < range.whole_lo || i >= range.whole_hi) && note(tile, tile_of(span, i) * 32))
+          clear_odd_values<D>(tile, 0, 1, lane);
       } else {
         // every wave's copies of this tile have landed, and every wave is done
         // with the tile before it, whose place the next copies take
-        if (i < tiles) land();
-        asm volatile("s_barrier" ::: "memory");
-        if (next < tiles) fetch();
-        bool edge = false;  // of any stream: all waves come to the barriers
-#pragma unroll
-        for (int x = 0; x < S; ++x) {
-          const int j = i - stream + x;
-          edge |= j < tiles && !all_visible(span, tile_of(span, j) * 32, 32, a.window, a.sinks);
+        if (next < tiles) {
+          --ahead;
+          wait_copies<(RING - 2) * C::kLoads>();
+          asm volatile("s_barrier" ::: "memory");
+          fetch();
+        } else {
+          if (i < tiles) land();
+          asm volatile("s_barrier" ::: "memory");
         }
-        if (uniform(edge)) {
-          const bool odd = i < tiles && note(tile, key);
+        // some stream's tile is not seen whole by all rows: all waves come to
+        // the barriers
+        if (i - stream < range.whole_lo || i - stream + S > range.whole_hi) {
+          const bool odd = i < tiles && note(tile, tile_of(span, i) * 32);
           __syncthreads();
           if (odd) clear_odd_values<D>(tile, rg, R, lane);
           __syncthreads();
@@ -391,13 +403,13 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         if (i >= tiles) continue;
       }
       slot_out = slot_out + 1 == RING ? 0 : slot_out + 1;
-      if (R > 1 && (key > seen.pmax ||
-                    (a.window && key + 31 <= seen.pmin - a.window && key >= a.sinks)))
+      if (R > 1 && (i >= mine_range.some_hi || (i < mine_range.some_lo && i >= mine_range.sink_hi)))
         continue;  // none of this wave's rows sees it
       v16f s = scores<D>(tile, k0_off, Q);
       ValueFrags v = read_values<D>(tile, v0_off, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (!all_visible(seen, key, 32, a.window, a.sinks)) {
+      if (i < mine_range.whole_lo || i >= mine_range.whole_hi) {
+        const int key = tile_of(span, i) * 32;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[j] = -INFINITY;
