@@ -136,14 +136,14 @@ struct RowState {
 
 constexpr float kSlack = 8.f;
 
-// Scores of a tile to weights: updates the running sum, first rescaling what
+// Scores of N tiles to weights: updates the running sum, first rescaling what
 // there is where the maximum has outgrown m, and leaves the weights, rounded to
 // bf16 for the second product, in p.
-template <int D>
-__device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[2], float scale_log2) {
-  float top = fmaxf(s[0], s[1]);
+template <int D, int N>
+__device__ __forceinline__ void softmax_step(v16f (&s)[N], RowState<D>& st, v8s (&p)[N][2], float scale_log2) {
+  float top = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
-  for (int i = 2; i < 16; ++i) top = fmaxf(top, s[i]);
+  for (int i = 2; i < 16 * N; ++i) top = fmaxf(top, s[i / 16][i % 16]);
   top = max_halves(top);
   // also true at a row's first visible score, where m is -inf
   if (__any(top * scale_log2 > st.m * scale_log2 + kSlack)) {
@@ -155,19 +155,22 @@ __device__ __forceinline__ void softmax_step(v16f& s, RowState<D>& st, v8s (&p)[
     st.m = mn;
   }
   const float ref = st.m == -INFINITY ? 0.f : st.m * scale_log2;
-  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale_log2, -ref));
-    sum += s[i];
+  for (int t = 0; t < N; ++t) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], scale_log2, -ref));
+      sum += s[t][i];
+    }
+    st.l += sum;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(s[t][2 * i], s[t][2 * i + 1]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      p[t][c] = __builtin_bit_cast(v8s, (u32x4{w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]}));
   }
-  st.l += sum;
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(s[2 * i], s[2 * i + 1]);
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    p[c] = __builtin_bit_cast(v8s, (u32x4{w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]}));
 }
 
 // S^T = K Q^T for one tile.  The fragments are all on their way before the

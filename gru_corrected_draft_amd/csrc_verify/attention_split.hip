@@ -40,7 +40,10 @@ struct Shape {
   static constexpr int kRing = D == 64 ? 4 : (R == 1 ? 2 : 4);
   static constexpr int kLds = S * kRing * KeyTile<D>::kBytes;
   static constexpr int kJoin = kLds / (W * D * 4) < 32 ? kLds / (W * D * 4) : 32;  // rows joined at a time
-  static constexpr int kLoads = KeyTile<D>::kLoads / R;  // copies of a tile by one wave
+  static constexpr int N = R == 8 ? 2 : 1;  // tiles of a stream in a step
+  static constexpr int kStep = S * N;
+  static constexpr int kAhead = kRing / N - 1;              // steps on their way
+  static constexpr int kLoads = N * KeyTile<D>::kLoads / R;  // copies of a step by one wave
 };
 
 __device__ __forceinline__ int steps_of(int count, int streams) {
@@ -55,10 +58,10 @@ __device__ __forceinline__ KeySpan row_tile_span(const AttendArgs& a, const Requ
 }
 
 // steps of a request
-template <int ROWS, int S>
+template <int ROWS, int STEP>
 __device__ __forceinline__ int request_steps(const AttendArgs& a, const Request& r) {
   int n = 0;
-  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += steps_of(row_tile_span<ROWS>(a, r, rt).count, S);
+  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += steps_of(row_tile_span<ROWS>(a, r, rt).count, STEP);
   return n * a.kv_heads;
 }
 
@@ -66,7 +69,7 @@ template <int D, int R, bool WHOLE>
 __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void attend_split_kernel(AttendArgs a) {
   using T = KeyTile<D>;
   using C = Shape<D, R>;
-  constexpr int S = C::S, ROWS = C::kRows, RING = C::kRing, THREADS = C::kThreads, JOIN = C::kJoin;
+  constexpr int S = C::S, N = C::N, STEP = C::kStep, ROWS = C::kRows, RING = C::kRing, THREADS = C::kThreads, JOIN = C::kJoin;
   extern __shared__ __align__(1024) unsigned char ring[];
   __shared__ int s_sum[C::W];
   __shared__ float s_m[C::W][32], s_l[C::W][32], s_f[C::W][32];
@@ -86,7 +89,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     int total;
     if (few) {
       if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
-      upto = lane < a.requests ? request_steps<ROWS, S>(a, mine) : 0;
+      upto = lane < a.requests ? request_steps<ROWS, STEP>(a, mine) : 0;
       if (a.pieces) {
         // The shortest piece at which there are workgroups for all, each lane
         // trying one between an even share and twice that, where there are.
@@ -115,7 +118,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       for (int b0 = 0; b0 < a.requests; b0 += THREADS) {
         const int b = b0 + tid;
         int x = b < a.requests
-                    ? request_steps<ROWS, S>(a, request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv))
+                    ? request_steps<ROWS, STEP>(a, request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv))
                     : 0;
   #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -193,7 +196,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       if (rt * ROWS >= req.n * a.group) return;
       span = row_tile_span<ROWS>(a, req, rt);
       first = 0;
-      stop = seg = uniform(steps_of(span.count, S));
+      stop = seg = uniform(steps_of(span.count, STEP));
     } else {
       if (few) {
         b = __builtin_ctzll(__ballot(upto > at));
@@ -205,7 +208,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       } else {
         for (;;) {  // requests without rows have no steps
           req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
-          const int steps = request_steps<ROWS, S>(a, req);
+          const int steps = request_steps<ROWS, STEP>(a, req);
           if (uniform(at < begin + steps)) break;
           begin = uniform(begin + steps);
           b = uniform(b + 1);
@@ -213,7 +216,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       }
       int off = at - begin;
       span = row_tile_span<ROWS>(a, req, 0);
-      seg = steps_of(span.count, S);
+      seg = steps_of(span.count, STEP);
       if (a.pieces) {
         const int pieces = __builtin_amdgcn_readlane(mine_pieces, b);
         h = uniform(off / pieces);
@@ -224,7 +227,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         while (uniform(off >= seg * a.kv_heads)) {
           off -= seg * a.kv_heads;
           span = row_tile_span<ROWS>(a, req, ++rt);
-          seg = steps_of(span.count, S);
+          seg = steps_of(span.count, STEP);
         }
         h = off / seg;
         first = off - h * seg;
@@ -245,8 +248,8 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     const uint32_t row_bytes = 2 * (uint32_t)a.row;
     const TileRange range = uniform(tile_range<32>(span, a.window, a.sinks));
     const int page_mask = (1 << a.page_shift) - 1;
-    const int tiles = min(stop * S, span.count);
-    int next = first * S + stream, ahead = 0, slot_in = 0, slot_out = 0;
+    const int tiles = min(stop * STEP, span.count);
+    int next = first * STEP + stream * N, ahead = 0, slot_in = 0, slot_out = 0;
 
     // The page of the 16 keys from `key` on; keys that no row sees may have
     // none and take that of `other`, the tile's other half.  Read for a tile
@@ -255,12 +258,17 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       const bool seen = key < span.hi && (key + 15 >= span.lo || key < a.sinks);
       return table[(seen ? key : other) >> a.page_shift];
     };
-    const int own_half = R >= 4 ? rg / (R / 4) % 2 : 0;  // of a tile's keys, R >= 4
+    // R >= 4: the half of a tile's keys, and of a step's tiles the one, that this
+    // wave copies
+    const int own_half = R >= 4 ? rg % 2 : 0, own_tile = R == 8 ? rg / 4 : 0;
     int page0 = 0, page1 = 0, next_key = 0;
     auto look_up = [&]() {
-      next_key = tile_of(span, next) * 32;
+      // a step's last tile may not be there: the one before it in its place,
+      // whose values are cleared
+      const int i = min(next + own_tile, span.count - 1);
+      next_key = tile_of(span, i) * 32;
       const int k0 = next_key + 16 * own_half, k1 = next_key + 16 - 16 * own_half;
-      if (next >= range.whole_lo && next < range.whole_hi) {
+      if (i >= range.whole_lo && i < range.whole_hi) {
         page0 = table[k0 >> a.page_shift];
         if (R < 4) page1 = table[k1 >> a.page_shift];
       } else {
@@ -277,54 +285,51 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       }
       return (int64_t)((uint32_t)page * page_bytes + head) + (uint32_t)(key & page_mask) * row_bytes;
     };
-    auto copy = [&](const void* cache, int64_t at16, const lds_byte* dst, int j0, int j1) {
+    auto copy = [&](const void* cache, int64_t at16, const lds_byte* dst) {
       const char* from = (const char*)cache + at16;
 #pragma unroll
-      for (int j = 0; j < T::kChunkLoads; ++j)
-        if (j >= j0 && j < j1)
-          copy_to_lds(from, src[j], dst + j * 1024);
+      for (int j = 0; j < T::kChunkLoads; ++j) copy_to_lds(from, src[j], dst + j * 1024);
     };
     // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
       const int key = next_key, p0 = page0, p1 = page1;
-      next += S;
+      next += STEP;
       ++ahead;
       if (next < tiles) look_up();
-      const lds_byte* dst = own + slot_in * T::kBytes;
-      slot_in = slot_in + 1 == RING ? 0 : slot_in + 1;
-      if constexpr (R >= 4) {  // 16 rows of K or of V, or half the copies of them
-        constexpr int PART = R / 4, LOADS = T::kChunkLoads / PART;
-        const int x = rg / (2 * PART), c = own_half, j0 = rg % PART * LOADS;
-        copy(x ? a.v : a.k, chunk(key + 16 * c, p0), dst + x * T::kHalf + c * (T::kHalf / 2), j0,
-             j0 + LOADS);
+      const lds_byte* dst = own + slot_in * (N * T::kBytes);
+      slot_in = slot_in + 1 == RING / N ? 0 : slot_in + 1;
+      if constexpr (R >= 4) {  // 16 rows of K or of V
+        const int x = rg / 2 % 2;
+        copy(x ? a.v : a.k, chunk(key + 16 * own_half, p0),
+             dst + own_tile * T::kBytes + x * T::kHalf + own_half * (T::kHalf / 2));
       } else {
         const int64_t c0 = chunk(key, p0), c1 = chunk(key + 16, p1);
         if (R == 1 || rg == 0) {
-          copy(a.k, c0, dst, 0, T::kChunkLoads);
-          copy(a.k, c1, dst + T::kHalf / 2, 0, T::kChunkLoads);
+          copy(a.k, c0, dst);
+          copy(a.k, c1, dst + T::kHalf / 2);
         }
         if (R == 1 || rg == 1) {
-          copy(a.v, c0, dst + T::kHalf, 0, T::kChunkLoads);
-          copy(a.v, c1, dst + T::kHalf + T::kHalf / 2, 0, T::kChunkLoads);
+          copy(a.v, c0, dst + T::kHalf);
+          copy(a.v, c1, dst + T::kHalf + T::kHalf / 2);
         }
       }
     };
-    // waits until the oldest of `ahead` tiles in flight has landed
+    // waits until the oldest of `ahead` steps in flight has landed
     auto land = [&]() {
       --ahead;
       if (ahead >= 3)
-        wait_copies<(RING > 3 ? 3 : 0) * C::kLoads>();
+        wait_copies<(C::kAhead >= 3 ? 3 : 0) * C::kLoads>();
       else if (ahead == 2)
-        wait_copies<(RING > 2 ? 2 : 0) * C::kLoads>();
+        wait_copies<(C::kAhead >= 2 ? 2 : 0) * C::kLoads>();
       else if (ahead == 1)
-        wait_copies<C::kLoads>();
+        wait_copies<(C::kAhead >= 2 || R == 1 ? 1 : 0) * C::kLoads>();
       else
         wait_copies<0>();
     };
     // the ring's first copies leave before the queries are read, so that the
     // wait for the queries does not hold them up
 #pragma unroll 1
-    for (int i = 0; i < RING - 1; ++i)
+    for (int i = 0; i < C::kAhead; ++i)
       if (next < tiles) fetch();
 
     const int rows = req.n * a.group, r0 = rt * ROWS, last = min(r0 + ROWS, rows) - 1;
@@ -367,25 +372,25 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     };
 
 #pragma unroll 1
-    for (int i = first * S + stream; i - stream < tiles; i += S) {
-      lds_byte* const tile = own + slot_out * T::kBytes;
+    for (int i = first * STEP + stream * N; i - stream * N < tiles; i += STEP) {
+      lds_byte* const tile = own + slot_out * (N * T::kBytes);
       if constexpr (R == 1) {
         if (i >= tiles) break;
         if (next < tiles) {
           fetch();
           --ahead;
-          wait_copies<(RING - 1) * C::kLoads>();
+          wait_copies<C::kAhead * C::kLoads>();
         } else {
           land();
         }
         if ((i < range.whole_lo || i >= range.whole_hi) && note(tile, tile_of(span, i) * 32))
           clear_odd_values<D>(tile, 0, 1, lane);
       } else {
-        // every wave's copies of this tile have landed, and every wave is done
-        // with the tile before it, whose place the next copies take
+        // every wave's copies of this step have landed, and every wave is done
+        // with the step before it, whose place the next copies take
         if (next < tiles) {
           --ahead;
-          wait_copies<(RING - 2) * C::kLoads>();
+          wait_copies<(C::kAhead - 1) * C::kLoads>();
           asm volatile("s_barrier" ::: "memory");
           fetch();
         } else {
@@ -394,35 +399,48 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         }
         // some stream's tile is not seen whole by all rows: all waves come to
         // the barriers
-        if (i - stream < range.whole_lo || i - stream + S > range.whole_hi) {
-          const bool odd = i < tiles && note(tile, tile_of(span, i) * 32);
+        if (i - stream * N < range.whole_lo || i - stream * N + STEP > range.whole_hi) {
+          bool odd[N] = {};
+          if (i < tiles) {
+#pragma unroll
+            for (int x = 0; x < N; ++x) odd[x] = note(tile + x * T::kBytes, tile_of(span, i + x) * 32);
+          }
           __syncthreads();
-          if (odd) clear_odd_values<D>(tile, rg, R, lane);
+#pragma unroll
+          for (int x = 0; x < N; ++x)
+            if (odd[x]) clear_odd_values<D>(tile + x * T::kBytes, rg, R, lane);
           __syncthreads();
         }
         if (i >= tiles) continue;
       }
-      slot_out = slot_out + 1 == RING ? 0 : slot_out + 1;
-      if (R > 1 && (i >= mine_range.some_hi || (i < mine_range.some_lo && i >= mine_range.sink_hi)))
+      slot_out = slot_out + 1 == RING / N ? 0 : slot_out + 1;
+      if (R > 1 && (i >= mine_range.some_hi || (i + N <= mine_range.some_lo && i >= mine_range.sink_hi)))
         continue;  // none of this wave's rows sees it
-      v16f s = scores<D>(tile, k0_off, Q);
+      v16f s[N];
+#pragma unroll
+      for (int x = 0; x < N; ++x) s[x] = scores<D>(tile + x * T::kBytes, k0_off, Q);
       ValueFrags v = read_values<D>(tile, v0_off, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < mine_range.whole_lo || i >= mine_range.whole_hi) {
-        const int key = tile_of(span, i) * 32;
+      if (i < mine_range.whole_lo || i + N > mine_range.whole_hi) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[j] = -INFINITY;
+        for (int x = 0; x < N; ++x) {
+          const int key = tile_of(span, i + x) * 32;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[x][j] = -INFINITY;
+        }
       }
-      v8s p[2];
-      softmax_step<D>(s, st, p, a.scale_log2);
+      v8s p[N][2];
+      softmax_step<D, N>(s, st, p, a.scale_log2);
+      constexpr int PAIRS = D / 64;
 #pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
+      for (int x = 0; x < N * PAIRS; ++x) {
         // the next fragments are read under these products
         ValueFrags after;
-        if (x + 1 < D / 64) after = read_values<D>(tile, v0_off, x + 1);
+        if (x + 1 < N * PAIRS)
+          after = read_values<D>(tile + (x + 1) / PAIRS * T::kBytes, v0_off, (x + 1) % PAIRS);
         __builtin_amdgcn_sched_barrier(0);
-        add_values<D>(v, x, st, p);
+        add_values<D>(v, x % PAIRS, st, p[x / PAIRS]);
         v = after;
       }
     }
@@ -536,7 +554,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 // (request, row tile, key head).
 template <int D, int R>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int workers, int row_groups) {
-  constexpr int S = Shape<D, R>::S, ROWS = Shape<D, R>::kRows, PER = 1024 / D;
+  constexpr int STEP = Shape<D, R>::kStep, ROWS = Shape<D, R>::kRows, PER = 1024 / D;
   const int b = blockIdx.z, rt = blockIdx.x, h = blockIdx.y / row_groups, group = blockIdx.y - h * row_groups;
   const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
   const int rows = req.n * a.group, r0 = rt * ROWS;
@@ -552,8 +570,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
     const int total = a.plan[a.requests];
     const int share = max(a.min_share, (total + workers - 1) / workers);
     int from = from0;
-    for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, S) * a.kv_heads;
-    const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, S);
+    for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, STEP) * a.kv_heads;
+    const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, STEP);
     from += h * seg;
     g0 = from / share;
     g1 = (from + seg - 1) / share;
@@ -601,7 +619,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
   const int64_t row_tiles = (rows + ROWS - 1) / ROWS;
   const int64_t segments = a.requests * row_tiles * a.kv_heads;
-  const int64_t seg_most = (a.max_kv + 32 * C::S - 1) / (32 * C::S) + 1;
+  const int64_t seg_most = (a.max_kv + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
   // one launch where there is little to split, or enough segments to fill the
   // chip several times over
   if (seg_most <= 4 || segments >= (R >= 4 ? 2 : 8) * (int64_t)cus)
