@@ -364,3 +364,71 @@ def test_refusals():
     # tensors of no token at all
     out = s.op.run(s.q[:0], s.k_cache, s.v_cache, s.table, s.kv_len, torch.zeros_like(s.q_start))
     assert out.shape == (0, 8, 128)
+
+
+def _ragged(n, least, most, seed):
+    rng = np.random.default_rng(seed)
+    return np.exp(rng.uniform(np.log(least), np.log(most + 1), n)).astype(int).clip(least, most).tolist()
+
+
+# heads, dim, page, dtype, new, kv, window, sinks: the ways to divide the work among workgroups
+PLANS = {
+    # more requests than lanes, equal shares that end inside segments
+    "shares of 70 requests": ((8, 2), 128, 16, "bf16", [1] * 70, [0, 1] + _ragged(68, 3, 1500, 1), 0, 0),
+    "shares of 70 requests, window": ((8, 2), 64, 16, "bf16", [1, 2] * 35, _ragged(70, 2, 1500, 2), 300, 5),
+    "shares of 70 blocks": ((8, 2), 128, 16, "bf16", [16, 0, 9, 1, 12] * 14, _ragged(70, 16, 900, 3), 0, 0),
+    "shares of 20 requests": ((32, 8), 128, 32, "bf16", [1] * 20, _ragged(20, 1, 2500, 4), 0, 0),
+    "shares of 20 blocks": ((32, 8), 128, 16, "bf16", [16, 3] * 10, _ragged(20, 16, 900, 5), 0, 0),
+    "shares of 20 wide blocks": ((64, 8), 128, 64, "bf16", [16, 9] * 10, _ragged(20, 16, 900, 6), 400, 4),
+    "shares of 20 wide blocks, 64": ((64, 8), 64, 64, "bf16", [16, 9] * 10, _ragged(20, 16, 900, 6), 0, 0),
+    "shares of 30 blocks, 256": ((24, 8), 256, 16, "bf16", [16, 2, 1] * 10, _ragged(30, 16, 500, 7), 0, 0),
+    # each segment cut into pieces of its own
+    "pieces of one request": ((8, 2), 128, 16, "bf16", [1], [6001], 0, 0),
+    "pieces of ragged requests": ((8, 2), 64, 16, "bf16", [1, 1, 0, 1, 1], [3, 5000, 70, 0, 900], 0, 0),
+    "pieces of blocks": ((32, 8), 128, 16, "bf16", [16, 1, 16], [2500, 2000, 31], 0, 0),
+    "pieces of wide blocks, window": ((64, 8), 128, 16, "bf16", [16, 4], [5000, 2111], 1500, 40),
+    "pieces, 256": ((16, 2), 256, 64, "bf16", [1, 3], [3000, 700], 0, 0),
+    "pieces of blocks, 256": ((16, 2), 256, 64, "bf16", [16, 3], [3000, 700], 900, 3),
+    # prompts: shares of row tiles, and a workgroup for each
+    "shares of a prompt": ((8, 2), 128, 16, "bf16", [333], [1700], 0, 0),
+    "shares of prompts, window": ((8, 2), 64, 16, "bf16", [333, 20, 0, 270], [1700, 900, 4, 290], 200, 7),
+    "shares of 70 prompts": ((8, 2), 64, 16, "bf16", [40, 0, 90, 1, 33] * 14, _ragged(70, 90, 400, 8), 0, 0),
+    "a workgroup a row tile": ((8, 2), 64, 16, "bf16", [400] * 40, _ragged(40, 400, 700, 9), 0, 0),
+    "a workgroup a row tile, window": ((8, 2), 128, 16, "bf16", [400] * 40, _ragged(40, 400, 700, 10), 100, 35),
+    # fp32, keys dealt to several workgroups
+    "fp32 parts": ((8, 2), 64, 16, "fp32", [7, 1, 0, 16], [2100, 900, 4, 17], 0, 0),
+    "fp32 parts, window": ((8, 2), 128, 16, "fp32", [3, 1, 2], [2100, 900, 1], 700, 3),
+    "fp32 parts, 256": ((4, 2), 256, 16, "fp32", [3, 1], [1100, 0], 0, 0),
+}
+
+
+@pytest.mark.parametrize("plan", PLANS)
+def test_division_of_work(plan):
+    heads, dim, page, dtype, new, kv, window, sinks = PLANS[plan]
+    log(f"[gpu-test] attention {plan}")
+    s = Setup(heads, dim, page, dtype, new, kv, seed=len(plan))
+    s.check(*s.run(window=window, sinks=sinks, max_new=max(new), max_kv=max(kv)), window, sinks)
+
+
+@pytest.mark.parametrize("heads,new,kv", [((8, 2), 1, 3000), ((8, 2), 16, 3000), ((16, 2), 16, 3000),
+                                          ((8, 2), 200, 1500)])
+def test_odd_values_in_every_division(heads, new, kv):
+    """Infinities and NaN among values that all tokens see reach the result; those past a token's position
+    do not, wherever the keys are divided."""
+    import torch
+    log(f"[gpu-test] attention odd values {heads} {new} {kv}")
+    s = Setup(heads, 128, 16, "bf16", [new], [kv], seed=15)
+    for pos, i, x in ((5, 0, float("inf")), (kv // 2, 1, float("-inf")), (kv - new, 2, float("nan")),
+                      (kv - 1, 3, float("inf")), (7, 4, float("inf")), (kv // 2 + 1, 4, float("-inf"))):
+        s.v_cache[s.table[0, pos // 16].long(), :, pos % 16, i] = x
+        s.values[0][pos, :, i] = 0
+    out, lse = s.run(max_new=new, max_kv=kv)
+    torch.cuda.synchronize()
+    o = out.float()
+    assert (o[:, :, 0] == float("inf")).all() and (o[:, :, 1] == float("-inf")).all()
+    assert torch.isnan(o[:, :, 2]).all() and torch.isnan(o[:, :, 4]).all()
+    assert (o[-1, :, 3] == float("inf")).all() and torch.isfinite(o[:-1, :, 3]).all()
+    a, _, c, reach = ref.attention(*(x.float().cpu().numpy() for x in (s.q, s.keys[0], s.values[0])), kv, 0, 0)
+    tol, _ = ref.attention_bounds(a, c, reach, kv, s.dim, True)
+    err = np.abs(o.cpu().numpy() - a)
+    assert np.all((err <= tol)[:, :, 5:]) and np.all((err <= tol)[:-1, :, 3])
