@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Four waves share a tile of 16 rows and take 16-key tiles in turn, each with
 // its own running maximum and sum; the four are joined in LDS at the end.
 // Where few row tiles would leave the chip idle, the keys of each are dealt to
-// several workgroups, whose outputs a second launch joins.
+// several workgroups, the last of which joins their outputs.
 // The scores are computed transposed (keys x rows), so the row's maximum and
 // sum stay in the row's lanes and the accumulator registers of the scores are
 // the second product's operand as they are: lane (n = l % 16, q = l / 16)
@@ -61,6 +61,35 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // element 16 c + 4 q + i, and output row m of accumulator (blk, j) is element
 // 64 blk + 4 m + j.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// Parts of an output pass between workgroups of one launch on any XCD: written
+// through to and read from where all see them, 8 bytes at a time.  A fence in
+// their place writes a whole L2 back (a block of 3 requests 27.5 us against
+// 10.8), a second launch for the join takes 12.6.
+__device__ __forceinline__ void share2(float* p, float x, float y) {
+  const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 shared2(const float* p) {
+  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float4 shared4(const float* p) {
+  const float2 a = shared2(p), b = shared2(p + 2);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+// Called by all threads of a workgroup after they shared a part of a segment:
+// whether it was the last of `parts`, in which case all of them can be read.
+__device__ __forceinline__ bool last_of(int32_t* arrived, int parts, int* s_last) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's are where all see them
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    if (*s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *s_last;
+}
 
 template <int D>
 __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a, int splits) {
@@ -185,71 +214,68 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a, int split
           make_float4(O[x][0][e], O[x][1][e], O[x][2][e], O[x][3][e]);
   __syncthreads();
   const bool spoilt = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
-  for (int i = threadIdx.x; i < ROWS * D; i += 256) {
-    const int rr = i / D, d = i - rr * D;
+  const int64_t part = ((int64_t)b * a.kv_heads + h) * gridDim.x + blockIdx.x;
+  for (int i = threadIdx.x; i < ROWS * D / 2; i += 256) {  // two elements of a row
+    const int rr = i / (D / 2), d = 2 * (i - rr * (D / 2));
     if (r0 + rr > last) break;
     float top = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 4; ++x) top = fmaxf(top, s_m[x][rr]);
     const float ref = top == -INFINITY ? 0.f : top;
-    float num = 0.f, den = 0.f;
+    float2 num = make_float2(0.f, 0.f);
+    float den = 0.f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const float f = exp2f((s_m[x][rr] - ref) * a.scale_log2);
       den += f * s_l[x][rr];
       // a wave that saw no key of this row holds only zeros
-      if (s_m[x][rr] != -INFINITY) num += f * s_o[x][rr][d];
+      if (s_m[x][rr] != -INFINITY) {
+        num.x += f * s_o[x][rr][d];
+        num.y += f * s_o[x][rr][d + 1];
+      }
     }
     if (spoilt) den = NAN;
     if (splits > 1) {
-      const int64_t part = ((int64_t)b * a.kv_heads + h) * gridDim.x + blockIdx.x;
-      a.part_o[(part * ROWS + rr) * D + d] = num;
-      if (d == 0) {
-        a.part_ml[(part * ROWS + rr) * 2] = top;
-        a.part_ml[(part * ROWS + rr) * 2 + 1] = den;
-      }
+      share2(a.part_o + (part * ROWS + rr) * D + d, num.x, num.y);
+      if (d == 0) share2(a.part_ml + (part * ROWS + rr) * 2, top, den);
       continue;
     }
-    const float o = den == 0.f && top == -INFINITY ? 0.f : num / den;
+    const bool none = den == 0.f && top == -INFINITY;
     const int tk = (r0 + rr) / a.group, hd = h * a.group + (r0 + rr) - tk * a.group;
-    ((float*)a.out)[(req.q0 + tk) * a.o_tok + hd * a.o_head + d] = o;
+    *(float2*)((float*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + d) =
+        none ? make_float2(0.f, 0.f) : make_float2(num.x / den, num.y / den);
     if (d == 0 && a.lse)
-      a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] =
-          den == 0.f && top == -INFINITY ? -INFINITY : top * a.scale + logf(den);
+      a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] = none ? -INFINITY : top * a.scale + logf(den);
   }
-}
+  if (splits == 1) return;
 
-// Joins the parts of each row: a thread takes four elements of one.
-template <int D>
-__global__ __launch_bounds__(256) void join_f32_kernel(AttendArgs a, int splits, int row_tiles) {
-  constexpr int ROWS = 16;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
-  const int i = blockIdx.x * 256 + threadIdx.x, r = i / (D / 4), piece = i - r * (D / 4);
-  if (r >= req.n * a.group) return;
-  const int tile = r / ROWS, row = r - tile * ROWS;
-  const int64_t first = (((int64_t)b * a.kv_heads + h) * row_tiles + tile) * splits;
-  float top = -INFINITY, den = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the last of the row tile's workgroups joins its parts, in their order
+  __shared__ int s_last;
+  if (!last_of(a.arrived + (part - split) / splits, splits, &s_last)) return;
+  for (int i = threadIdx.x; i < (last - r0 + 1) * (D / 4); i += 256) {
+    const int rr = i / (D / 4), piece = i - rr * (D / 4);
+    float top = -INFINITY, den = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = *(const float2*)(a.part_ml + ((first + s) * ROWS + row) * 2);
-    const float4 y = load4(a.part_o + ((first + s) * ROWS + row) * D + 4 * piece);
-    const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-    const float fo = exp2f((top - ref) * a.scale_log2), fn = exp2f((ml.x - ref) * a.scale_log2);
-    den = den * fo + ml.y * fn;
-    o.x = scaled(o.x, fo) + scaled(y.x, fn);
-    o.y = scaled(o.y, fo) + scaled(y.y, fn);
-    o.z = scaled(o.z, fo) + scaled(y.z, fn);
-    o.w = scaled(o.w, fo) + scaled(y.w, fn);
-    top = mn;
+    for (int64_t g = part - split; g < part - split + splits; ++g) {
+      const float2 ml = shared2(a.part_ml + (g * ROWS + rr) * 2);
+      const float4 y = shared4(a.part_o + (g * ROWS + rr) * D + 4 * piece);
+      const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+      const float fo = exp2f((top - ref) * a.scale_log2), fn = exp2f((ml.x - ref) * a.scale_log2);
+      den = den * fo + ml.y * fn;
+      o.x = scaled(o.x, fo) + scaled(y.x, fn);
+      o.y = scaled(o.y, fo) + scaled(y.y, fn);
+      o.z = scaled(o.z, fo) + scaled(y.z, fn);
+      o.w = scaled(o.w, fo) + scaled(y.w, fn);
+      top = mn;
+    }
+    const bool none = den == 0.f && top == -INFINITY;
+    const int tk = (r0 + rr) / a.group, hd = h * a.group + (r0 + rr) - tk * a.group;
+    *(float4*)((float*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + 4 * piece) =
+        none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / den, o.y / den, o.z / den, o.w / den);
+    if (piece == 0 && a.lse)
+      a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] = none ? -INFINITY : top * a.scale + logf(den);
   }
-  const bool none = den == 0.f && top == -INFINITY;
-  const int tk = r / a.group, hd = h * a.group + r - tk * a.group;
-  *(float4*)((float*)a.out + (req.q0 + tk) * a.o_tok + hd * a.o_head + 4 * piece) =
-      none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x / den, o.y / den, o.z / den, o.w / den);
-  if (piece == 0 && a.lse)
-    a.lse[(int64_t)(req.q0 + tk) * a.q_heads + hd] = none ? -INFINITY : top * a.scale + logf(den);
 }
 
 // workspace of split fp32 attention: 2 parts of 16 rows to a CU
@@ -260,7 +286,8 @@ struct domino_attention : HandleBase {
   domino_attention_config_t cfg;
   int cus = 256;
   float* part = nullptr;    // split segments: outputs, then (m, l)
-  int32_t* plan = nullptr;  // running sum of the requests' steps
+  int32_t* plan = nullptr;     // bf16: running sum of the requests' steps
+  int32_t* arrived = nullptr;  // fp32: parts there are of each row tile and key head, 0 between calls
 };
 
 static thread_local char t_err[256] = "";
@@ -302,7 +329,10 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
                                                         : attend_f32_floats(cfg->head_dim, h->cus);
   h->part = (float*)h->take(floats * sizeof(float));
   h->plan = (int32_t*)h->take((size_t)(cfg->max_requests + 1) * sizeof(int32_t));
-  if (!h->part || !h->plan) {
+  h->arrived = (int32_t*)h->take((size_t)h->cus * sizeof(int32_t));
+  if (!h->part || !h->plan || !h->arrived || hipMemset(h->arrived, 0, (size_t)h->cus * sizeof(int32_t)) != hipSuccess ||
+      hipDeviceSynchronize() != hipSuccess) {
+    (void)hipGetLastError();
     h->release();
     delete h;
     return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: workspace allocation failed");
@@ -425,9 +455,6 @@ static void launch_attend_f32(const AttendArgs& a, int cus, hipStream_t st) {
   if (splits < 1) splits = 1;
   hipLaunchKernelGGL((attend_f32_kernel<D>), dim3((unsigned)(tiles * splits), a.kv_heads, a.requests), dim3(256), 0, st,
                      a, (int)splits);
-  if (splits > 1)
-    hipLaunchKernelGGL((join_f32_kernel<D>), dim3((unsigned)((rows * (D / 4) + 255) / 256), a.kv_heads, a.requests),
-                       dim3(256), 0, st, a, (int)splits, (int)tiles);
 }
 
 extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t* c,
@@ -498,6 +525,7 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
   } else {
     a.part_o = h->part;
     a.part_ml = h->part + attend_f32_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;
+    a.arrived = h->arrived;
     if (f.head_dim == 64)
       launch_attend_f32<64>(a, h->cus, (hipStream_t)stream);
     else if (f.head_dim == 128)

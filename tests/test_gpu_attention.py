@@ -432,3 +432,33 @@ def test_odd_values_in_every_division(heads, new, kv):
     tol, _ = ref.attention_bounds(a, c, reach, kv, s.dim, True)
     err = np.abs(o.cpu().numpy() - a)
     assert np.all((err <= tol)[:, :, 5:]) and np.all((err <= tol)[:-1, :, 3])
+
+
+def test_fp32_parts_give_the_same_bits_again():
+    """Whichever workgroup comes last joins the parts in their order: the same bits each time, on replays of a
+    graph with other lengths in between, and for a smaller call after a larger one."""
+    import torch
+    log("[gpu-test] attention fp32 parts again")
+    s = Setup((8, 2), 64, 16, "fp32", [7, 1, 16], [2100, 900, 333], seed=16)
+    kw = dict(max_new=16, max_kv=2100)
+    want, want_l = s.run(**kw)
+    s.check(want, want_l)
+    held = torch.empty_like(s.q)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        s.op.run(s.q, s.k_cache, s.v_cache, s.table, s.kv_len, s.q_start, out=held, **kw)
+    full = s.kv_len.clone()
+    for i in range(4):
+        held.zero_()
+        g.replay()
+        assert torch.equal(held, want)
+        s.kv_len -= 100 + i
+        g.replay()
+        got = held.clone()
+        eager, _ = s.run(**kw)
+        assert torch.equal(got, eager)
+        s.kv_len.copy_(full)
+        out, lse = s.run(**kw)
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+        torch.cuda.synchronize()
