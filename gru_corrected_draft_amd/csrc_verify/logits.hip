@@ -167,9 +167,18 @@ __device__ __forceinline__ float tame(float x) {
   return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);
 }
 
+// all ones or none, as bit j of x.  Hidden from the compiler, which otherwise
+// tests the bit once more for what the ones keep (five instructions for a masked
+// logit in place of two).
+__device__ __forceinline__ uint32_t spread(uint32_t x, int j) {
+  uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)x, j, 1);
+  asm("" : "+v"(m));
+  return m;
+}
+
 // -inf where bit j of `out` is set
 __device__ __forceinline__ float masked(float x, uint32_t out, int j) {
-  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)out, j, 1);  // all ones or none
+  const uint32_t m = spread(out, j);
   return __uint_as_float((m & 0xFF800000u) | (~m & __float_as_uint(x)));
 }
 
@@ -433,7 +442,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
         hi = mid;
     }
   }
-  constexpr int AHEAD = 4;  // loads in flight for a lane
+  constexpr int AHEAD = VERIFY && TOUCH ? 3 : 4;  // loads in flight for a lane
   for (int row = slot; row < rows; row += a.row_slots) {
     const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
     const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
@@ -455,7 +464,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
           const int i = i0 + u * 64 * V;
-          out[u] = mask ? ~(mask[i / 32] >> (i % 32)) : 0u;
+          out[u] = mask ? ~(mask[(uint32_t)i >> 5] >> (i & 31)) : 0u;
         }
       } else {
 #pragma unroll
@@ -463,7 +472,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           const int i = i0 + u * 64 * V;
           if (i < end) {
             raw[u] = load_raw<T>(src + i, ids - i);
-            out[u] = mask ? ~(mask[i / 32] >> (i % 32)) : 0u;
+            out[u] = mask ? ~(mask[(uint32_t)i >> 5] >> (i & 31)) : 0u;
           }
         }
       }
@@ -473,7 +482,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
         if (i >= end) break;
         if constexpr (!VERIFY) {
           if (TOUCH) {
-            uint32_t hit = t.bits[i / 32] >> (i % 32) & ~out[u] & ((1u << V) - 1);
+            uint32_t hit = t.bits[(uint32_t)i >> 5] >> (i & 31) & ~out[u] & ((1u << V) - 1);
             while (hit) {
               const int j = __builtin_ctz(hit), off = i + j;
               hit &= hit - 1;
@@ -485,8 +494,8 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               if constexpr (sizeof(T) == 2) {
-                const uint32_t lo_ = (uint32_t)__builtin_amdgcn_sbfe((int)out[u], 2 * w, 1) & 0xFFFFu;
-                const uint32_t hi_ = (uint32_t)__builtin_amdgcn_sbfe((int)out[u], 2 * w + 1, 1) << 16;
+                const uint32_t lo_ = spread(out[u], 2 * w) & 0xFFFFu;
+                const uint32_t hi_ = spread(out[u], 2 * w + 1) << 16;
                 const uint32_t m = lo_ | hi_;
                 raw[u][w] = (m & 0xFF80FF80u) | (~m & raw[u][w]);
               } else {
@@ -508,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
           }
         } else {
           uint32_t touched = 0;
-          if (TOUCH) touched = t.bits[i / 32] >> (i % 32);
+          if (TOUCH) touched = t.bits[(uint32_t)i >> 5] >> (i & 31);
           float x[V];
           unpack<T>(raw[u], x);
           if ((out[u] | touched) & ((1u << V) - 1)) {
