@@ -57,12 +57,60 @@ __device__ __forceinline__ KeySpan row_tile_span(const AttendArgs& a, const Requ
   return key_span<32>(r, r0 / a.group, last / a.group, a.window, a.sinks);
 }
 
-// steps of a request
+// steps of row tile rt of a request, none past its rows
+template <int ROWS, int STEP>
+__device__ __forceinline__ int tile_steps(const AttendArgs& a, const Request& r, int rt) {
+  return rt * ROWS < r.n * a.group ? steps_of(row_tile_span<ROWS>(a, r, rt).count, STEP) : 0;
+}
+
+// steps of a request, by each lane for a request of its own
 template <int ROWS, int STEP>
 __device__ __forceinline__ int request_steps(const AttendArgs& a, const Request& r) {
   int n = 0;
-  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += steps_of(row_tile_span<ROWS>(a, r, rt).count, STEP);
+  for (int rt = 0; rt * ROWS < r.n * a.group; ++rt) n += tile_steps<ROWS, STEP>(a, r, rt);
   return n * a.kv_heads;
+}
+
+__device__ __forceinline__ int scan_lanes(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Row tile of step `off` of a request's, which becomes the step among the row
+// tile's, by a wave for one request: a lane to each row tile.  With `off` past
+// the last, off is less by all there are.  A prompt of 2048 tokens has 32 row
+// tiles, and gone through one by one they were a third of its time.
+template <int ROWS, int STEP>
+__device__ __forceinline__ int find_row_tile(const AttendArgs& a, const Request& r, int& off, int lane) {
+  const int row_tiles = (r.n * a.group + ROWS - 1) / ROWS;
+#pragma unroll 1
+  for (int rt = 0; rt < row_tiles; rt += 64) {
+    const int upto = scan_lanes(tile_steps<ROWS, STEP>(a, r, rt + lane), lane) * a.kv_heads;
+    const uint64_t past = __ballot(upto > off);
+    const int x = past ? __builtin_ctzll(past) : 64;
+    if (x) off -= __builtin_amdgcn_readlane(upto, x - 1);
+    if (past) return rt + x;
+  }
+  return row_tiles;
+}
+
+// the same number from the row tile: steps of a request's first rt row tiles
+template <int ROWS, int STEP>
+__device__ __forceinline__ int steps_before(const AttendArgs& a, const Request& r, int rt, int lane) {
+  int n = 0;
+#pragma unroll 1
+  for (int x = 0; x < rt; x += 64)
+    n += __builtin_amdgcn_readlane(scan_lanes(x + lane < rt ? tile_steps<ROWS, STEP>(a, r, x + lane) : 0, lane), 63);
+  return n * a.kv_heads;
+}
+
+__device__ __forceinline__ Request of_lane(const Request& r, int lane) {
+  return Request{__builtin_amdgcn_readlane(r.q0, lane), __builtin_amdgcn_readlane(r.n, lane),
+                 __builtin_amdgcn_readlane(r.kv, lane), (bool)__builtin_amdgcn_readlane((int)r.bad, lane)};
 }
 
 template <int D, int R, bool WHOLE>
@@ -89,7 +137,15 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     int total;
     if (few) {
       if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
-      upto = lane < a.requests ? request_steps<ROWS, STEP>(a, mine) : 0;
+      if (a.row_tiles <= 2) {
+        upto = lane < a.requests ? request_steps<ROWS, STEP>(a, mine) : 0;
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < a.requests; ++x) {
+          const int n = steps_before<ROWS, STEP>(a, of_lane(mine, x), a.row_tiles, lane);
+          if (lane == x) upto = n;
+        }
+      }
       if (a.pieces) {
         // The shortest piece at which there are workgroups for all, each lane
         // trying one between an even share and twice that, where there are.
@@ -106,11 +162,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         mine_pieces = (steps + piece - 1) / piece;
         upto = mine_pieces * a.kv_heads;
       }
-  #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(upto, d, 64);
-        if (lane >= d) upto += y;
-      }
+      upto = scan_lanes(upto, lane);
       total = __builtin_amdgcn_readlane(upto, 63);
     } else {
       int* const s_pre = (int*)ring;
@@ -120,11 +172,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         int x = b < a.requests
                     ? request_steps<ROWS, STEP>(a, request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv))
                     : 0;
-  #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const int y = __shfl_up(x, d, 64);
-          if (lane >= d) x += y;
-        }
+        x = scan_lanes(x, lane);
         if (lane == 63) s_sum[w] = x;
         __syncthreads();
         for (int i = 0; i < w; ++i) x += s_sum[i];
@@ -201,10 +249,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       if (few) {
         b = __builtin_ctzll(__ballot(upto > at));
         begin = b ? __builtin_amdgcn_readlane(upto, b - 1) : 0;
-        req.q0 = __builtin_amdgcn_readlane(mine.q0, b);
-        req.n = __builtin_amdgcn_readlane(mine.n, b);
-        req.kv = __builtin_amdgcn_readlane(mine.kv, b);
-        req.bad = __builtin_amdgcn_readlane((int)mine.bad, b);
+        req = of_lane(mine, b);
       } else {
         for (;;) {  // requests without rows have no steps
           req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
@@ -215,7 +260,8 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         }
       }
       int off = at - begin;
-      span = row_tile_span<ROWS>(a, req, 0);
+      if (!a.pieces && a.row_tiles > 1) rt = find_row_tile<ROWS, STEP>(a, req, off, lane);
+      span = row_tile_span<ROWS>(a, req, rt);
       seg = steps_of(span.count, STEP);
       if (a.pieces) {
         const int pieces = __builtin_amdgcn_readlane(mine_pieces, b);
@@ -224,11 +270,6 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         first = uniform((int)((int64_t)seg * x / pieces));
         stop = uniform((int)((int64_t)seg * (x + 1) / pieces));
       } else {
-        while (uniform(off >= seg * a.kv_heads)) {
-          off -= seg * a.kv_heads;
-          span = row_tile_span<ROWS>(a, req, ++rt);
-          seg = steps_of(span.count, STEP);
-        }
         h = off / seg;
         first = off - h * seg;
         stop = min(seg, first + end - at);
@@ -559,7 +600,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
   const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
   const int rows = req.n * a.group, r0 = rt * ROWS;
   const int row = group * PER + threadIdx.x / (D / 4), piece = threadIdx.x % (D / 4);
-  if (r0 + row >= rows || row >= ROWS) return;
+  if (r0 >= rows || group * PER >= ROWS) return;
   const int from0 = a.plan[b];
   int g0, g1;
   if (a.pieces) {
@@ -569,14 +610,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
   } else {
     const int total = a.plan[a.requests];
     const int share = max(a.min_share, (total + workers - 1) / workers);
-    int from = from0;
-    for (int x = 0; x < rt; ++x) from += steps_of(row_tile_span<ROWS>(a, req, x).count, STEP) * a.kv_heads;
+    int from = from0 + steps_before<ROWS, STEP>(a, req, rt, threadIdx.x & 63);
     const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, STEP);
     from += h * seg;
     g0 = from / share;
     g1 = (from + seg - 1) / share;
   }
-  if (g0 == g1) return;
+  if (g0 == g1 || r0 + row >= rows) return;
   float top = -INFINITY, den = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -622,10 +662,11 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t seg_most = (a.max_kv + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
   // one launch where there is little to split, or enough segments to fill the
   // chip several times over
-  if (seg_most <= 4 || segments >= (R >= 4 ? 2 : 8) * (int64_t)cus)
+  if (seg_most <= 4 || segments >= (R == 8 ? 1 : R == 4 ? 2 : 8) * (int64_t)cus)
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
   const int workers = (int)(need < cus ? need : cus);
+  a.row_tiles = (int)row_tiles;
   a.pieces = row_tiles == 1 && a.requests <= 64 && 2 * segments <= workers;
   launch_kernel<D, R, false>(a, dim3(workers), st);
   const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
