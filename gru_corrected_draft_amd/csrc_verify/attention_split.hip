@@ -662,7 +662,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t seg_most = (a.max_kv + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
   // one launch where there is little to split, or enough segments to fill the
   // chip several times over
-  if (seg_most <= 4 || segments >= (R == 8 ? 1 : R == 4 ? 2 : 8) * (int64_t)cus)
+  if (seg_most <= 4 || segments >= (R == 8 || (D == 256 && R == 4) ? 1 : R == 4 ? 2 : 8) * (int64_t)cus)
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
   const int workers = (int)(need < cus ? need : cus);
