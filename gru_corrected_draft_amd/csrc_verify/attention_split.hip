@@ -659,10 +659,19 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
   const int64_t row_tiles = (rows + ROWS - 1) / ROWS;
   const int64_t segments = a.requests * row_tiles * a.kv_heads;
-  const int64_t seg_most = (a.max_kv + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
-  // one launch where there is little to split, or enough segments to fill the
-  // chip several times over
-  if (seg_most <= 4 || segments >= (R == 8 || (D == 256 && R == 4) ? 1 : R == 4 ? 2 : 8) * (int64_t)cus)
+  int64_t keys = a.max_kv;  // the most that a segment has
+  if (a.window && (int64_t)a.window + ROWS / a.group + a.sinks + 65 < keys)
+    keys = (int64_t)a.window + ROWS / a.group + a.sinks + 65;
+  const int64_t seg_most = (keys + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
+  // One launch where there is little to split, or enough segments to fill the
+  // chip several times over.  Prompts cost much to split (256 or 128 rows' sums
+  // go through memory, and a share that straddles segments starts anew), about
+  // 14 steps: undivided, one prompt of 512 tokens over 1024 keys (12.8 steps
+  // more than an even share) takes 41 us against 47, of 1000 over 1000 (8.5)
+  // 42 against 100, but of 512 over 2048 (24.8) 68 against 55.
+  const bool prompt = R == 8 || (D == 256 && R == 4);
+  if (seg_most <= 4 || (prompt ? seg_most * (cus - segments) <= 14 * (int64_t)cus
+                               : segments >= (R == 4 ? 2 : 8) * (int64_t)cus))
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
   const int workers = (int)(need < cus ? need : cus);
