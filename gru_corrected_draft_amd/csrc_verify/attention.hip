@@ -384,8 +384,11 @@ static bool rows_ok(const void* p, int64_t tok, int64_t head, int unit) {
   return !((uintptr_t)p & 15) && tok >= 0 && head >= 0 && tok % unit == 0 && head % unit == 0;
 }
 
+// Also 2^30, so that sums of positions, windows and tiles stay in 32 bits: no
+// cache in this memory holds so many keys of a request.
 static int32_t clip_kv(const domino_cache_t* c, int page_size) {
-  const int64_t most = (int64_t)c->table_width * page_size;
+  int64_t most = (int64_t)c->table_width * page_size;
+  if (most > 1 << 30) most = 1 << 30;
   return (int32_t)(c->max_kv < most ? c->max_kv : most);
 }
 

@@ -55,8 +55,8 @@ typedef struct domino_attention domino_attention_t;
  * p in row p % page_size of page page_table[b][p / page_size].
  *
  * A request is malformed if its rows are not within [0, tokens], it has more
- * than max_new new tokens, kv_len[b] is negative, or kv_len[b] exceeds max_kv
- * or what the table's width holds.  A position before 0 (fewer keys than new
+ * than max_new new tokens, kv_len[b] is negative, or kv_len[b] exceeds max_kv,
+ * what the table's width holds or 2^30.  A position before 0 (fewer keys than new
  * tokens) has no key; its token's attention is empty. */
 typedef struct {
   void* k_cache;
