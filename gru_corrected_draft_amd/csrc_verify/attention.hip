@@ -9,8 +9,10 @@
 
 // ---------------------------------------------------------------- append
 // A copy: one 16-byte piece per thread, keys in the first half of the grid's
-// y, values in the second.  Bound by the launch for a decoding step and by
-// memory for a prompt; rows of a head are contiguous on both sides.
+// y, values in the second.  Bound by the launch for a decoding step (2.1 us on
+// the GPU, 7 us from call to call) and by memory for a prompt: 8 requests of up
+// to 1024 tokens, 51.6 MB read and written, take 10.9 us, 4.7 TB/s of a large
+// copy's 5.2.  Rows of a head are contiguous on both sides.
 struct AppendArgs {
   const void* src[2];
   void* dst[2];
@@ -51,7 +53,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Four waves share a tile of 16 rows and take 16-key tiles in turn, each with
 // its own running maximum and sum; the four are joined in LDS at the end.
 // Where few row tiles would leave the chip idle, the keys of each are dealt to
-// several workgroups, the last of which joins their outputs.
+// several workgroups, the last of which joins their outputs: fp32 calls are
+// small checks, bound by the time from load to use (blocks of 7 tokens of 3
+// requests over up to 1001 keys 22 us undivided, 12.6 with a second launch, 10.8).
 // The scores are computed transposed (keys x rows), so the row's maximum and
 // sum stay in the row's lanes and the accumulator registers of the scores are
 // the second product's operand as they are: lane (n = l % 16, q = l / 16)
@@ -64,8 +68,7 @@ __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_ca
 
 // Parts of an output pass between workgroups of one launch on any XCD: written
 // through to and read from where all see them, 8 bytes at a time.  A fence in
-// their place writes a whole L2 back (a block of 3 requests 27.5 us against
-// 10.8), a second launch for the join takes 12.6.
+// their place writes a whole L2 back (27.5 us for those 10.8).
 __device__ __forceinline__ void share2(float* p, float x, float y) {
   const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
   __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

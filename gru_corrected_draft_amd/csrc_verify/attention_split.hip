@@ -2,36 +2,52 @@
 //
 // A workgroup takes R * 32 rows of one request and key head (a row tile) and S
 // streams of key tiles: wave w works for row group w / S on stream w % S, with
-// its own running maximum and sum.  The streams of a row group are joined in
-// LDS at the end.  One group of 32 rows to a wave keeps a wave's sums, queries
-// and scores in 256 registers; with more rows the sums move to accumulation
-// registers, and the moves cost more than the halved reads of LDS save.
+// its own running maximum and sum (softmax in one pass: sums against a maximum
+// m are rescaled by e^(m - m') when it becomes m').  The streams of a row group
+// are joined in LDS at the end.  One group of 32 rows to a wave keeps a wave's
+// sums, queries and scores in 256 registers; with more rows the sums move to
+// accumulation registers, and the moves cost more than the halved reads of LDS
+// save.
 //   R = 1: a wave copies its own tiles into its own ring and never waits for
 //          another; no barrier in the walk.  For few rows, bound by the
-//          cache's bytes.
+//          cache's bytes: 64 requests with one token each over 4 to 8 thousand
+//          keys take 281 us, 5.8 TB/s (a large copy reaches 5.2).
 //   R > 1: the R waves on a stream share its tiles, each copies a part, and a
-//          barrier separates the tiles.  R = 2 and 4 for up to 64 and 128 rows,
+//          barrier separates the steps.  R = 2 and 4 for up to 64 and 128 rows,
 //          so that a draft block of 16 positions with 4 or 8 heads to a key
-//          head reads its keys once; R = 8 for prompts, bound by the matrix
-//          cores.
+//          head reads its keys once: 8 requests over 2 to 4 thousand keys take
+//          35 us, 3.0 TB/s, of which 2.4 find the work, 4 fill the rings and 4.5
+//          join; 16 requests with a window of 4096 70 us, 3.9 TB/s.
+//   R = 8: for prompts; steps of 64 keys (234 us against 262 with 32 for 2
+//          requests of up to 2048 tokens over up to 5120 keys), 970 TFLOP/s
+//          (a large product 1390 to 1490).  Bound by issue: vector and matrix
+//          instructions are busy 41 and 40 % of the time and those of
+//          two waves of a SIMD overlap only in part (beside a wave of products
+//          alone, one of softmax alone takes 1.4 times as long).  Products of
+//          the next tile put between a tile's softmax (278 us against 262),
+//          waves half a step apart (269 against 242) and two workgroups of 4
+//          waves to a CU (243 against 234) were slower.
 //
 // Steps.  A segment is one (request, row tile, key head); it has one step for
-// each S key tiles, and at least one, so that rows without keys are written
-// too.  With WHOLE a workgroup takes one segment.  Otherwise the steps of all
-// segments in order are cut into equal shares, one for each workgroup,
+// each S (R = 8: 2) key tiles, and at least one, so that rows without keys are
+// written too.  With WHOLE a workgroup takes one segment.  Otherwise the steps of
+// all segments in order are cut into equal shares, one for each workgroup,
 // whatever the lengths of the requests: each workgroup sums up the lengths
 // itself.  A share ends at most two segments inside; those leave their
 // unnormalised output, maximum and sum in the workspace, and a second launch
-// joins them.  With no more segments than half the workgroups, each segment is
-// cut into pieces of its own instead, one to a workgroup: a share that straddles
-// two segments would pay for two starts and two ends (8 requests with 16 tokens
-// over 2 to 4 thousand keys took 35 us so).
+// joins them (the last workgroup of a segment in its place, without a launch but
+// alone with the loads: block of 8 requests 40 us against 35).  With no more
+// segments than half the workgroups, each segment is cut into pieces of its own
+// instead, one to a workgroup: a share that straddles two segments would pay for
+// two starts and two ends (block of 8 requests 42 us against 36).
 #include "attention_bf16.h"
 
 namespace {
 
 template <int D, int R>
 struct Shape {
+  // R = 2: 4 streams with rings of 2 take as long as 2 with rings of 4 (36.1 and
+  // 35.6 us, block of 8 requests)
   static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : R == 2 ? 2 : 8 / R);  // streams
   static constexpr int W = R * S;                                                // waves
   static constexpr int kThreads = 64 * W;
@@ -592,7 +608,8 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 }
 
 // Joins the parts of split segments: 256 threads take 1024 / D rows of one
-// (request, row tile, key head).
+// (request, row tile, key head).  4.5 us for 8 requests with 16 tokens, of which
+// the launch and the way to memory and back are most.
 template <int D, int R>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int workers, int row_groups) {
   constexpr int STEP = Shape<D, R>::kStep, ROWS = Shape<D, R>::kRows, PER = 1024 / D;
@@ -684,7 +701,8 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
 }
 
 // The fewest rows to a workgroup that hold a request's, so that its keys are
-// read once; beyond 128 rows the largest.
+// read once; beyond 128 rows the largest.  A wave costs the same whether its
+// rows are there or not.
 template <int D>
 void launch_d(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;

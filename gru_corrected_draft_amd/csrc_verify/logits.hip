@@ -13,7 +13,8 @@
 // of history took 212 us against 137.  Where they are not (bound by arithmetic),
 // the pass leaves touched ids out and each row takes them afterwards from a list,
 // a lane to each: taken in the pass, for a lane or two of a wave at a time, they
-// made 64 greedy blocks with that history take 188 us against 137.  Counting uses
+// made 64 greedy blocks with that history take 188 us against 137, which has
+// since come to 113.  Counting uses
 // integer atomics in LDS and the list is in the order of the ids, so nothing
 // depends on the order of arrival.
 #include <cmath>
@@ -364,7 +365,16 @@ __device__ __forceinline__ float touched_logit(float x, uint32_t c, uint32_t ent
 }
 
 // Reads logits once; writes them (process) or keeps each row's statistics
-// (verify).  Bound by memory at the larger sizes.
+// (verify): m and s = sum e^((x - m) / T), rescaled as m grows, and the largest
+// x - T ln E with its id, which falls on id v with the probability e^(x_v / T) /
+// sum e^(x / T).  Measured on 64 blocks of 16 rows of 151936 bf16 logits:
+//   process, history, biases, masks   156 us, 643 MB, 4.1 TB/s (a large copy
+//                                     5.2): memory
+//   verify, greedy, no rules          71 us, 311 MB, 4.4 TB/s
+//   verify, history, masks, T > 0     135 us: vector instructions, busy 81 % of
+//                                     the time; touched ids read again bring the
+//                                     bytes from 370 to 563 MB
+// and on one block of fp32 logits, where starting and joining are most, 13.7.
 template <typename T, bool VERIFY, bool TOUCH>
 __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   constexpr int V = Elem<T>::kVec;
@@ -442,7 +452,9 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
         hi = mid;
     }
   }
-  constexpr int AHEAD = VERIFY && TOUCH ? 3 : 4;  // loads in flight for a lane
+  // Loads in flight for a lane.  With touched ids to look after, a fourth spills
+  // registers, and 64 sampled blocks take 150 us against 131.
+  constexpr int AHEAD = VERIFY && TOUCH ? 3 : 4;
   for (int row = slot; row < rows; row += a.row_slots) {
     const T* src = (const T*)a.logits + b * a.req_stride + row * a.row_stride + lo;
     const uint32_t* mask = a.mask ? a.mask + b * a.mask_req + row * a.mask_row + lo / 32 : nullptr;
@@ -641,7 +653,10 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
 }
 
 // One workgroup per request joins the parts of its rows, walks the proposals
-// and writes the outputs.
+// and writes the outputs.  5 us, most of it the launch and two ways to memory
+// and back; done by the last workgroup of the launch before instead, it took
+// registers from the pass (64 blocks 155 us against 141, one block 15.0 against
+// 13.5).
 __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
   __shared__ float s_lse[kMaxRows], s_m[kMaxRows], s_best[kMaxRows];
   __shared__ int s_id[kMaxRows], s_stands[kMaxRows];
@@ -758,7 +773,8 @@ static int longest_range(size_t per_id) {
 // are taken in the pass, ranges differ in work and at least four rounds even
 // it out: 64 blocks of 151936 ids with 4096 tokens of history, 300 biases and
 // masks took 171 us in two rounds, 164 in three, 160 in four and six; the
-// verification of 64 blocks, whose start takes longer, 144, 144, 151 and 170.
+// verification of 64 blocks, whose start takes longer, 144, 144, 151 and 170
+// (135 since, in two).
 // requests * ranges is at most requests * (ranges of the longest) + 8 rounds.
 static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t per_id, bool touch, bool verify) {
   Cut k;
