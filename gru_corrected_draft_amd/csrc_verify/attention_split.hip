@@ -97,8 +97,7 @@ __device__ __forceinline__ int scan_lanes(int x, int lane) {
 }
 
 // Row tile of step `off` of a request's, which becomes the step among the row
-// tile's, by a wave for one request: a lane to each row tile.  With `off` past
-// the last, off is less by all there are.  A prompt of 2048 tokens has 32 row
+// tile's, by a wave for one request: a lane to each row tile.  A prompt of 2048 tokens has 32 row
 // tiles, and gone through one by one they were a third of its time.
 template <int ROWS, int STEP>
 __device__ __forceinline__ int find_row_tile(const AttendArgs& a, const Request& r, int& off, int lane) {
@@ -114,7 +113,7 @@ __device__ __forceinline__ int find_row_tile(const AttendArgs& a, const Request&
   return row_tiles;
 }
 
-// the same number from the row tile: steps of a request's first rt row tiles
+// steps of a request's first rt row tiles, in the same way
 template <int ROWS, int STEP>
 __device__ __forceinline__ int steps_before(const AttendArgs& a, const Request& r, int rt, int lane) {
   int n = 0;

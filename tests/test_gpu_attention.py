@@ -462,3 +462,24 @@ def test_fp32_parts_give_the_same_bits_again():
         out, lse = s.run(**kw)
         assert torch.equal(out, want) and torch.equal(lse, want_l)
         torch.cuda.synchronize()
+
+
+# prompts that are divided: many row tiles to a request, many requests, a window longer than a few steps
+PROMPTS = {
+    "75 row tiles": ((64, 1), 64, 16, "bf16", [300], [2000], 0, 0),
+    "75 row tiles of two requests": ((64, 1), 64, 16, "bf16", [300, 7], [3000, 100], 0, 0),
+    "70 requests": ((8, 2), 64, 16, "bf16", [40, 33] * 35, _ragged(70, 40, 2500, 11), 0, 0),
+    "window": ((8, 2), 64, 16, "bf16", [333, 270], [2600, 2900], 1500, 7),
+    "window, 128": ((8, 2), 128, 32, "bf16", [100, 0, 333], [2600, 5, 400], 1500, 70),
+    "heads of 256": ((6, 2), 256, 32, "bf16", [150, 40], [900, 700], 0, 0),
+    "heads of 256, window": ((6, 2), 256, 32, "bf16", [150], [1300], 700, 2),
+    "heads of 256, undivided": ((8, 8), 256, 16, "bf16", [140] * 5, _ragged(5, 140, 400, 12), 0, 0),
+}
+
+
+@pytest.mark.parametrize("prompt", PROMPTS)
+def test_divided_prompts(prompt):
+    heads, dim, page, dtype, new, kv, window, sinks = PROMPTS[prompt]
+    log(f"[gpu-test] attention prompt {prompt}")
+    s = Setup(heads, dim, page, dtype, new, kv, seed=100 + len(prompt))
+    s.check(*s.run(window=window, sinks=sinks, max_new=max(new), max_kv=max(kv)), window, sinks)
