@@ -42,7 +42,7 @@ struct AttendArgs {
   // split attention
   float* part_o;   // [slots][rows][head_dim]
   float* part_ml;  // [slots][rows][2]
-  int32_t* plan;   // bf16: [requests + 1]
+  int32_t* plan;   // bf16: [max(requests, 64) + 1]
   int32_t* arrived;  // fp32: [CUs] parts there are of a row tile and key head; 0 between calls
   int32_t min_share;
   int32_t row_tiles;  // of the longest request there can be

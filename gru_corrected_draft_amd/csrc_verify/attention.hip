@@ -289,7 +289,7 @@ struct domino_attention : HandleBase {
   domino_attention_config_t cfg;
   int cus = 256;
   float* part = nullptr;    // split segments: outputs, then (m, l)
-  int32_t* plan = nullptr;     // bf16: running sum of the requests' steps
+  int32_t* plan = nullptr;     // bf16: running sum of the requests' steps, or of 64 row tiles' pieces
   int32_t* arrived = nullptr;  // fp32: parts there are of each row tile and key head, 0 between calls
 };
 
@@ -331,7 +331,7 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   const size_t floats = cfg->dtype == DOMINO_DTYPE_BF16 ? attend_split_floats(cfg->head_dim, h->cus)
                                                         : attend_f32_floats(cfg->head_dim, h->cus);
   h->part = (float*)h->take(floats * sizeof(float));
-  h->plan = (int32_t*)h->take((size_t)(cfg->max_requests + 1) * sizeof(int32_t));
+  h->plan = (int32_t*)h->take((size_t)((cfg->max_requests < 64 ? 64 : cfg->max_requests) + 1) * sizeof(int32_t));
   h->arrived = (int32_t*)h->take((size_t)h->cus * sizeof(int32_t));
   if (!h->part || !h->plan || !h->arrived || hipMemset(h->arrived, 0, (size_t)h->cus * sizeof(int32_t)) != hipSuccess ||
       hipDeviceSynchronize() != hipSuccess) {

@@ -37,9 +37,11 @@
 // unnormalised output, maximum and sum in the workspace, and a second launch
 // joins them (the last workgroup of a segment in its place, without a launch but
 // alone with the loads: block of 8 requests 40 us against 35).  With no more
-// segments than half the workgroups, each segment is cut into pieces of its own
-// instead, one to a workgroup: a share that straddles two segments would pay for
-// two starts and two ends (block of 8 requests 42 us against 36).
+// segments than half the workgroups, of no more row tiles than a wave has lanes,
+// each segment is cut into pieces of its own instead, one to a workgroup: a share
+// that straddles two segments would pay for two starts and two ends (block of 8
+// requests 42 us against 36, one prompt of 512 tokens over 4096 keys 73 against
+// 64).
 #include "attention_bf16.h"
 
 namespace {
@@ -151,8 +153,12 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     // through LDS, over the rings.
     int total;
     if (few) {
-      if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
-      if (a.row_tiles <= 2) {
+      // (a lane to each request, or with pieces to each row tile of one)
+      const int own = a.pieces ? lane / a.row_tiles : lane;
+      if (own < a.requests) mine = request_of(a.q_start, a.kv_len, own, a.tokens, a.max_new, a.max_kv);
+      if (a.pieces) {
+        upto = own < a.requests ? tile_steps<ROWS, STEP>(a, mine, lane - own * a.row_tiles) * a.kv_heads : 0;
+      } else if (a.row_tiles <= 2) {
         upto = lane < a.requests ? request_steps<ROWS, STEP>(a, mine) : 0;
       } else {
 #pragma unroll 1
@@ -171,7 +177,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         const int steps = upto / a.kv_heads, size = even + lane + (int)((int64_t)even * lane / 63);
         int need = 0;
 #pragma unroll 1
-        for (int i = 0; i < a.requests; ++i) need += (__builtin_amdgcn_readlane(steps, i) + size - 1) / size;
+        for (int i = 0; i < a.requests * a.row_tiles; ++i) need += (__builtin_amdgcn_readlane(steps, i) + size - 1) / size;
         const uint64_t fits = __ballot(need * a.kv_heads <= (int)gridDim.x);
         const int piece = __builtin_amdgcn_readlane(size, fits ? __builtin_ctzll(fits) : 63);
         mine_pieces = (steps + piece - 1) / piece;
@@ -207,7 +213,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
     if (blockIdx.x == 0) {  // for the join
       if (few) {
         if (w == 0 && lane == 0) a.plan[0] = 0;
-        if (w == 0 && lane < a.requests) a.plan[lane + 1] = upto;
+        if (w == 0) a.plan[lane + 1] = upto;
       } else {
         for (int i = tid; i <= a.requests; i += THREADS) a.plan[i] = ((const int*)ring)[i];
       }
@@ -246,7 +252,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
 
   while (at < end) {
     Request req;
-    int rt = 0, h, first, stop, seg;
+    int rt = 0, tile = 0, h, first, stop, seg;  // tile: of all requests' row tiles, with pieces
     KeySpan span;
     if constexpr (WHOLE) {
       // key heads vary fastest, so that the row tiles of a head, which read the
@@ -265,6 +271,11 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         b = __builtin_ctzll(__ballot(upto > at));
         begin = b ? __builtin_amdgcn_readlane(upto, b - 1) : 0;
         req = of_lane(mine, b);
+        tile = b;
+        if (a.pieces) {
+          b = uniform(tile / a.row_tiles);
+          rt = tile - b * a.row_tiles;
+        }
       } else {
         for (;;) {  // requests without rows have no steps
           req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
@@ -279,7 +290,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       span = row_tile_span<ROWS>(a, req, rt);
       seg = steps_of(span.count, STEP);
       if (a.pieces) {
-        const int pieces = __builtin_amdgcn_readlane(mine_pieces, b);
+        const int pieces = __builtin_amdgcn_readlane(mine_pieces, tile);
         h = uniform(off / pieces);
         const int x = off - h * pieces;
         first = uniform((int)((int64_t)seg * x / pieces));
@@ -617,10 +628,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
   const int rows = req.n * a.group, r0 = rt * ROWS;
   const int row = group * PER + threadIdx.x / (D / 4), piece = threadIdx.x % (D / 4);
   if (r0 >= rows || group * PER >= ROWS) return;
-  const int from0 = a.plan[b];
+  const int tile = a.pieces ? b * a.row_tiles + rt : b;
+  const int from0 = a.plan[tile];
   int g0, g1;
   if (a.pieces) {
-    const int pieces = (a.plan[b + 1] - from0) / a.kv_heads;
+    const int pieces = (a.plan[tile + 1] - from0) / a.kv_heads;
     g0 = from0 + h * pieces;
     g1 = g0 + pieces - 1;
   } else {
@@ -684,7 +696,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   // go through memory, and a share that straddles segments starts anew), about
   // 14 steps: undivided, one prompt of 512 tokens over 1024 keys (12.8 steps
   // more than an even share) takes 41 us against 47, of 1000 over 1000 (8.5)
-  // 42 against 100, but of 512 over 2048 (24.8) 68 against 55.
+  // 42 against 100, but of 512 over 2048 (24.8) 68 against 46.
   const bool prompt = R == 8 || (D == 256 && R == 4);
   if (seg_most <= 4 || (prompt ? seg_most * (cus - segments) <= 14 * (int64_t)cus
                                : segments >= (R == 4 ? 2 : 8) * (int64_t)cus))
@@ -692,7 +704,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
   const int workers = (int)(need < cus ? need : cus);
   a.row_tiles = (int)row_tiles;
-  a.pieces = row_tiles == 1 && a.requests <= 64 && 2 * segments <= workers;
+  a.pieces = a.requests * row_tiles <= 64 && 2 * segments <= workers;
   launch_kernel<D, R, false>(a, dim3(workers), st);
   const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
   hipLaunchKernelGGL((attend_join_kernel<D, R>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests),
