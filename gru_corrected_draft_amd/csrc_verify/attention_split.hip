@@ -693,12 +693,11 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int64_t seg_most = (keys + 32 * C::kStep - 1) / (32 * C::kStep) + 1;
   // One launch where there is little to split, or enough segments to fill the
   // chip several times over.  Prompts cost much to split (256 or 128 rows' sums
-  // go through memory, and a share that straddles segments starts anew), about
-  // 14 steps: undivided, one prompt of 512 tokens over 1024 keys (12.8 steps
-  // more than an even share) takes 41 us against 47, of 1000 over 1000 (8.5)
-  // 42 against 100, but of 512 over 2048 (24.8) 68 against 46.
+  // go through memory), about 10 steps: undivided, one prompt of 1000 tokens over
+  // 1000 keys (8.5 steps more than an even share) takes 41 us against 46, but of
+  // 512 over 1024 (12.8) 41 against 37, over 2048 (24.8) 68 against 46.
   const bool prompt = R == 8 || (D == 256 && R == 4);
-  if (seg_most <= 4 || (prompt ? seg_most * (cus - segments) <= 14 * (int64_t)cus
+  if (seg_most <= 4 || (prompt ? seg_most * (cus - segments) <= 10 * (int64_t)cus
                                : segments >= (R == 4 ? 2 : 8) * (int64_t)cus))
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
