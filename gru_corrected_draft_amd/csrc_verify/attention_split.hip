@@ -497,8 +497,9 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
             if (!visible(key + 16 * (j >> 3) + 8 * h2 + (j & 7), pos, a.window, a.sinks)) s[x][j] = -INFINITY;
         }
       }
-      v8s p[N][2];
-      softmax_step<D, N>(s, st, p, a.scale_log2);
+      constexpr bool FINE = R == 1;
+      v8s p[N][2], rest[N][2];
+      softmax_step<D, N, FINE>(s, st, p, rest, a.scale_log2);
       constexpr int PAIRS = D / 64;
 #pragma unroll
       for (int x = 0; x < N * PAIRS; ++x) {
@@ -508,6 +509,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
           after = read_values<D>(tile + (x + 1) / PAIRS * T::kBytes, v0_off, (x + 1) % PAIRS);
         __builtin_amdgcn_sched_barrier(0);
         add_values<D>(v, x % PAIRS, st, p[x / PAIRS]);
+        if constexpr (FINE) add_values<D>(v, x % PAIRS, st, rest[x / PAIRS]);
         v = after;
       }
     }

@@ -96,8 +96,8 @@ domino_status_t domino_attention_append(domino_attention_t* h, const domino_cach
  *   s_j = scale * (q . k_j);  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m);
  *   lse = m + ln sum_j e^(s_j - m),  m = max_j s_j, j over the visible keys.
  * Scores, softmax statistics and sums are fp32; for bf16 the weights
- * e^(s_j - m) are rounded to bf16 before they multiply v, and the result is
- * rounded once.  Without a visible key, out is 0 and lse is -inf.  Keys and
+ * e^(s_j - m) multiply v to 15 bits where max_new * q_heads / kv_heads is at
+ * most 32, rounded to bf16 beyond that, and the result is rounded once.  Without a visible key, out is 0 and lse is -inf.  Keys and
  * values that no new token sees do not influence the result whatever they
  * hold, and pages that hold only such keys are not read.  Tokens of a
  * malformed request (its first max_new rows within [0, tokens)) get NaN, and
