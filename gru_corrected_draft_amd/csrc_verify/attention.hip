@@ -150,7 +150,11 @@ __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a, int split
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float mn = fmaxf(m, top);
     const float ref = mn == -INFINITY ? 0.f : mn * a.scale_log2;
-    const float alpha = exp2f(m * a.scale_log2 - ref);
+    // From the difference, so that it is 1 while the maximum stays.  m c - ref
+    // contracts to a fused product whose rest, half an ulp of the score, would
+    // multiply the sums once a tile: 7 to 11 times the error over 6001 and 8192
+    // keys (2 requests with 500 tokens over 2000 keys take 344 us against 338).
+    const float alpha = mn == -INFINITY ? 1.f : exp2f((m - mn) * a.scale_log2);
     float p[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) p[j] = exp2f(__builtin_fmaf(s[j], a.scale_log2, -ref));

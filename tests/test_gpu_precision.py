@@ -47,3 +47,49 @@ def test_few_rows_keep_their_weights(case):
             bad = (out[at:at + n] < low) | (out[at:at + n] > high)
             assert not bad.any(), f"request {b}: {bad.sum()} of {bad.size} off"
             at += n
+
+
+def plain_fp32(q, keys, values, scale):
+    """Attention of one row over all keys, each operation rounded to fp32: scores by one fused sum after the
+    other, weights against the maximum, sums in steps of 16 keys."""
+    f = np.float32
+    s = np.zeros(len(keys), f)
+    for i in range(len(q)):
+        s = (s.astype(np.float64) + np.float64(q[i]) * keys[:, i]).astype(f)
+    s = (s * f(scale)).astype(f)
+    m = s.max()
+    p = np.exp(s - m).astype(f)
+    den, num = f(0), np.zeros(values.shape[1], f)
+    for a in range(0, len(p), 16):
+        den = f(den + p[a:a + 16].sum(dtype=f))
+        num = (num + (p[a:a + 16, None] * values[a:a + 16]).sum(0, dtype=f)).astype(f)
+    return num / den, m + np.log(den)
+
+
+@pytest.mark.parametrize("divided", [False, True])
+@pytest.mark.parametrize("dim,kv,spread,early", [(64, 6001, 4.0, 0), (64, 6001, 1.0, 1), (128, 8192, 1.0, 0), (128, 8192, 4.0, 0)])
+def test_fp32_errs_as_a_plain_evaluation_over_long_contexts(dim, kv, spread, early, divided):
+    """fp32, thousands of keys: the kernel rounds as often as a plain fp32 evaluation does, in another order, so
+    its error is that one's: within three times of it in the root mean square, for outputs and log-sum-exps.
+    With other requests beside it a row's keys stay in one workgroup, alone they are dealt to many."""
+    log(f"[gpu-test] attention fp32 long {dim} {kv} {spread} {early} {divided}")
+    others = 0 if divided else 33  # x 8 key heads: more segments than CUs
+    s = Setup((8, 8), dim, 64, "fp32", [1] * (1 + others), [kv] + [1] * others, seed=41)
+    s.q *= spread
+    if early:  # the largest score comes first
+        s.keys[0][3] = s.q[0] / s.q[0].norm(dim=-1, keepdim=True) * (0.7 * dim ** 0.5)
+        s.k_cache[s.table[0, 0].long(), :, 3] = s.keys[0][3]
+    out, lse = s.run(max_new=1, max_kv=kv)
+    out, lse = out[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+    q, keys, values = (x.cpu().numpy() for x in (s.q[:1], s.keys[0], s.values[0]))
+    want, want_l, _, _ = ref.attention(q, keys, values, kv)
+    plain = [plain_fp32(q[0, h], keys[:, h], values[:, h], dim ** -0.5) for h in range(8)]
+
+    def rms(x):
+        return float(np.sqrt(np.mean(np.square(x))))
+
+    for name, got, exact, base in (("out", out, want[0], np.stack([o for o, _ in plain])),
+                                   ("lse", lse, want_l[0], np.array([n for _, n in plain]))):
+        here, there = rms(got - exact), rms(base - exact)
+        log(f"[gpu-test]   {name}: {here:.2e}, plain {there:.2e}")
+        assert here <= 3 * there, f"{name}: {here:.3g}, a plain evaluation {there:.3g}"
