@@ -74,9 +74,10 @@ struct LogitsArgs {
 };
 
 // What one wave knows of a row: a reference m, the sum of e^((x - m) / T), and
-// the best candidate with its id (kNone: no candidate).
+// the best candidate: its score, its logit (a score less T ln E is not quite the
+// logit, by an ulp over T of its log-probability) and its id (kNone: no candidate).
 struct RowPart {
-  float m, s, best;
+  float m, s, best, logit;
   int32_t id;
 };
 constexpr int32_t kNone = 0x7FFFFFFF;
@@ -255,6 +256,11 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 __device__ __forceinline__ int wave_min(int x) {
   return (int)wave_reduce((uint32_t)x, [](uint32_t a, uint32_t b) { return (uint32_t)min((int)a, (int)b); });
+}
+
+// x of the first lane where `mine` holds (some lane's has to)
+__device__ __forceinline__ float of_lane_with(float x, bool mine) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), __builtin_ctzll(__ballot(mine))));
 }
 
 // LDS of a workgroup: counts, last bias entry, list and bitmap of touched ids
@@ -582,6 +588,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
       }
     }
     int id = kNone;
+    float logit = 0.f;
     if constexpr (VERIFY) {
       // exact id of this lane's best candidate: the first of its vector
       if (where >= 0) {
@@ -593,8 +600,12 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
         for (int j = V - 1; j >= 0; --j) {
           float y = tame(x[j]);
           if (((gone >> j) & 1) || where + j == own) continue;
+          const float l = y;
           if (temp > 0.f) y -= noise[where + j];
-          if (y == best) id = lo + where + j;
+          if (y == best) {
+            id = lo + where + j;
+            logit = l;
+          }
         }
       }
     }
@@ -628,10 +639,12 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
             s += exp2_fast((y - m) * c);
           }
           if (off[u] == own) continue;
+          const float l = y;
           if (temp > 0.f) y -= noise[off[u]];
           if (y > best || (y == best && lo + off[u] < id)) {
             best = y;
             id = lo + off[u];
+            logit = l;
           }
         }
       }
@@ -643,13 +656,20 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
         m = all;
       }
       const float most = wave_max(best);
-      id = wave_min(best == most ? id : kNone);
+      const int mine = best == most ? id : kNone;
+      id = wave_min(mine);
       best = most;
+      logit = of_lane_with(logit, mine == id);
       if (lane == 0)
         a.partial[((int64_t)b * a.rows + row) * ((int64_t)gridDim.y * a.parts) +
-                  (int64_t)blockIdx.y * a.parts + part] = RowPart{m, s, best, id};
+                  (int64_t)blockIdx.y * a.parts + part] = RowPart{m, s, best, logit, id};
     }
   }
+}
+
+// ln e^((x - m) / T) / s, above 0 only by roundings
+__device__ __forceinline__ float log_probability(float x, float m, float scale, float ln_s) {
+  return fminf((x - m) / scale - ln_s, 0.f);
 }
 
 // One workgroup per request joins the parts of its rows, walks the proposals
@@ -658,7 +678,7 @@ __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
 // registers from the pass (64 blocks 155 us against 141, one block 15.0 against
 // 13.5).
 __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
-  __shared__ float s_lse[kMaxRows], s_m[kMaxRows], s_best[kMaxRows];
+  __shared__ float s_lse[kMaxRows], s_m[kMaxRows], s_logit[kMaxRows];
   __shared__ int s_id[kMaxRows], s_stands[kMaxRows];
   const int b = blockIdx.x, lane = threadIdx.x & 63, w = wave_index();
   const int n = a.draft ? clip_len(a.draft_len, b, a.rows - 1) : 0;
@@ -666,7 +686,7 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
   const float scale = temp > 0.f ? temp : 1.f, c = 1.44269504088896340736f / scale;
   for (int row = w; row <= n; row += (int)(blockDim.x >> 6)) {
     const RowPart* p = a.partial + ((int64_t)b * a.rows + row) * parts;
-    float m = -INFINITY, s = 0.f, best = -INFINITY;
+    float m = -INFINITY, s = 0.f, best = -INFINITY, logit = 0.f;
     int id = kNone;
     for (int i = lane; i < parts; i += 64) {
       const RowPart o = p[i];
@@ -676,14 +696,17 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
       if (o.best > best || (o.best == best && o.id < id)) {
         best = o.best;
         id = o.id;
+        logit = o.logit;
       }
     }
     const float all = wave_max(m);
     if (all > -INFINITY) s = wave_sum(s * exp2_fast((m - all) * c));
     m = all;
     const float most = wave_max(best);
-    id = wave_min(best == most ? id : kNone);
+    const int mine = best == most ? id : kNone;
+    id = wave_min(mine);
     best = most;
+    logit = of_lane_with(logit, mine == id);
     if (lane == 0) {
       int stands = 0;
       float lp = -INFINITY;
@@ -692,7 +715,7 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
         if (d >= 0 && d < a.vocab) {
           const float x = a.drafted[b * a.rows + row];
           if (x > -INFINITY) {
-            lp = (x - m) / scale - logf(s);
+            lp = log_probability(x, m, scale, logf(s));
             stands = id == kNone || (temp > 0.f ? a.accept_u[b * a.accept_stride + row] < expf(lp)
                                                 : x > best || (x == best && d < id));
           }
@@ -701,7 +724,7 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
       s_stands[row] = stands;
       s_id[row] = id;
       s_m[row] = m;
-      s_best[row] = best;
+      s_logit[row] = logit;
       // log-probability of the proposal where it stands; of the chosen id below
       s_lse[row] = stands ? lp : logf(s);
     }
@@ -724,9 +747,7 @@ __global__ __launch_bounds__(1024) void accept_kernel(LogitsArgs a, int parts) {
           lp = -INFINITY;
         } else {
           tok = id;
-          // the best score is x - T ln E: the logit itself is that plus T ln E
-          const float x = temp > 0.f ? s_best[lane] + temp * logf(a.noise[b * a.noise_stride + id]) : s_best[lane];
-          lp = (x - s_m[lane]) / scale - s_lse[lane];
+          lp = log_probability(s_logit[lane], s_m[lane], scale, s_lse[lane]);
         }
       }
       a.out_tokens[b * a.rows + lane] = tok;

@@ -93,3 +93,62 @@ def test_fp32_errs_as_a_plain_evaluation_over_long_contexts(dim, kv, spread, ear
         here, there = rms(got - exact), rms(base - exact)
         log(f"[gpu-test]   {name}: {here:.2e}, plain {there:.2e}")
         assert here <= 3 * there, f"{name}: {here:.3g}, a plain evaluation {there:.3g}"
+
+
+def _rules(kind, batch, vocab):
+    """No rule, or biases of 0 that put every third id on the list of touched ones."""
+    import torch
+    if kind == "plain":
+        return {}
+    ids = torch.arange(0, vocab, 3, dtype=torch.int32, device="cuda").repeat(batch, 1)
+    return dict(bias_ids=ids, bias_values=torch.zeros(ids.shape, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["plain", "touched"])
+@pytest.mark.parametrize("temp", [0.01, 0.05, 0.3, 1.0])
+def test_log_probabilities_of_sampled_tokens(temp, kind, dtype):
+    """Logits near 20, apart by about a temperature.  With u = 2^-24: z = (x - m) / T is off by 2 u |z|, a term of
+    the sum by 3.5 u |z| (difference, product, two roundings of its factor) and 2 u of the exponential, the sum
+    by u for each of at most 64 additions one after the other, the logarithm by 2 u of itself and the result by
+    u.  m is at most 16 powers of two below the largest logit, so |z| <= 11.1 + ln V where it counts and
+    |ln s| <= 11.1 + ln V: in all u (5 |lp| + 10 (11.1 + ln V) + 66)."""
+    import torch
+    from gru_corrected_draft_amd import verify
+    vocab, batch, rows = 1501, 64, 2
+    log(f"[gpu-test] log-probabilities {temp} {kind} {dtype}")
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x = (20 + temp * torch.randn((batch, rows, vocab), generator=g, device="cuda")).to(dt)
+    draft = torch.randint(0, vocab, (batch, rows - 1), generator=g, device="cuda", dtype=torch.int32)
+    noise = torch.empty((batch, vocab), device="cuda").exponential_(generator=g).clamp_(min=1e-30)
+    t = torch.full((batch,), temp, device="cuda")
+    op = verify.DraftVerifier(vocab, dt, batch, rows)
+    tokens, accepted, lp = op.run(x, draft, temperature=t, noise=noise, return_logprob=True,
+                                  accept_u=torch.zeros((batch, rows - 1), device="cuda"), **_rules(kind, batch, vocab))
+    assert (lp <= 0).all() and (accepted == rows - 1).all()
+    want = torch.log_softmax(x.double() / t.double()[:, None, None], -1).gather(2, tokens.long()[..., None])[..., 0]
+    err = (lp.double() - want).abs()
+    tol = 2.0 ** -24 * (5 * want.abs() + 10 * (11.1 + np.log(vocab)) + 66)
+    log(f"[gpu-test]   off by {err.max().item():.2e}, bound {tol.min().item():.2e}")
+    assert (err <= tol).all(), f"{(err / tol).max().item():.3g} of the bound"
+
+
+@pytest.mark.parametrize("kind", ["plain", "touched"])
+def test_a_sampled_only_candidate_has_log_probability_zero(kind):
+    import torch
+    from gru_corrected_draft_amd import verify
+    vocab, batch = 700, 200
+    log(f"[gpu-test] only candidate {kind}")
+    g = torch.Generator(device="cuda").manual_seed(19)
+    x = 20 + 3 * torch.randn((batch, 1, vocab), generator=g, device="cuda")
+    at = torch.randint(0, vocab, (batch,), generator=g, device="cuda")
+    words = torch.zeros((batch, 1, (vocab + 31) // 32), dtype=torch.int64, device="cuda")
+    words[torch.arange(batch, device="cuda"), 0, at // 32] = 1 << (at % 32)
+    words = torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
+    noise = torch.empty((batch, vocab), device="cuda").exponential_(generator=g).clamp_(min=1e-30)
+    op = verify.DraftVerifier(vocab, torch.float32, batch, 1)
+    for temp in (0.05, 0.3, 1.5):
+        tokens, _, lp = op.run(x, temperature=torch.full((batch,), temp, device="cuda"), noise=noise, mask=words,
+                               return_logprob=True, **_rules(kind, batch, vocab))
+        assert torch.equal(tokens[:, 0].long(), at) and (lp == 0).all(), f"{(lp != 0).sum().item()} are not 0"
