@@ -827,6 +827,18 @@ static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t
   return k;
 }
 
+// more dynamic LDS than the default 64 KB for every kernel of this type
+template <typename T>
+static hipError_t allow_lds() {
+  const void* const kernels[] = {(const void*)&logits_kernel<T, false, false>, (const void*)&logits_kernel<T, false, true>,
+                                 (const void*)&logits_kernel<T, true, false>, (const void*)&logits_kernel<T, true, true>};
+  for (const void* k : kernels) {
+    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 extern "C" domino_status_t domino_verify_create(const domino_verify_config_t* cfg, domino_verify_t** out) {
   if (!out) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: out is NULL");
   *out = nullptr;
@@ -844,6 +856,10 @@ extern "C" domino_status_t domino_verify_create(const domino_verify_config_t* cf
   int dev = 0;
   domino_status_t st = check_device(t_err, &dev);
   if (st != DOMINO_OK) return st;
+  if ((cfg->dtype == DOMINO_DTYPE_BF16 ? allow_lds<bf16_t>() : allow_lds<float>()) != hipSuccess) {
+    (void)hipGetLastError();
+    return say(t_err, DOMINO_ERR_HIP, "create: the kernels' LDS limit could not be set");
+  }
   domino_verify* h = new (std::nothrow) domino_verify();
   if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
   h->cfg = *cfg;
