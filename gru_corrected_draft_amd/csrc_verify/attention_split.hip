@@ -707,6 +707,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   a.row_tiles = (int)row_tiles;
   a.pieces = a.requests * row_tiles <= 64 && 2 * segments <= workers;
   launch_kernel<D, R, false>(a, dim3(workers), st);
+  if (hipPeekAtLastError() != hipSuccess) return;  // the join would follow the plan of an earlier call
   const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
   hipLaunchKernelGGL((attend_join_kernel<D, R>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests),
                      dim3(256), 0, st, a, workers, groups);

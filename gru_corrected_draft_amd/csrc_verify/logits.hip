@@ -1033,6 +1033,8 @@ extern "C" domino_status_t domino_verify_run(domino_verify_t* h, const domino_lo
   (void)hipGetLastError();
   Cut k;
   launch_logits<true>(h, a, k, (hipStream_t)stream);
-  hipLaunchKernelGGL(accept_kernel, dim3(a.requests), dim3(a.rows < 16 ? 64 * a.rows : 1024), 0, (hipStream_t)stream, a, k.ranges * k.parts);
+  if (hipPeekAtLastError() == hipSuccess)  // else it would join what an earlier call left
+    hipLaunchKernelGGL(accept_kernel, dim3(a.requests), dim3(a.rows < 16 ? 64 * a.rows : 1024), 0, (hipStream_t)stream, a,
+                       k.ranges * k.parts);
   return launched(h, "run");
 }

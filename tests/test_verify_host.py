@@ -1,0 +1,87 @@
+"""The host side of the handles of ``domino_verify.h``, walked without a GPU: what they ask of the runtime, and
+what they do when it refuses (CPU only).
+
+Each test runs in a process of its own whose HIP runtime is ``_host_runtime.cpp``: launches are counted, none
+is carried out, so pointers need not point anywhere."""
+import os
+import shutil
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+from tests.conftest import ROOT
+
+PREAMBLE = """
+import ctypes, sys, types
+sys.path.insert(0, {root!r})
+rt = ctypes.CDLL({runtime!r}, mode=ctypes.RTLD_GLOBAL)
+for n in ("bytes", "lds_asked", "lds_launched"):
+    getattr(rt, "host_" + n).restype = ctypes.c_longlong
+torch = types.ModuleType("torch")
+torch.bfloat16, torch.float32, torch.int32 = "bfloat16", "float32", "int32"
+torch._C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: None)
+torch.cuda = types.SimpleNamespace(current_device=lambda: 0)
+sys.modules["torch"] = torch
+from gru_corrected_draft_amd import rollout as R, verify
+lib = verify.load_library()
+P = ctypes.c_void_p(1 << 20)
+
+def attention(hq=8, hk=2, dim=128, page=16, requests=4, dtype=R.DTYPE_BF16):
+    h = ctypes.c_void_p()
+    st = lib.domino_attention_create(ctypes.byref(verify.AttentionConfig(hq, hk, dim, page, requests, dtype)), ctypes.byref(h))
+    return st, h
+
+def attend(h, kv=4096, width=256, tokens=4, max_new=1, hk=2, dim=128, page=16, requests=4, elem=2, out=(1024, 128)):
+    c = verify.CacheArgs(1 << 20, 1 << 20, hk * page * dim, page * dim, dim, 4096, 1 << 20, width, width, 1 << 20, 1 << 20,
+                         requests, tokens, max_new, kv)
+    return lib.domino_attention_run(h, ctypes.byref(c), P, 1024, 128, 0, 0, 0.1, P, *out, None, None)
+
+def verifier(vocab=151936, requests=16, rows=16, dtype=R.DTYPE_BF16):
+    h = ctypes.c_void_p()
+    return lib.domino_verify_create(ctypes.byref(verify.VerifyConfig(vocab, requests, rows, dtype)), ctypes.byref(h)), h
+
+def check(h, requests=16, rows=1, vocab=151936):
+    a = verify.LogitsArgs(1 << 20, vocab * rows, vocab, requests, rows)
+    return lib.domino_verify_run(h, ctypes.byref(a), None, None, 0, None, 0, P, P, None, None)
+"""
+
+
+@pytest.fixture(scope="module")
+def runtime(tmp_path_factory):
+    include = "/opt/rocm/include"
+    if not shutil.which("g++") or not os.path.isdir(include):
+        pytest.skip("needs g++ and the HIP headers")
+    so = str(tmp_path_factory.mktemp("runtime") / "libamdhip64.so.7")
+    subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-w", "-D__HIP_PLATFORM_AMD__", "-I", include, "-Wl,-soname,libamdhip64.so.7",
+                    os.path.join(ROOT, "tests", "_host_runtime.cpp"), "-o", so], check=True)
+    return so
+
+
+def walk(runtime, body):
+    """Runs `body`, whose assertions have to hold."""
+    code = PREAMBLE.format(root=ROOT, runtime=runtime) + textwrap.dedent(body)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_failed_launch_ends_the_call(runtime):
+    """The second launch of a call joins what the first one left: after a failed first there is none."""
+    walk(runtime, """
+        st, h = verifier()
+        assert st == 0 and check(h) == 0 and rt.host_launches() == 2
+        rt.host_fail(0, -1)
+        assert check(h) == R.DOMINO_ERR_HIP and rt.host_launches() == 2
+        assert b"launch failed" in lib.domino_verify_last_error(h)
+        assert check(h) == 0 and rt.host_launches() == 4
+        rt.host_fail(1, -1)
+        assert check(h) == R.DOMINO_ERR_HIP and rt.host_launches() == 5
+
+        st, h = attention()
+        assert st == 0 and attend(h) == 0 and rt.host_launches() == 7
+        rt.host_fail(0, -1)
+        assert attend(h) == R.DOMINO_ERR_HIP and rt.host_launches() == 7
+        assert b"launch failed" in lib.domino_attention_last_error(h)
+        assert attend(h) == 0 and rt.host_launches() == 9
+        """)
