@@ -324,6 +324,10 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   int dev = 0;
   domino_status_t st = check_device(t_err, &dev);
   if (st != DOMINO_OK) return st;
+  if (cfg->dtype == DOMINO_DTYPE_BF16 && attend_split_prepare(cfg->head_dim) != hipSuccess) {
+    (void)hipGetLastError();
+    return say(t_err, DOMINO_ERR_HIP, "create: the kernels' LDS limit could not be set");
+  }
   domino_attention* h = new (std::nothrow) domino_attention();
   if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
   h->cfg = *cfg;

@@ -299,5 +299,7 @@ __device__ __forceinline__ float noted(float x, uint32_t bits) {
   return bits == 0 ? x : x + (bits == 3 ? NAN : bits == 2 ? -INFINITY : INFINITY);
 }
 
+// once for a device, before the first launch there
+hipError_t attend_split_prepare(int head_dim);
 void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st);
 size_t attend_split_floats(int head_dim, int cus);

@@ -675,11 +675,27 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
 template <int D, int R, bool WHOLE>
 void launch_kernel(const AttendArgs& a, dim3 grid, hipStream_t st) {
   using C = Shape<D, R>;
-  // more than the default 64 KB of LDS; asked for once
-  static const hipError_t big = hipFuncSetAttribute((const void*)&attend_split_kernel<D, R, WHOLE>,
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-  (void)big;
   hipLaunchKernelGGL((attend_split_kernel<D, R, WHOLE>), grid, dim3(C::kThreads), C::kLds, st, a);
+}
+
+// more than the default 64 KB of LDS
+template <int D, int R>
+hipError_t allow_lds() {
+  for (const void* k : {(const void*)&attend_split_kernel<D, R, false>, (const void*)&attend_split_kernel<D, R, true>}) {
+    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, Shape<D, R>::kLds);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+template <int D>
+hipError_t allow_lds_d() {
+  hipError_t e = allow_lds<D, 1>();
+  if (e == hipSuccess) e = allow_lds<D, 4>();
+  if constexpr (D < 256) {
+    if (e == hipSuccess) e = allow_lds<D, 2>();
+    if (e == hipSuccess) e = allow_lds<D, 8>();
+  }
+  return e;
 }
 
 template <int D, int R>
@@ -735,6 +751,10 @@ void launch_d(const AttendArgs& a, int cus, hipStream_t st) {
 // workgroup
 size_t attend_split_floats(int head_dim, int cus) {
   return (size_t)2 * cus * (head_dim == 256 ? 128 : 256) * (head_dim + 2);
+}
+
+hipError_t attend_split_prepare(int head_dim) {
+  return head_dim == 64 ? allow_lds_d<64>() : head_dim == 128 ? allow_lds_d<128>() : allow_lds_d<256>();
 }
 
 void launch_attend_split(int head_dim, const AttendArgs& a, int cus, hipStream_t st) {

@@ -6,11 +6,15 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <map>
+
 namespace {
 hipError_t last = hipSuccess;
 int device = 0, launches = 0, attributes = 0, live = 0;
 int fail_launch = -1, fail_attribute = -1;  // the n-th from now, from 0
-long long lds_asked = 0, lds_launched = 0, bytes = 0;
+long long lds_launched = 0, bytes = 0;
+int over = 0;                              // launches with more LDS than was asked for
+std::map<const void*, size_t> limits;
 struct {
   dim3 grid, block;
   size_t lds;
@@ -25,11 +29,15 @@ hipError_t done(hipError_t e) {
 
 extern "C" {
 void host_fail(int launch, int attribute) { fail_launch = launch, fail_attribute = attribute; }
+void host_reset() {
+  launches = attributes = over = 0, lds_launched = 0;
+  limits.clear();
+}
 int host_launches() { return launches; }
 int host_attributes() { return attributes; }
 int host_allocations() { return live; }
 long long host_bytes() { return bytes; }
-long long host_lds_asked() { return lds_asked; }
+int host_over() { return over; }
 long long host_lds_launched() { return lds_launched; }
 
 void** __hipRegisterFatBinary(const void*) { return (void**)&device; }
@@ -45,24 +53,25 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
   *grid = pushed.grid, *block = pushed.block, *lds = pushed.lds, *stream = pushed.stream;
   return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void*, dim3, dim3, void**, size_t lds, hipStream_t) {
+hipError_t hipLaunchKernel(const void* kernel, dim3, dim3, void**, size_t lds, hipStream_t) {
   if (fail_launch == 0) {
     fail_launch = -1;
     return done(hipErrorLaunchFailure);
   }
   if (fail_launch > 0) --fail_launch;
   ++launches;
+  over += lds > 65536 && (!limits.count(kernel) || lds > limits[kernel]);
   if ((long long)lds > lds_launched) lds_launched = lds;
   return done(hipSuccess);
 }
-hipError_t hipFuncSetAttribute(const void*, hipFuncAttribute, int value) {
+hipError_t hipFuncSetAttribute(const void* kernel, hipFuncAttribute, int value) {
   if (fail_attribute == 0) {
     fail_attribute = -1;
     return done(hipErrorInvalidValue);
   }
   if (fail_attribute > 0) --fail_attribute;
   ++attributes;
-  if (value > lds_asked) lds_asked = value;
+  limits[kernel] = value;
   return done(hipSuccess);
 }
 

@@ -17,7 +17,7 @@ PREAMBLE = """
 import ctypes, sys, types
 sys.path.insert(0, {root!r})
 rt = ctypes.CDLL({runtime!r}, mode=ctypes.RTLD_GLOBAL)
-for n in ("bytes", "lds_asked", "lds_launched"):
+for n in ("bytes", "lds_launched"):
     getattr(rt, "host_" + n).restype = ctypes.c_longlong
 torch = types.ModuleType("torch")
 torch.bfloat16, torch.float32, torch.int32 = "bfloat16", "float32", "int32"
@@ -84,4 +84,43 @@ def test_a_failed_launch_ends_the_call(runtime):
         assert attend(h) == R.DOMINO_ERR_HIP and rt.host_launches() == 7
         assert b"launch failed" in lib.domino_attention_last_error(h)
         assert attend(h) == 0 and rt.host_launches() == 9
+        """)
+
+
+def test_lds_is_asked_for_at_create(runtime):
+    """Before a handle's first launch its device has been asked for as much LDS as any launch takes, by each
+    handle (another one may be on another device), and a refusal is the create's error."""
+    walk(runtime, """
+        for make, use in ((verifier, check), (attention, attend)):
+            st, h = make()
+            asked = rt.host_attributes()
+            assert st == 0 and asked > 0 and rt.host_launches() == 0
+            st, h = make()
+            assert st == 0 and rt.host_attributes() == 2 * asked
+            rt.host_fail(-1, asked - 1)
+            live = rt.host_allocations()
+            st, none = make()
+            assert st == R.DOMINO_ERR_HIP and not none.value and rt.host_allocations() == live
+            before = rt.host_attributes()
+            assert use(h) == 0 and rt.host_attributes() == before
+            rt.host_reset()
+
+        for dim in (64, 128, 256):
+            for new in (1, 16, 32, 300):
+                for kv in (64, 4096):
+                    st, h = attention(dim=dim)
+                    assert st == 0 and attend(h, kv=kv, dim=dim, max_new=new, tokens=4 * new) == 0
+        assert rt.host_lds_launched() > 65536 and rt.host_over() == 0
+        rt.host_reset()
+        for dtype in (R.DTYPE_BF16, R.DTYPE_FP32):
+            st, h = verifier(dtype=dtype, requests=512)
+            for requests in (1, 16, 24, 64, 512):
+                for rules in (0, 1, 2, 3):
+                    a = verify.LogitsArgs(1 << 20, 151936, 151936, requests, 1)
+                    if rules & 1:
+                        a.repetition = 1 << 20
+                    if rules & 2:
+                        a.bias_ids, a.bias_values, a.bias_width, a.bias_stride = 1 << 20, 1 << 20, 9, 9
+                    assert lib.domino_verify_run(h, ctypes.byref(a), P, None, 0, P, 151936, P, P, None, None) == 0
+        assert rt.host_lds_launched() > 65536 and rt.host_over() == 0
         """)
