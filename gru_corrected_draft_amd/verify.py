@@ -4,7 +4,8 @@ that reads it, and the rules on the target's logits with the acceptance of the p
 Thin ctypes binding of ``include/domino_verify.h``; the mathematics of each operator stands there.
 ``PagedAttention`` and ``DraftVerifier`` marshal tensors: every argument is checked for type, shape,
 device and layout, work goes to the current stream of the tensors' device, and the handle must not
-be used by two threads at once.  Importing this module needs the built library; there is no fallback.
+be used by two threads at once.  A handle belongs to the GPU that is current where it is made, and takes
+tensors of that GPU alone.  Importing this module needs the built library; there is no fallback.
 """
 from __future__ import annotations
 
@@ -108,10 +109,14 @@ class _Handle:
         if st:
             raise DominoError(st, self._error(None).decode())
         self.handle = h
+        self.index = torch.cuda.current_device()  # the GPU that the handle's workspace is on
 
     def _check(self, st):
         if st:
             raise DominoError(st, self._error(self.handle).decode())
+
+    def _elsewhere(self, index):
+        return ValueError(f"the handle is on cuda:{self.index}, the tensors on cuda:{index}")
 
     def close(self):
         if getattr(self, "handle", None):
@@ -151,7 +156,7 @@ class PagedAttention(_Handle):
         strides = k_cache.stride()
         b, width = page_table.shape if page_table.dim() == 2 else (-1, -1)
         if not (_fits(k_cache, self.dtype, shape, index) and _fits(v_cache, self.dtype, shape, index)
-                and v_cache.stride() == strides and strides[3] == 1 and index >= 0
+                and v_cache.stride() == strides and strides[3] == 1 and index == self.index
                 and _fits(page_table, torch.int32, (b, width), index) and _fits(kv_len, torch.int32, (b,), index)
                 and _fits(q_start, torch.int32, (b + 1,), index) and page_table.stride(1) == 1
                 and kv_len.stride(0) == 1 and q_start.stride(0) == 1):
@@ -162,6 +167,8 @@ class PagedAttention(_Handle):
             _want("page_table", page_table, torch.int32, (b, width), index)
             _want("kv_len", kv_len, torch.int32, (b,), index)
             _want("q_start", q_start, torch.int32, (b + 1,), index)
+            if index != self.index:
+                raise self._elsewhere(index)
         if max_new is None:
             max_new = tokens
         if max_kv is None:
@@ -246,8 +253,8 @@ class DraftVerifier(_Handle):
 
         take("logits", logits, self.dtype, (b, rows, self.vocab))
         a = LogitsArgs(logits.data_ptr(), ls[0], ls[1], b, rows)
-        if index < 0:
-            raise ValueError("tensors must be on a GPU")
+        if index != self.index:
+            raise self._elsewhere(index) if index >= 0 else ValueError("tensors must be on a GPU")
         if draft is not None and rows > 1:
             a.draft, a.draft_stride = take("draft", draft, i32, (b, rows - 1)), draft.stride(0)
         if history is not None:

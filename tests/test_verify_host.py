@@ -45,6 +45,37 @@ def verifier(vocab=151936, requests=16, rows=16, dtype=R.DTYPE_BF16):
 def check(h, requests=16, rows=1, vocab=151936):
     a = verify.LogitsArgs(1 << 20, vocab * rows, vocab, requests, rows)
     return lib.domino_verify_run(h, ctypes.byref(a), None, None, 0, None, 0, P, P, None, None)
+
+class Tensor:
+    # what the binding looks at
+    def __init__(self, dtype, *shape, device=0):
+        self.dtype, self.shape, self.index = dtype, shape, device
+        self.strides = [1]
+        for n in reversed(shape[1:]):
+            self.strides.insert(0, self.strides[0] * n)
+    def dim(self): return len(self.shape)
+    def stride(self, i=None): return tuple(self.strides) if i is None else self.strides[i]
+    def get_device(self): return self.index
+    def data_ptr(self): return 1 << 20
+    @property
+    def device(self): return f"cuda:{{self.index}}"
+
+torch.empty = lambda shape, dtype=None, device=None: Tensor(dtype, *shape, device=int(str(device)[-1]))
+
+def cache_tensors(requests=4, device=0):
+    i = "int32"
+    return (Tensor("bfloat16", 64, 2, 16, 128, device=device), Tensor("bfloat16", 64, 2, 16, 128, device=device),
+            Tensor(i, requests, 8, device=device), Tensor(i, requests, device=device), Tensor(i, requests + 1, device=device))
+
+def refused(call, match):
+    n = rt.host_launches()
+    try:
+        call()
+    except ValueError as e:
+        assert match in str(e), e
+    else:
+        raise AssertionError("not refused")
+    assert rt.host_launches() == n
 """
 
 
@@ -123,4 +154,28 @@ def test_lds_is_asked_for_at_create(runtime):
                         a.bias_ids, a.bias_values, a.bias_width, a.bias_stride = 1 << 20, 1 << 20, 9, 9
                     assert lib.domino_verify_run(h, ctypes.byref(a), P, None, 0, P, 151936, P, P, None, None) == 0
         assert rt.host_lds_launched() > 65536 and rt.host_over() == 0
+        """)
+
+
+def test_tensors_of_another_gpu_are_refused(runtime):
+    """A handle's workspace is on one GPU: tensors of another would be read from there on the wrong stream."""
+    walk(runtime, """
+        a = verify.PagedAttention(8, 2, 128, 16, max_requests=4)
+        for device in (0, 1):
+            q, k = (Tensor("bfloat16", 4, h, 128, device=device) for h in (8, 2))
+            c = cache_tensors(device=device)
+            calls = (lambda: a.run(q, *c), lambda: a.append(k, k, *c))
+            for call in calls:
+                if device == 0:
+                    call()
+                else:
+                    refused(call, "the handle is on cuda:0")
+        v = verify.DraftVerifier(1000, max_requests=4)
+        for device in (0, 1):
+            x = Tensor("bfloat16", 4, 3, 1000, device=device)
+            for call in (lambda: v.run(x), lambda: v.process(x)):
+                if device == 0:
+                    call()
+                else:
+                    refused(call, "the handle is on cuda:0")
         """)
