@@ -94,6 +94,13 @@ def _want(name, t, dtype, shape, index):
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
+def _int32(name, x):
+    """Refuses what ctypes would cut to 32 bits without a word (2 ** 32 + 64 would become 64)."""
+    if not -2147483648 <= x < 2147483648:
+        raise ValueError(f"{name} must be a 32-bit number, got {x}")
+    return x
+
+
 # the current stream's address without a Stream object around it (a call's checks and arguments take
 # about as long on the host as its kernel on the GPU, so each microsecond shows)
 _stream = torch._C._cuda_getCurrentRawStream
@@ -145,8 +152,8 @@ class PagedAttention(_Handle):
     def __init__(self, q_heads, kv_heads, head_dim, page_size, dtype=torch.bfloat16, max_requests=64):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-        super().__init__("attention", AttentionConfig(q_heads, kv_heads, head_dim, page_size,
-                                                      max_requests, _DTYPES[dtype]))
+        sizes = dict(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, max_requests=max_requests)
+        super().__init__("attention", AttentionConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]))
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype = page_size, dtype
         self._scale = 1.0 / math.sqrt(head_dim)
@@ -173,6 +180,9 @@ class PagedAttention(_Handle):
             max_new = tokens
         if max_kv is None:
             max_kv = min(width * self.page_size, 2 ** 31 - 1)
+        if (max_new | max_kv) >> 31:  # negative ones are the library's to refuse
+            _int32("max_new", max_new)
+            _int32("max_kv", max_kv)
         return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
                          page_table.data_ptr(), page_table.stride(0), width, kv_len.data_ptr(),
                          q_start.data_ptr(), b, tokens, max_new, max_kv)
@@ -205,6 +215,9 @@ class PagedAttention(_Handle):
         if not (_fits(q, self.dtype, shape, index) and qs[2] == 1):
             _want("q", q, self.dtype, shape, index)
         c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index)
+        if (window | sinks) >> 31:
+            _int32("window", window)
+            _int32("sinks", sinks)
         if out is None:
             out = torch.empty(shape, dtype=self.dtype, device=q.device)
         else:
@@ -236,7 +249,8 @@ class DraftVerifier(_Handle):
     def __init__(self, vocab, dtype=torch.bfloat16, max_requests=64, max_rows=16):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-        super().__init__("verify", VerifyConfig(vocab, max_requests, max_rows, _DTYPES[dtype]))
+        sizes = dict(vocab=vocab, max_requests=max_requests, max_rows=max_rows)
+        super().__init__("verify", VerifyConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]))
         self.vocab, self.dtype = vocab, dtype
 
     def _args(self, logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,

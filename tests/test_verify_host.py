@@ -179,3 +179,20 @@ def test_tensors_of_another_gpu_are_refused(runtime):
                 else:
                     refused(call, "the handle is on cuda:0")
         """)
+
+
+def test_numbers_beyond_32_bits_are_refused(runtime):
+    """ctypes keeps the low 32 bits: a window of 2^32 + 64 would be one of 64."""
+    walk(runtime, """
+        a = verify.PagedAttention(8, 2, 128, 16, max_requests=4)
+        q, k, c = Tensor("bfloat16", 4, 8, 128), Tensor("bfloat16", 4, 2, 128), cache_tensors()
+        a.run(q, *c, window=2 ** 31 - 1, sinks=2 ** 31 - 1, max_new=2 ** 31 - 1, max_kv=2 ** 31 - 1)
+        for name in ("window", "sinks", "max_new", "max_kv"):
+            for x in (2 ** 32 + 64, 2 ** 31, -2 ** 31 - 1):
+                refused(lambda: a.run(q, *c, **{name: x}), name)
+                if name.startswith("max"):
+                    refused(lambda: a.append(k, k, *c, **{name: x}), name)
+        refused(lambda: verify.PagedAttention(2 ** 32 + 8, 2, 128, 16), "q_heads")
+        refused(lambda: verify.PagedAttention(8, 2, 128, 2 ** 32 + 16), "page_size")
+        refused(lambda: verify.DraftVerifier(2 ** 32 + 1000), "vocab")
+        """)
