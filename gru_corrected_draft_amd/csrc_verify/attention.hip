@@ -491,6 +491,8 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
   if (!rows_ok(q, q_token_stride, q_head_stride, unit) || !rows_ok(out, out_token_stride, out_head_stride, unit))
     return say(h->err, DOMINO_ERR_INVALID_ARG,
                "run: q and out must be 16-byte aligned, their strides multiples of 16 bytes");
+  if ((c->tokens > 1 && out_token_stride < f.head_dim) || (f.q_heads > 1 && out_head_stride < f.head_dim))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "run: rows of out overlap");
   if ((uintptr_t)lse & 3) return say(h->err, DOMINO_ERR_INVALID_ARG, "run: lse must be 4-byte aligned");
   const int32_t max_new = c->max_new < c->tokens ? c->max_new : c->tokens;
   if ((int64_t)max_new * (f.q_heads / f.kv_heads) > (1 << 30))

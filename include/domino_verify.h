@@ -104,8 +104,9 @@ domino_status_t domino_attention_append(domino_attention_t* h, const domino_cach
  * so do tokens that see a key of a page outside [0, num_pages); other tokens
  * of that request may.  window >= 0, sinks >= 0, scale finite and > 0.  q and out rows:
  * token i, head h at i * token_stride + h * head_stride (elements, multiples
- * of 16 bytes); lse is [tokens, q_heads] fp32 or NULL.  max_new and max_kv
- * choose the kernels: bounds near the truth are faster. */
+ * of 16 bytes; out's at least head_dim where there is more than one); lse is
+ * [tokens, q_heads] fp32 or NULL.  max_new and max_kv choose the kernels:
+ * bounds near the truth are faster. */
 domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t* cache,
                                      const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                      int32_t window, int32_t sinks, float scale, void* out,

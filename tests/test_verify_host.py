@@ -33,10 +33,11 @@ def attention(hq=8, hk=2, dim=128, page=16, requests=4, dtype=R.DTYPE_BF16):
     st = lib.domino_attention_create(ctypes.byref(verify.AttentionConfig(hq, hk, dim, page, requests, dtype)), ctypes.byref(h))
     return st, h
 
-def attend(h, kv=4096, width=256, tokens=4, max_new=1, hk=2, dim=128, page=16, requests=4, elem=2, out=(1024, 128)):
+def attend(h, kv=4096, width=256, tokens=4, max_new=1, hk=2, dim=128, page=16, requests=4, out=None):
     c = verify.CacheArgs(1 << 20, 1 << 20, hk * page * dim, page * dim, dim, 4096, 1 << 20, width, width, 1 << 20, 1 << 20,
                          requests, tokens, max_new, kv)
-    return lib.domino_attention_run(h, ctypes.byref(c), P, 1024, 128, 0, 0, 0.1, P, *out, None, None)
+    return lib.domino_attention_run(h, ctypes.byref(c), P, 1024, 128, 0, 0, 0.1, P,
+                                    *(out or (8 * dim, dim)), None, None)
 
 def verifier(vocab=151936, requests=16, rows=16, dtype=R.DTYPE_BF16):
     h = ctypes.c_void_p()
@@ -195,4 +196,16 @@ def test_numbers_beyond_32_bits_are_refused(runtime):
         refused(lambda: verify.PagedAttention(2 ** 32 + 8, 2, 128, 16), "q_heads")
         refused(lambda: verify.PagedAttention(8, 2, 128, 2 ** 32 + 16), "page_size")
         refused(lambda: verify.DraftVerifier(2 ** 32 + 1000), "vocab")
+        """)
+
+
+def test_rows_of_out_that_overlap_are_refused(runtime):
+    """An expanded tensor as the output of attention: several workgroups would write the same place."""
+    walk(runtime, """
+        st, h = attention()
+        for token, head, status in ((1024, 128, 0), (128, 512, 0), (0, 128, R.DOMINO_ERR_INVALID_ARG),
+                                    (1024, 0, R.DOMINO_ERR_INVALID_ARG), (1024, 64, R.DOMINO_ERR_INVALID_ARG)):
+            assert attend(h, out=(token, head)) == status, (token, head)
+        assert b"overlap" in lib.domino_attention_last_error(h)
+        assert attend(h, tokens=1, requests=1, out=(0, 128)) == 0
         """)
