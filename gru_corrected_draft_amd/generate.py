@@ -12,7 +12,9 @@ products are torch's.  A block costs one pass over 16 positions of each request:
 4. the lengths advance by what was accepted.  Keys of refused proposals stay in their pages: they lie
    past the new length, where no token sees them, and the next block overwrites them.
 
-Lengths, page tables and texts stay on the GPU; the host only knows bounds for them.
+Lengths, page tables and texts stay on the GPU; the host only knows bounds for them.  A block may add
+16 tokens to a text and often adds few, so the bound runs ahead of the lengths; where it leaves no room
+for a block, the longest length is read back once.
 """
 from __future__ import annotations
 
@@ -105,6 +107,7 @@ class Generator:
         self.prompt_len = torch.tensor(lens, dtype=torch.int32, device=dev)
         self.length = self.prompt_len.clone()  # of the text; its last token is not in the cache yet
         self.longest = max(lens)  # what the host knows of it: no text is longer
+        self._ahead = False       # whether blocks have run since that was a text's own length
 
         # the prompts, all but their last tokens, in one ragged pass
         cached = [n - 1 for n in lens]
@@ -147,6 +150,8 @@ class Generator:
         Returns (tokens [requests, n + 1], -1 after the last new one, accepted [requests])."""
         b, dev = self.requests, self.text.device
         rows = 1 if proposals is None else proposals.shape[1] + 1
+        if self.longest + rows > self.max_kv and self._ahead:
+            self.longest, self._ahead = int(self.length.max()), False
         if self.longest + rows > self.max_kv:
             raise ValueError("the texts may outgrow max_new")
         tokens = self.last() if proposals is None else torch.cat([self.last(), proposals], 1)
@@ -164,6 +169,7 @@ class Generator:
         self.text.scatter_(1, at, torch.where(new >= 0, new, self.text.gather(1, at)))
         self.length = self.length + (new >= 0).sum(1, dtype=torch.int32)
         self.longest += rows
+        self._ahead = True
         return new, accepted
 
 
