@@ -89,6 +89,10 @@ class Generator:
         lens = [len(p) for p in prompts]
         if not lens or min(lens) < 1:
             raise ValueError("a prompt needs a token")
+        for p in prompts:  # as an index on the GPU, one would end the process
+            ids = torch.as_tensor(p)
+            if int(ids.min()) < 0 or int(ids.max()) >= target.vocab:
+                raise ValueError(f"a prompt's ids must be in [0, {target.vocab})")
         # a block may write up to 15 refused positions past the text
         self.max_kv = max(lens) + max_new + BLOCK
         if self.max_kv > len(target.position):
