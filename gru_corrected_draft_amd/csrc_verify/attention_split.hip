@@ -714,8 +714,11 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   // go through memory), about 10 steps: undivided, one prompt of 1000 tokens over
   // 1000 keys (8.5 steps more than an even share) takes 41 us against 46, but of
   // 512 over 1024 (12.8) 41 against 37, over 2048 (24.8) 68 against 46.
+  // Also where the bounds allow more steps than 32 bits count (from 2^27 keys
+  // with thousands of segments): lengths are not trusted, and a sum that wraps
+  // would lead past the cache.
   const bool prompt = R == 8 || (D == 256 && R == 4);
-  if (seg_most <= 4 || (prompt ? seg_most * (cus - segments) <= 10 * (int64_t)cus
+  if (seg_most <= 4 || segments * seg_most >= (int64_t)1 << 31 || (prompt ? seg_most * (cus - segments) <= 10 * (int64_t)cus
                                : segments >= (R == 4 ? 2 : 8) * (int64_t)cus))
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
   const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;

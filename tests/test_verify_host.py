@@ -209,3 +209,16 @@ def test_rows_of_out_that_overlap_are_refused(runtime):
         assert b"overlap" in lib.domino_attention_last_error(h)
         assert attend(h, tokens=1, requests=1, out=(0, 128)) == 0
         """)
+
+
+def test_bounds_beyond_32_bit_sums_divide_nothing(runtime):
+    """A divided call sums up steps in 32 bits from lengths that lie on the device.  Where the bounds allow more
+    than that holds, each segment is taken whole, in one launch."""
+    walk(runtime, """
+        st, h = attention(hq=256, hk=256, dim=64, page=4096, requests=1)
+        for kv, launches in ((1 << 20, 2), (1 << 29, 2), (1 << 30, 1)):
+            n = rt.host_launches()
+            assert st == 0 and attend(h, kv=kv, width=262144, tokens=1, hk=256, dim=64, page=4096, requests=1,
+                                      out=(1 << 14, 64)) == 0
+            assert rt.host_launches() == n + launches, kv
+        """)
