@@ -44,7 +44,6 @@ struct AttendArgs {
   float* part_ml;  // [slots][rows][2]
   int32_t* plan;   // bf16: [max(requests, 64) + 1]
   int32_t* arrived;  // fp32: [CUs] parts there are of a row tile and key head; 0 between calls
-  int32_t min_share;
   int32_t row_tiles;  // of the longest request there can be
   bool pieces;  // segments cut for themselves
 };

@@ -339,10 +339,15 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   const size_t floats = cfg->dtype == DOMINO_DTYPE_BF16 ? attend_split_floats(cfg->head_dim, h->cus)
                                                         : attend_f32_floats(cfg->head_dim, h->cus);
   h->part = (float*)h->take(floats * sizeof(float));
-  h->plan = (int32_t*)h->take((size_t)((cfg->max_requests < 64 ? 64 : cfg->max_requests) + 1) * sizeof(int32_t));
-  h->arrived = (int32_t*)h->take((size_t)h->cus * sizeof(int32_t));
-  if (!h->part || !h->plan || !h->arrived || hipMemset(h->arrived, 0, (size_t)h->cus * sizeof(int32_t)) != hipSuccess ||
-      hipDeviceSynchronize() != hipSuccess) {
+  bool ok = h->part != nullptr;
+  if (cfg->dtype == DOMINO_DTYPE_BF16) {
+    h->plan = (int32_t*)h->take((size_t)((cfg->max_requests < 64 ? 64 : cfg->max_requests) + 1) * sizeof(int32_t));
+    ok = ok && h->plan;
+  } else {
+    h->arrived = (int32_t*)h->take((size_t)h->cus * sizeof(int32_t));
+    ok = ok && h->arrived && hipMemset(h->arrived, 0, (size_t)h->cus * sizeof(int32_t)) == hipSuccess;
+  }
+  if (!ok || hipDeviceSynchronize() != hipSuccess) {
     (void)hipGetLastError();
     h->release();
     delete h;
@@ -536,7 +541,6 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
     a.part_o = h->part;
     a.part_ml = h->part + attend_split_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;
     a.plan = h->plan;
-    a.min_share = 2;
     launch_attend_split(f.head_dim, a, h->cus, (hipStream_t)stream);
   } else {
     a.part_o = h->part;

@@ -46,6 +46,8 @@
 
 namespace {
 
+constexpr int kMinShare = 2;  // steps: fewer to a workgroup would be all start and end
+
 template <int D, int R>
 struct Shape {
   // R = 2: 4 streams with rings of 2 take as long as 2 with rings of 4 (36.1 and
@@ -173,7 +175,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
         int all = upto;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
-        const int even = max(a.min_share, (all + (int)gridDim.x - 1) / (int)gridDim.x);
+        const int even = max(kMinShare, (all + (int)gridDim.x - 1) / (int)gridDim.x);
         const int steps = upto / a.kv_heads, size = even + lane + (int)((int64_t)even * lane / 63);
         int need = 0;
 #pragma unroll 1
@@ -206,7 +208,7 @@ __global__ __launch_bounds__((Shape<D, R>::kThreads), (D < 256 ? 2 : 1)) void at
       total = carry;
     }
     total = uniform(total);
-    const int share = a.pieces ? 1 : max(a.min_share, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+    const int share = a.pieces ? 1 : max(kMinShare, (total + (int)gridDim.x - 1) / (int)gridDim.x);
     at = blockIdx.x * share;
     end = min(at + share, total);
     if (at >= end) return;
@@ -639,7 +641,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int work
     g1 = g0 + pieces - 1;
   } else {
     const int total = a.plan[a.requests];
-    const int share = max(a.min_share, (total + workers - 1) / workers);
+    const int share = max(kMinShare, (total + workers - 1) / workers);
     int from = from0 + steps_before<ROWS, STEP>(a, req, rt, threadIdx.x & 63);
     const int seg = steps_of(row_tile_span<ROWS>(a, req, rt).count, STEP);
     from += h * seg;
@@ -721,7 +723,7 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   if (seg_most <= 4 || segments * seg_most >= (int64_t)1 << 31 || (prompt ? seg_most * (cus - segments) <= 10 * (int64_t)cus
                                : segments >= (R == 4 ? 2 : 8) * (int64_t)cus))
     return launch_kernel<D, R, true>(a, dim3(a.kv_heads, (unsigned)row_tiles, a.requests), st);
-  const int64_t need = (segments * seg_most + a.min_share - 1) / a.min_share;
+  const int64_t need = (segments * seg_most + kMinShare - 1) / kMinShare;
   const int workers = (int)(need < cus ? need : cus);
   a.row_tiles = (int)row_tiles;
   a.pieces = a.requests * row_tiles <= 64 && 2 * segments <= workers;
