@@ -11,12 +11,12 @@
 //   R = 1: a wave copies its own tiles into its own ring and never waits for
 //          another; no barrier in the walk.  For few rows, bound by the
 //          cache's bytes: 64 requests with one token each over 4 to 8 thousand
-//          keys take 281 us, 5.8 TB/s (a large copy reaches 5.2).
+//          keys take 285 us, 5.7 TB/s (a large copy reaches 5.2).
 //   R > 1: the R waves on a stream share its tiles, each copies a part, and a
 //          barrier separates the steps.  R = 2 and 4 for up to 64 and 128 rows,
 //          so that a draft block of 16 positions with 4 or 8 heads to a key
 //          head reads its keys once: 8 requests over 2 to 4 thousand keys take
-//          35 us, 3.0 TB/s, of which 2.4 find the work, 4 fill the rings and 4.5
+//          36 us, 2.9 TB/s, of which 2.4 find the work, 4 fill the rings and 4.5
 //          join; 16 requests with a window of 4096 70 us, 3.9 TB/s.
 //   R = 8: for prompts; steps of 64 keys (234 us against 262 with 32 for 2
 //          requests of up to 2048 tokens over up to 5120 keys), 970 TFLOP/s

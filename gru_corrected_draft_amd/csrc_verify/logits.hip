@@ -377,10 +377,10 @@ __device__ __forceinline__ float touched_logit(float x, uint32_t c, uint32_t ent
 //   process, history, biases, masks   156 us, 643 MB, 4.1 TB/s (a large copy
 //                                     5.2): memory
 //   verify, greedy, no rules          71 us, 311 MB, 4.4 TB/s
-//   verify, history, masks, T > 0     135 us: vector instructions, busy 81 % of
+//   verify, history, masks, T > 0     136 us: vector instructions, busy 82 % of
 //                                     the time; touched ids read again bring the
 //                                     bytes from 370 to 563 MB
-// and on one block of fp32 logits, where starting and joining are most, 13.7.
+// and on one block of fp32 logits, where starting and joining are most, 14.0.
 template <typename T, bool VERIFY, bool TOUCH>
 __global__ __launch_bounds__(kThreads, 8) void logits_kernel(LogitsArgs a) {
   constexpr int V = Elem<T>::kVec;
@@ -795,7 +795,7 @@ static int longest_range(size_t per_id) {
 // it out: 64 blocks of 151936 ids with 4096 tokens of history, 300 biases and
 // masks took 171 us in two rounds, 164 in three, 160 in four and six; the
 // verification of 64 blocks, whose start takes longer, 144, 144, 151 and 170
-// (135 since, in two).
+// (136 since, in three).
 // requests * ranges is at most requests * (ranges of the longest) + 8 rounds.
 static Cut cut_vocab(int vocab, int cus, int requests, int rows, int vec, size_t per_id, bool touch, bool verify) {
   Cut k;

@@ -4,8 +4,9 @@ that reads it, and the rules on the target's logits with the acceptance of the p
 Thin ctypes binding of ``include/domino_verify.h``; the mathematics of each operator stands there.
 ``PagedAttention`` and ``DraftVerifier`` marshal tensors: every argument is checked for type, shape,
 device and layout, work goes to the current stream of the tensors' device, and the handle must not
-be used by two threads at once.  A handle belongs to the GPU that is current where it is made, and takes
-tensors of that GPU alone.  Importing this module needs the built library; there is no fallback.
+be used by two threads at once, nor on two streams whose work is not ordered.  A handle belongs to the
+GPU that is current where it is made, and takes tensors of that GPU alone.  Importing this module needs
+the built library; there is no fallback.
 """
 from __future__ import annotations
 

@@ -13,8 +13,9 @@
  *   domino_verify_run         the same rules fused with the acceptance of the
  *                             proposals and the choice of the token that follows
  *
- * Conventions are those of domino_rollout.h: a handle owns its workspace and
- * is not re-entrant; every run enqueues kernels on the caller's stream (NULL =
+ * Conventions are those of domino_rollout.h: a handle owns its workspace, on
+ * the device that is current at create, and is not re-entrant (one run in
+ * flight per handle); every run enqueues kernels on the caller's stream (NULL =
  * the default stream), checks host scalars and pointers only, allocates
  * nothing, does not synchronise and may be captured into a graph.  Lengths,
  * page tables and token ids live on the device and are never trusted as
