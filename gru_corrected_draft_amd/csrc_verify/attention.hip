@@ -5,6 +5,7 @@
 
 #include "../../include/domino_verify.h"
 #include "attention_bf16.h"
+#include "fp4.h"
 #include "handle.h"
 
 // ---------------------------------------------------------------- append
@@ -291,6 +292,7 @@ static size_t attend_f32_floats(int head_dim, int cus) { return (size_t)2 * cus 
 // ---------------------------------------------------------------- handle
 struct domino_attention : HandleBase {
   domino_attention_config_t cfg;
+  bool fp4 = false;  // the cache is held in 4 bits
   int cus = 256;
   float* part = nullptr;    // split segments: outputs, then (m, l)
   int32_t* plan = nullptr;     // bf16: running sum of the requests' steps, or of 64 row tiles' pieces
@@ -299,8 +301,7 @@ struct domino_attention : HandleBase {
 
 static thread_local char t_err[256] = "";
 
-extern "C" domino_status_t domino_attention_create(const domino_attention_config_t* cfg,
-                                                   domino_attention_t** out) {
+static domino_status_t create(const domino_attention_config_t* cfg, bool fp4, domino_attention_t** out) {
   if (!out) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: out is NULL");
   *out = nullptr;
   if (!cfg) return say(t_err, DOMINO_ERR_INVALID_ARG, "create: cfg is NULL");
@@ -313,6 +314,8 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   if (cfg->dtype != DOMINO_DTYPE_BF16 && cfg->dtype != DOMINO_DTYPE_FP32)
     return say(t_err, DOMINO_ERR_INVALID_CONFIG,
                "create: dtype must be DOMINO_DTYPE_BF16 or DOMINO_DTYPE_FP32");
+  if (fp4 && cfg->dtype != DOMINO_DTYPE_BF16)
+    return say(t_err, DOMINO_ERR_UNSUPPORTED, "create: a cache in 4 bits takes DOMINO_DTYPE_BF16");
   if (cfg->head_dim != 64 && cfg->head_dim != 128 && cfg->head_dim != 256)
     return say(t_err, DOMINO_ERR_UNSUPPORTED, "create: head_dim must be 64, 128 or 256 (got %d)",
                cfg->head_dim);
@@ -324,13 +327,15 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   int dev = 0;
   domino_status_t st = check_device(t_err, &dev);
   if (st != DOMINO_OK) return st;
-  if (cfg->dtype == DOMINO_DTYPE_BF16 && attend_split_prepare(cfg->head_dim) != hipSuccess) {
+  if (cfg->dtype == DOMINO_DTYPE_BF16 &&
+      (fp4 ? attend_fp4_prepare(cfg->head_dim) : attend_split_prepare(cfg->head_dim)) != hipSuccess) {
     (void)hipGetLastError();
     return say(t_err, DOMINO_ERR_HIP, "create: the kernels' LDS limit could not be set");
   }
   domino_attention* h = new (std::nothrow) domino_attention();
   if (!h) return say(t_err, DOMINO_ERR_OUT_OF_MEMORY, "create: out of host memory");
   h->cfg = *cfg;
+  h->fp4 = fp4;
   h->device = dev;
   if (hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) {
     (void)hipGetLastError();
@@ -357,6 +362,16 @@ extern "C" domino_status_t domino_attention_create(const domino_attention_config
   return DOMINO_OK;
 }
 
+extern "C" domino_status_t domino_attention_create(const domino_attention_config_t* cfg,
+                                                   domino_attention_t** out) {
+  return create(cfg, false, out);
+}
+
+extern "C" domino_status_t domino_attention_create_fp4(const domino_attention_config_t* cfg,
+                                                       domino_attention_t** out) {
+  return create(cfg, true, out);
+}
+
 extern "C" void domino_attention_destroy(domino_attention_t* h) {
   if (!h) return;
   h->release();
@@ -369,7 +384,8 @@ extern "C" const char* domino_attention_last_error(const domino_attention_t* h) 
 
 static domino_status_t check_cache(domino_attention_t* h, const char* who, const domino_cache_t* c) {
   const domino_attention_config_t& f = h->cfg;
-  const int elem = f.dtype == DOMINO_DTYPE_BF16 ? 2 : 4, unit = 16 / elem;
+  // strides count elements; those of a cache in 4 bits bytes
+  const int elem = h->fp4 ? 1 : f.dtype == DOMINO_DTYPE_BF16 ? 2 : 4, unit = 16 / elem;
   if (!c) return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: cache is NULL", who);
   if (!c->k_cache || !c->v_cache || !c->page_table || !c->kv_len || !c->q_start)
     return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: a pointer of the cache is NULL", who);
@@ -385,12 +401,14 @@ static domino_status_t check_cache(domino_attention_t* h, const char* who, const
   if (c->num_pages < 1 || c->table_width < 1 || c->table_stride < 0)
     return say(h->err, DOMINO_ERR_INVALID_ARG,
                "%s: num_pages and table_width must be positive, table_stride >= 0", who);
-  if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < f.head_dim ||
+  if (h->fp4 && c->row_stride != f.head_dim / 2)
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: row_stride must be head_dim / 2 bytes", who);
+  if (c->page_stride < 0 || c->head_stride < 0 || (!h->fp4 && c->row_stride < f.head_dim) ||
       c->page_stride % unit || c->head_stride % unit || c->row_stride % unit)
     return say(h->err, DOMINO_ERR_INVALID_ARG,
                "%s: cache strides must be multiples of 16 bytes, row_stride at least head_dim", who);
-  if (((double)(f.kv_heads - 1) * c->head_stride + (double)f.page_size * c->row_stride) * elem >=
-      2147483648.0)
+  const double page_rows = (double)f.page_size * (h->fp4 ? f.head_dim / 2 + f.head_dim / 32 : c->row_stride);
+  if (((double)(f.kv_heads - 1) * c->head_stride + page_rows) * elem >= 2147483648.0)
     return say(h->err, DOMINO_ERR_INVALID_ARG, "%s: a page must span less than 2^31 bytes", who);
   return DOMINO_OK;
 }
@@ -416,6 +434,35 @@ static domino_status_t launched(domino_attention_t* h, const char* who) {
   return DOMINO_OK;
 }
 
+static RowsArgs4 rows_args(const domino_attention_t* h, const domino_cache_t* c, void* k, int64_t k_token_stride,
+                           int64_t k_head_stride, void* v, int64_t v_token_stride, int64_t v_head_stride) {
+  const domino_attention_config_t& f = h->cfg;
+  RowsArgs4 a;
+  a.tok[0] = k;
+  a.tok[1] = v;
+  a.cache[0] = c->k_cache;
+  a.cache[1] = c->v_cache;
+  a.tok_stride[0] = k_token_stride;
+  a.tok_stride[1] = v_token_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  a.page = c->page_stride;
+  a.head = c->head_stride;
+  a.num_pages = c->num_pages;
+  a.head_dim = f.head_dim;
+  a.table = c->page_table;
+  a.table_stride = c->table_stride;
+  a.page_shift = __builtin_ctz(f.page_size);
+  a.kv_len = c->kv_len;
+  a.q_start = c->q_start;
+  a.requests = c->requests;
+  a.tokens = c->tokens;
+  a.max_new = c->max_new;
+  a.max_kv = clip_kv(c, f.page_size);
+  a.kv_heads = f.kv_heads;
+  return a;
+}
+
 extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const domino_cache_t* c,
                                                    const void* k, int64_t k_token_stride,
                                                    int64_t k_head_stride, const void* v,
@@ -431,6 +478,13 @@ extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const 
   if (!rows_ok(k, k_token_stride, k_head_stride, unit) || !rows_ok(v, v_token_stride, v_head_stride, unit))
     return say(h->err, DOMINO_ERR_INVALID_ARG,
                "append: k and v must be 16-byte aligned, their strides multiples of 16 bytes");
+  if (h->fp4) {
+    const RowsArgs4 a = rows_args(h, c, (void*)k, k_token_stride, k_head_stride, (void*)v, v_token_stride, v_head_stride);
+    DeviceGuard dg(h->device);
+    (void)hipGetLastError();
+    launch_append_fp4(a, (hipStream_t)stream);
+    return launched(h, "append");
+  }
   AppendArgs a;
   a.src[0] = k;
   a.src[1] = v;
@@ -462,6 +516,29 @@ extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const 
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)(blocks < 1024 ? blocks : 1024), 2 * c->requests),
                      dim3(256), 0, (hipStream_t)stream, a);
   return launched(h, "append");
+}
+
+extern "C" domino_status_t domino_attention_read(domino_attention_t* h, const domino_cache_t* c, void* k,
+                                                 int64_t k_token_stride, int64_t k_head_stride, void* v,
+                                                 int64_t v_token_stride, int64_t v_head_stride, void* stream) {
+  if (!h) return DOMINO_ERR_INVALID_ARG;
+  domino_status_t st = check_cache(h, "read", c);
+  if (st != DOMINO_OK) return st;
+  const int dim = h->cfg.head_dim;
+  if (!h->fp4) return say(h->err, DOMINO_ERR_UNSUPPORTED, "read: for caches in 4 bits");
+  if (c->tokens == 0 || c->max_new == 0) return DOMINO_OK;
+  if (!k || !v) return say(h->err, DOMINO_ERR_INVALID_ARG, "read: k and v must be non-NULL");
+  if (!rows_ok(k, k_token_stride, k_head_stride, 8) || !rows_ok(v, v_token_stride, v_head_stride, 8))
+    return say(h->err, DOMINO_ERR_INVALID_ARG,
+               "read: k and v must be 16-byte aligned, their strides multiples of 16 bytes");
+  if ((c->tokens > 1 && (k_token_stride < dim || v_token_stride < dim)) ||
+      (h->cfg.kv_heads > 1 && (k_head_stride < dim || v_head_stride < dim)))
+    return say(h->err, DOMINO_ERR_INVALID_ARG, "read: rows of k or v overlap");
+  const RowsArgs4 a = rows_args(h, c, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride);
+  DeviceGuard dg(h->device);
+  (void)hipGetLastError();
+  launch_read_fp4(a, (hipStream_t)stream);
+  return launched(h, "read");
 }
 
 template <int D>
@@ -541,7 +618,10 @@ extern "C" domino_status_t domino_attention_run(domino_attention_t* h, const dom
     a.part_o = h->part;
     a.part_ml = h->part + attend_split_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;
     a.plan = h->plan;
-    launch_attend_split(f.head_dim, a, h->cus, (hipStream_t)stream);
+    if (h->fp4)
+      launch_attend_fp4(f.head_dim, a, h->cus, (hipStream_t)stream);
+    else
+      launch_attend_split(f.head_dim, a, h->cus, (hipStream_t)stream);
   } else {
     a.part_o = h->part;
     a.part_ml = h->part + attend_f32_floats(f.head_dim, h->cus) / (f.head_dim + 2) * f.head_dim;

@@ -35,6 +35,7 @@ EXPORTED = ("domino_rollout_create", "domino_rollout_run", "domino_rollout_run_g
             "domino_rollout_run_static",
             # declared in domino_verify.h, bound in verify.py
             "domino_attention_create", "domino_attention_append", "domino_attention_run",
+            "domino_attention_create_fp4", "domino_attention_read",
             "domino_attention_destroy", "domino_attention_last_error", "domino_verify_create",
             "domino_verify_process", "domino_verify_run", "domino_verify_destroy",
             "domino_verify_last_error")

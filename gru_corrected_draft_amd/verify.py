@@ -62,11 +62,13 @@ def load_library():
     lib.domino_attention_append.argtypes = [_vp, p(CacheArgs), _vp, _i64, _i64, _vp, _i64, _i64, _vp]
     lib.domino_attention_run.argtypes = [_vp, p(CacheArgs), _vp, _i64, _i64, _i32, _i32, _f32, _vp,
                                          _i64, _i64, _vp, _vp]
+    lib.domino_attention_create_fp4.argtypes = lib.domino_attention_create.argtypes
+    lib.domino_attention_read.argtypes = lib.domino_attention_append.argtypes
     lib.domino_verify_create.argtypes = [p(VerifyConfig), p(_vp)]
     lib.domino_verify_process.argtypes = [_vp, p(LogitsArgs), _vp, _i64, _i64, _vp]
     lib.domino_verify_run.argtypes = [_vp, p(LogitsArgs), _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
     for name in ("domino_attention_create", "domino_attention_append", "domino_attention_run",
-                 "domino_verify_create", "domino_verify_process", "domino_verify_run"):
+                 "domino_attention_create_fp4", "domino_attention_read", "domino_verify_create", "domino_verify_process", "domino_verify_run"):
         getattr(lib, name).restype = ctypes.c_int
     for name in ("domino_attention_destroy", "domino_verify_destroy"):
         getattr(lib, name).argtypes = [_vp]
@@ -108,12 +110,12 @@ _stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Handle:
-    def __init__(self, kind, cfg):
+    def __init__(self, kind, cfg, create="create"):
         self.lib = load_library()
         self._destroy = getattr(self.lib, f"domino_{kind}_destroy")
         self._error = getattr(self.lib, f"domino_{kind}_last_error")
         h = _vp()
-        st = getattr(self.lib, f"domino_{kind}_create")(ctypes.byref(cfg), ctypes.byref(h))
+        st = getattr(self.lib, f"domino_{kind}_{create}")(ctypes.byref(cfg), ctypes.byref(h))
         if st:
             raise DominoError(st, self._error(None).decode())
         self.handle = h
@@ -154,22 +156,29 @@ class PagedAttention(_Handle):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
         sizes = dict(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, max_requests=max_requests)
-        super().__init__("attention", AttentionConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]))
+        super().__init__("attention", AttentionConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]),
+                         self._create)
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype = page_size, dtype
         self._scale = 1.0 / math.sqrt(head_dim)
 
+    _create = "create"
+
+    def _layout(self, k_cache):
+        """Type and shape of a cache of as many pages, and the step between rows where it is not a stride."""
+        return self.dtype, (k_cache.shape[0] if k_cache.dim() else 0, self.kv_heads, self.page_size, self.head_dim), None
+
     def _cache(self, k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index):
-        shape = (k_cache.shape[0] if k_cache.dim() else 0, self.kv_heads, self.page_size, self.head_dim)
+        dtype, shape, row = self._layout(k_cache)
         strides = k_cache.stride()
         b, width = page_table.shape if page_table.dim() == 2 else (-1, -1)
-        if not (_fits(k_cache, self.dtype, shape, index) and _fits(v_cache, self.dtype, shape, index)
-                and v_cache.stride() == strides and strides[3] == 1 and index == self.index
+        if not (_fits(k_cache, dtype, shape, index) and _fits(v_cache, dtype, shape, index)
+                and v_cache.stride() == strides and strides[-1] == 1 and index == self.index
                 and _fits(page_table, torch.int32, (b, width), index) and _fits(kv_len, torch.int32, (b,), index)
                 and _fits(q_start, torch.int32, (b + 1,), index) and page_table.stride(1) == 1
                 and kv_len.stride(0) == 1 and q_start.stride(0) == 1):
-            _want("k_cache", k_cache, self.dtype, shape, index)
-            _want("v_cache", v_cache, self.dtype, shape, index)
+            _want("k_cache", k_cache, dtype, shape, index)
+            _want("v_cache", v_cache, dtype, shape, index)
             if v_cache.stride() != strides:
                 raise ValueError("k_cache and v_cache must have the same strides")
             _want("page_table", page_table, torch.int32, (b, width), index)
@@ -184,7 +193,7 @@ class PagedAttention(_Handle):
         if (max_new | max_kv) >> 31:  # negative ones are the library's to refuse
             _int32("max_new", max_new)
             _int32("max_kv", max_kv)
-        return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
+        return CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], row or strides[2], shape[0],
                          page_table.data_ptr(), page_table.stride(0), width, kv_len.data_ptr(),
                          q_start.data_ptr(), b, tokens, max_new, max_kv)
 
@@ -232,6 +241,40 @@ class PagedAttention(_Handle):
         if st:
             self._check(st)
         return (out, lse) if return_lse else out
+
+
+class PagedAttention4(PagedAttention):
+    """``PagedAttention`` in bfloat16 over a cache held in 4 bits, with the same calls.
+
+    ``k_cache`` and ``v_cache`` are [pages, kv_heads, page_bytes] uint8 tensors with the same strides
+    (multiples of 16) and a contiguous last dimension: page_size rows of head_dim / 2 bytes, two elements
+    in each, and page_size rows of head_dim / 32 bytes, the powers of two of 32 elements each.  What is
+    stored is the nearest such number; ``read`` gives it back.
+    """
+
+    _create = "create_fp4"
+
+    def __init__(self, q_heads, kv_heads, head_dim, page_size, max_requests=64):
+        super().__init__(q_heads, kv_heads, head_dim, page_size, torch.bfloat16, max_requests)
+        self.page_bytes = page_size * (head_dim // 2 + head_dim // 32)
+
+    def _layout(self, k_cache):
+        shape = (k_cache.shape[0] if k_cache.dim() else 0, self.kv_heads, self.page_bytes)
+        return torch.uint8, shape, self.head_dim // 2
+
+    def read(self, tokens, k_cache, v_cache, page_table, kv_len, q_start, max_new=None, max_kv=None):
+        """Keys and values, each [tokens, kv_heads, head_dim], that the cache holds at the positions of
+        the new tokens.  Rows that belong to no request are not written."""
+        if tokens < 0:
+            raise ValueError("tokens must be at least 0")
+        index, shape = k_cache.get_device(), (_int32("tokens", tokens), self.kv_heads, self.head_dim)
+        c = self._cache(k_cache, v_cache, page_table, kv_len, q_start, tokens, max_new, max_kv, index)
+        k, v = (torch.empty(shape, dtype=self.dtype, device=k_cache.device) for _ in range(2))
+        st = self.lib.domino_attention_read(self.handle, ctypes.byref(c), k.data_ptr(), shape[1] * shape[2], shape[2],
+                                            v.data_ptr(), shape[1] * shape[2], shape[2], _stream(index))
+        if st:
+            self._check(st)
+        return k, v
 
 
 class DraftVerifier(_Handle):

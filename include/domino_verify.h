@@ -9,6 +9,7 @@
  * around the target's own matrix products:
  *   domino_attention_append   keys and values of the new tokens into pages
  *   domino_attention_run      causal attention of the new tokens over the pages
+ *   domino_attention_create_fp4, _read   the same over a cache held in 4 bits
  *   domino_verify_process     penalties, biases and grammar masks on logits
  *   domino_verify_run         the same rules fused with the acceptance of the
  *                             proposals and the choice of the token that follows
@@ -113,6 +114,40 @@ domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t
                                      int32_t window, int32_t sinks, float scale, void* out,
                                      int64_t out_token_stride, int64_t out_head_stride, float* lse,
                                      void* stream);
+
+/* ---- a cache held in 4 bits
+ *
+ * A handle of domino_attention_create_fp4 takes the calls of one of
+ * domino_attention_create, with queries, new keys and values and outputs in
+ * bf16 (dtype must be DOMINO_DTYPE_BF16) and a cache in which 32 elements of a
+ * token and key head, a block, share a power of two 2^e.  Its byte holds e + 127,
+ * 255 makes the block NaN; an element is 4 bits, the upper one a sign and the
+ * lower three the number 0, 0.5, 1, 1.5, 2, 3, 4, 6 of that index.  In a page of a head lie
+ *   page_size x head_dim / 2 bytes: elements, row after row, the lower element
+ *     of two in the low bits of a byte;
+ *   page_size x head_dim / 32 bytes: powers, row after row.
+ * page_stride and head_stride of the cache count bytes and are multiples of 16,
+ * row_stride must be head_dim / 2.
+ *
+ * Append gives a block the least e with max |x| <= 7 x 2^e, kept within
+ * [-125, 125], and each element the nearest number, of two the one of even
+ * index, at most 6; a block with an infinity or NaN becomes NaN.  Numbers up to
+ * 6 x 2^e are off by at most half a step of the numbers around them, others by
+ * at most 2^e (the largest bf16 numbers, from 7 x 2^125 on, become 6 x 2^125).  Run
+ * computes its formula over the numbers that the cache stands for, which bf16
+ * holds exactly; blocks of NaN and unseen keys have the effects stated there.  Powers of 2^-126
+ * and less may count as zero. */
+domino_status_t domino_attention_create_fp4(const domino_attention_config_t* cfg,
+                                            domino_attention_t** out);
+
+/* Gives back what the cache of 4 bits stands for at the positions of the new
+ * tokens: rows of k and v as in append, written in bf16 (at least head_dim
+ * apart).  Tokens of a malformed request (its first max_new rows within
+ * [0, tokens)), at a negative position, or whose page id is outside
+ * [0, num_pages) get NaN. */
+domino_status_t domino_attention_read(domino_attention_t* h, const domino_cache_t* cache, void* k,
+                                      int64_t k_token_stride, int64_t k_head_stride, void* v,
+                                      int64_t v_token_stride, int64_t v_head_stride, void* stream);
 
 /* Frees the workspace.  NULL is a no-op. */
 void domino_attention_destroy(domino_attention_t* h);
