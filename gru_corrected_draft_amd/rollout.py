@@ -38,7 +38,9 @@ EXPORTED = ("domino_rollout_create", "domino_rollout_run", "domino_rollout_run_g
             "domino_attention_create_fp4", "domino_attention_read",
             "domino_attention_destroy", "domino_attention_last_error", "domino_verify_create",
             "domino_verify_process", "domino_verify_run", "domino_verify_destroy",
-            "domino_verify_last_error")
+            "domino_verify_last_error", "domino_rotation_create", "domino_rotation_run",
+            "domino_rotation_destroy", "domino_rotation_last_error", "domino_scores_create",
+            "domino_scores_run", "domino_scores_destroy", "domino_scores_last_error")
 STATIC_SCRATCH_BYTES = 4 << 20  # DOMINO_STATIC_SCRATCH_BYTES
 GRAPH_CACHE_MAX = 16  # DOMINO_GRAPH_CACHE_MAX
 # gru: the GRU gates (prefix launch, separate gate kernel); step: projector

@@ -1,8 +1,9 @@
-"""Operators around the verification of a draft block: a paged key-value cache with the attention
-that reads it, and the rules on the target's logits with the acceptance of the proposals.
+"""Operators around the verification of a draft block: norms and rotation of the target's heads, a paged
+key-value cache with the attention that reads it, the rules on the target's logits with the acceptance of
+the proposals, and the scores of tokens.
 
 Thin ctypes binding of ``include/domino_verify.h``; the mathematics of each operator stands there.
-``PagedAttention`` and ``DraftVerifier`` marshal tensors: every argument is checked for type, shape,
+The classes marshal tensors: every argument is checked for type, shape,
 device and layout, work goes to the current stream of the tensors' device, and the handle must not
 be used by two threads at once, nor on two streams whose work is not ordered.  A handle belongs to the
 GPU that is current where it is made, and takes tensors of that GPU alone.  Importing this module needs
@@ -32,6 +33,20 @@ class CacheArgs(ctypes.Structure):
                 ("row_stride", _i64), ("num_pages", _i32), ("page_table", _vp), ("table_stride", _i64),
                 ("table_width", _i32), ("kv_len", _vp), ("q_start", _vp), ("requests", _i32),
                 ("tokens", _i32), ("max_new", _i32), ("max_kv", _i32)]
+
+
+class RotationConfig(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in
+                ("q_heads", "kv_heads", "head_dim", "rotary_dim", "dtype", "interleaved")] + [("magnitude", _f32)]
+
+
+class HeadsArgs(ctypes.Structure):
+    _fields_ = [("input", _vp), ("token_stride", _i64), ("head_stride", _i64), ("weight", _vp), ("out", _vp),
+                ("out_token_stride", _i64), ("out_head_stride", _i64)]
+
+
+class ScoresConfig(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("vocab", "max_rows", "max_top", "dtype")]
 
 
 class VerifyConfig(ctypes.Structure):
@@ -67,13 +82,20 @@ def load_library():
     lib.domino_verify_create.argtypes = [p(VerifyConfig), p(_vp)]
     lib.domino_verify_process.argtypes = [_vp, p(LogitsArgs), _vp, _i64, _i64, _vp]
     lib.domino_verify_run.argtypes = [_vp, p(LogitsArgs), _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
-    for name in ("domino_attention_create", "domino_attention_append", "domino_attention_run",
+    lib.domino_rotation_create.argtypes = [p(RotationConfig), p(ctypes.c_double), p(_vp)]
+    lib.domino_rotation_run.argtypes = [_vp, p(HeadsArgs), p(HeadsArgs), _vp, _i32, _f32, _vp]
+    lib.domino_scores_create.argtypes = [p(ScoresConfig), p(_vp)]
+    lib.domino_scores_run.argtypes = [_vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
+    for name in ("domino_rotation_create", "domino_rotation_run", "domino_scores_create", "domino_scores_run",
+                 "domino_attention_create", "domino_attention_append", "domino_attention_run",
                  "domino_attention_create_fp4", "domino_attention_read", "domino_verify_create", "domino_verify_process", "domino_verify_run"):
         getattr(lib, name).restype = ctypes.c_int
-    for name in ("domino_attention_destroy", "domino_verify_destroy"):
+    for name in ("domino_attention_destroy", "domino_verify_destroy", "domino_rotation_destroy",
+                 "domino_scores_destroy"):
         getattr(lib, name).argtypes = [_vp]
         getattr(lib, name).restype = None
-    for name in ("domino_attention_last_error", "domino_verify_last_error"):
+    for name in ("domino_attention_last_error", "domino_verify_last_error", "domino_rotation_last_error",
+                 "domino_scores_last_error"):
         getattr(lib, name).argtypes = [_vp]
         getattr(lib, name).restype = ctypes.c_char_p
     _lib = lib
@@ -110,12 +132,12 @@ _stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Handle:
-    def __init__(self, kind, cfg, create="create"):
+    def __init__(self, kind, *args, create="create"):
         self.lib = load_library()
         self._destroy = getattr(self.lib, f"domino_{kind}_destroy")
         self._error = getattr(self.lib, f"domino_{kind}_last_error")
         h = _vp()
-        st = getattr(self.lib, f"domino_{kind}_{create}")(ctypes.byref(cfg), ctypes.byref(h))
+        st = getattr(self.lib, f"domino_{kind}_{create}")(*args, ctypes.byref(h))
         if st:
             raise DominoError(st, self._error(None).decode())
         self.handle = h
@@ -140,6 +162,61 @@ class _Handle:
             pass
 
 
+class HeadRotation(_Handle):
+    """Norms of query and key heads and their rotation by position, in one pass.
+
+    ``inv_freq`` holds the frequencies in radians a position, one for each pair of elements (a sequence or
+    tensor of float64; 1e6 ** (-2 i / head_dim) for instance, scaled as the model has it): twice as many
+    elements of a head are rotated, element i with i + len(inv_freq), or 2 i with 2 i + 1 if
+    ``interleaved``, and the rest is left.  ``magnitude`` multiplies cosines and sines.
+    """
+
+    def __init__(self, q_heads, kv_heads, head_dim, inv_freq, dtype=torch.bfloat16, interleaved=False,
+                 magnitude=1.0):
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+        freq = [float(x) for x in inv_freq]
+        sizes = dict(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, rotary_dim=2 * len(freq))
+        cfg = RotationConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype], bool(interleaved), magnitude)
+        super().__init__("rotation", ctypes.byref(cfg), (ctypes.c_double * len(freq))(*freq))
+        self.q_heads, self.kv_heads, self.head_dim, self.dtype = q_heads, kv_heads, head_dim, dtype
+
+    def run(self, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, out_q=None, out_k=None):
+        """Normalises (with ``q_weight`` and ``k_weight`` [head_dim]; without them not) and rotates ``q``
+        [tokens, q_heads, head_dim] and ``k`` [tokens, kv_heads, head_dim] by ``positions`` [tokens] int32;
+        returns both.  Rows of tokens with a negative position are not written.  ``out_q`` and ``out_k``
+        may be q and k."""
+        tokens, index = q.shape[0], q.get_device()
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight must be given together")
+        heads = []
+        for name, x, n, weight, out in (("q", q, self.q_heads, q_weight, out_q), ("k", k, self.kv_heads, k_weight, out_k)):
+            shape, xs = (tokens, n, self.head_dim), x.stride()
+            if not (_fits(x, self.dtype, shape, index) and xs[2] == 1):
+                _want(name, x, self.dtype, shape, index)
+            if weight is not None:
+                _want(f"{name}_weight", weight, self.dtype, (self.head_dim,), index)
+            if out is None:
+                out = torch.empty(shape, dtype=self.dtype, device=x.device)
+            else:
+                _want(f"out_{name}", out, self.dtype, shape, index)
+                if out.data_ptr() == x.data_ptr() and out.stride() != xs:
+                    raise ValueError(f"out_{name} over {name} must have its strides")
+            os = out.stride()
+            heads.append((HeadsArgs(x.data_ptr(), xs[0], xs[1], None if weight is None else weight.data_ptr(),
+                                    out.data_ptr(), os[0], os[1]), out))
+        if not (_fits(positions, torch.int32, (tokens,), index) and positions.stride(0) == 1):
+            _want("positions", positions, torch.int32, (tokens,), index)
+        if index != self.index:
+            raise self._elsewhere(index)
+        (q_args, out_q), (k_args, out_k) = heads
+        st = self.lib.domino_rotation_run(self.handle, ctypes.byref(q_args), ctypes.byref(k_args),
+                                          positions.data_ptr(), tokens, eps, _stream(index))
+        if st:
+            self._check(st)
+        return out_q, out_k
+
+
 class PagedAttention(_Handle):
     """Key-value cache in pages and the attention of new tokens over it.
 
@@ -156,8 +233,8 @@ class PagedAttention(_Handle):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
         sizes = dict(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, page_size=page_size, max_requests=max_requests)
-        super().__init__("attention", AttentionConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]),
-                         self._create)
+        cfg = AttentionConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype])
+        super().__init__("attention", ctypes.byref(cfg), create=self._create)
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype = page_size, dtype
         self._scale = 1.0 / math.sqrt(head_dim)
@@ -294,7 +371,7 @@ class DraftVerifier(_Handle):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
         sizes = dict(vocab=vocab, max_requests=max_requests, max_rows=max_rows)
-        super().__init__("verify", VerifyConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype]))
+        super().__init__("verify", ctypes.byref(VerifyConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype])))
         self.vocab, self.dtype = vocab, dtype
 
     def _args(self, logits, draft, draft_len, history, history_len, prompt_len, repetition, frequency,
@@ -400,3 +477,49 @@ class DraftVerifier(_Handle):
         if st:
             self._check(st)
         return (tokens, accepted, logprob) if return_logprob else (tokens, accepted)
+
+
+class TokenScores(_Handle):
+    """Log-probabilities of given tokens, entropies and the likeliest ids of rows of logits.
+
+    ``logits`` is [rows, vocab] in the handle's dtype, rows at any stride ([requests, rows, vocab] logits are
+    flattened).  ``max_top`` bounds the ids of a row that can be asked for (up to 64; with 0 the handle
+    needs no memory for them).
+    """
+
+    def __init__(self, vocab, dtype=torch.bfloat16, max_rows=1024, max_top=64):
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+        sizes = dict(vocab=vocab, max_rows=max_rows, max_top=max_top)
+        super().__init__("scores", ctypes.byref(ScoresConfig(*(_int32(n, x) for n, x in sizes.items()), _DTYPES[dtype])))
+        self.vocab, self.dtype, self.max_top = vocab, dtype, max_top
+
+    def run(self, logits, tokens=None, top=0):
+        """Returns (logprob, entropy, ids, values): the log-probability of ``tokens`` [rows] int32 (None
+        without them; -inf for a token outside the vocabulary), the entropy of each row [rows], and the
+        ``top`` likeliest ids [rows, top] int32 with their log-probabilities (None, None for 0), the
+        lower id first among equal logits, -1 and -inf where a row has no more."""
+        rows, index, dev = logits.shape[0], logits.get_device(), logits.device
+        if not (_fits(logits, self.dtype, (rows, self.vocab), index) and logits.stride(1) == 1):
+            _want("logits", logits, self.dtype, (rows, self.vocab), index)
+        if index != self.index:
+            raise self._elsewhere(index)
+        if not 0 <= top <= self.max_top:
+            raise ValueError(f"top must be in [0, {self.max_top}], got {top}")
+        logprob = ids = values = None
+        if tokens is not None:
+            if not (_fits(tokens, torch.int32, (rows,), index) and tokens.stride(0) == 1):
+                _want("tokens", tokens, torch.int32, (rows,), index)
+            logprob = torch.empty((rows,), dtype=torch.float32, device=dev)
+        entropy = torch.empty((rows,), dtype=torch.float32, device=dev)
+        if top:
+            ids = torch.empty((rows, top), dtype=torch.int32, device=dev)
+            values = torch.empty((rows, top), dtype=torch.float32, device=dev)
+        st = self.lib.domino_scores_run(self.handle, logits.data_ptr(), logits.stride(0), rows,
+                                        None if tokens is None else tokens.data_ptr(), top,
+                                        None if tokens is None else logprob.data_ptr(), entropy.data_ptr(),
+                                        ids.data_ptr() if top else None, values.data_ptr() if top else None,
+                                        _stream(index))
+        if st:
+            self._check(st)
+        return logprob, entropy, ids, values

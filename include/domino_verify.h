@@ -7,12 +7,15 @@
  * A rollout (domino_rollout.h) proposes up to 15 tokens for each request.  The
  * target model scores the block in one pass; these operators carry that pass
  * around the target's own matrix products:
+ *   domino_rotation_run       norms of query and key heads, rotation by position
  *   domino_attention_append   keys and values of the new tokens into pages
  *   domino_attention_run      causal attention of the new tokens over the pages
  *   domino_attention_create_fp4, _read   the same over a cache held in 4 bits
  *   domino_verify_process     penalties, biases and grammar masks on logits
  *   domino_verify_run         the same rules fused with the acceptance of the
  *                             proposals and the choice of the token that follows
+ *   domino_scores_run         log-probabilities of given tokens, entropies and the
+ *                             likeliest ids of rows of logits
  *
  * Conventions are those of domino_rollout.h: a handle owns its workspace, on
  * the device that is current at create, and is not re-entrant (one run in
@@ -31,6 +34,56 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* ------------------------------------------------------------ norm and rotation of heads */
+
+typedef struct {
+  int32_t q_heads;      /* 1..1024                                              */
+  int32_t kv_heads;     /* 1..1024                                              */
+  int32_t head_dim;     /* D: 64, 128 or 256                                    */
+  int32_t rotary_dim;   /* R: elements that are rotated, a multiple of 16, <= D */
+  int32_t dtype;        /* domino_dtype_t of heads and weights                  */
+  int32_t interleaved;  /* 0: element i turns with i + R / 2; 1: 2i with 2i + 1 */
+  float magnitude;      /* factor of cosines and sines, usually 1               */
+} domino_rotation_config_t;
+
+typedef struct domino_rotation domino_rotation_t;
+
+/* Heads of one kind (device pointers): token i, head h at
+ * in + i * token_stride + h * head_stride (elements), out alike; arrays are
+ * 16-byte aligned and strides multiples of 16 bytes, out's at least head_dim
+ * where there is more than one.  out may be in with the same strides; any other
+ * overlap is undefined. */
+typedef struct {
+  const void* in;
+  int64_t token_stride, head_stride;
+  const void* weight;   /* [head_dim] or NULL: no norm                          */
+  void* out;
+  int64_t out_token_stride, out_head_stride;
+} domino_heads_t;
+
+/* Validates the configuration, checks that the current HIP device is gfx950
+ * and keeps the frequencies inv_freq[rotary_dim / 2] (host memory, radians a
+ * position, finite and within 1000 of 0).  Synchronises the device. */
+domino_status_t domino_rotation_create(const domino_rotation_config_t* cfg, const double* inv_freq,
+                                       domino_rotation_t** out);
+
+/* For each token i and head, x its elements and p = positions[i]:
+ *   y = x / sqrt(mean(x^2) + eps) * weight       (y = x without weights)
+ *   a' = magnitude * (a cos(p f_j) - b sin(p f_j))
+ *   b' = magnitude * (b cos(p f_j) + a sin(p f_j))   for the pairs (a, b) of y, j < R / 2
+ * and elements from R on are y.  The weights of q and k are given together or
+ * not at all.  All of it is fp32 and rounded once; the angle is formed in 64
+ * bits, so that any position is as good as the first.  Tokens with a negative
+ * position are not written.  eps >= 0 and finite. */
+domino_status_t domino_rotation_run(domino_rotation_t* h, const domino_heads_t* q, const domino_heads_t* k,
+                                    const int32_t* positions, int32_t tokens, float eps, void* stream);
+
+/* Frees the workspace.  NULL is a no-op. */
+void domino_rotation_destroy(domino_rotation_t* h);
+
+/* As domino_attention_last_error. */
+const char* domino_rotation_last_error(const domino_rotation_t* h);
 
 /* ------------------------------------------------------------ paged attention */
 
@@ -248,6 +301,42 @@ void domino_verify_destroy(domino_verify_t* h);
 
 /* As domino_attention_last_error. */
 const char* domino_verify_last_error(const domino_verify_t* h);
+
+/* ------------------------------------------------------------ scores of tokens */
+
+typedef struct {
+  int32_t vocab;     /* V, 1..2^24                                             */
+  int32_t max_rows;  /* 1..65535                                               */
+  int32_t max_top;   /* 0..64: the most ids of a row that are asked for        */
+  int32_t dtype;     /* domino_dtype_t of the logits                           */
+} domino_scores_config_t;
+
+typedef struct domino_scores domino_scores_t;
+
+/* Validates the configuration, checks that the current HIP device is gfx950
+ * and allocates the workspace (statistics of parts of rows and, with max_top,
+ * V / 8 bytes a row).  Synchronises the device. */
+domino_status_t domino_scores_create(const domino_scores_config_t* cfg, domino_scores_t** out);
+
+/* Scores of rows of logits, row i at logits + i * row_stride (elements, >= 0).  With
+ * p = softmax(x) of a row's logits x:
+ *   logprob  [rows] fp32: ln p(tokens[i]); -inf for a token outside [0, V) or of x = -inf
+ *   entropy  [rows] fp32: -sum p ln p
+ *   top_ids  [rows, top] int32, top_logprob [rows, top] fp32: the ids of the
+ *            `top` largest x, largest first and the lower id first among equal
+ *            ones, with ln p; ids of x = -inf are none, -1 and -inf in their place
+ * Each is optional (NULL; top 0); tokens and logprob, and the outputs of top, go
+ * together.  NaN logits count as -inf and +inf as the largest fp32 number.  A row
+ * without x > -inf has entropy 0.  Sums are fp32. */
+domino_status_t domino_scores_run(domino_scores_t* h, const void* logits, int64_t row_stride, int32_t rows,
+                                  const int32_t* tokens, int32_t top, float* logprob, float* entropy,
+                                  int32_t* top_ids, float* top_logprob, void* stream);
+
+/* Frees the workspace.  NULL is a no-op. */
+void domino_scores_destroy(domino_scores_t* h);
+
+/* As domino_attention_last_error. */
+const char* domino_scores_last_error(const domino_scores_t* h);
 
 #ifdef __cplusplus
 }
