@@ -1,0 +1,439 @@
+// Attention of few rows over a cache in 4 bits: up to 64 rows of a request and
+// key head (a token of many heads, a draft block).
+//
+// Each wave works alone: it takes every S-th tile of 32 keys of its workgroup's
+// run of them, reads K and V straight into registers, a tile ahead of their
+// use, and keeps the sums of 16 G rows.  Products are 16 x 16 x 32, with both
+// results transposed: S^T = K Q^T (keys x rows) and O^T = V^T P^T.  Lane l (n = l % 16,
+// q = l / 16) holds row n, of S the keys 4 q .. 4 q + 3 of both halves of the
+// tile, which are its slots of the second product's operand, and of O the elements
+// 16 x + 4 q .. + 3 of block x.
+//   K: lane l converts elements q D / 4 .. of key n of a half: fragments as they
+//      are, with the queries' elements dealt alike.
+//   V: bf16 rows go through 64 D bytes of LDS of the wave's own for the transposing
+//      read, swizzled as in KeyTile.
+// For more than 32 rows H = 2 waves take the same keys for 32 rows each.
+#pragma once
+#include "fp4.h"
+
+namespace {
+
+__device__ __forceinline__ v4f mfma_16x16(v8s a, v8s b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// over the four lanes that hold a row
+__device__ __forceinline__ float max_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// a quarter of a row: D / 4 elements and their powers
+template <int D>
+struct Quarter {
+  static constexpr int kWords = D / 32;
+  uint32_t x[kWords];
+  uint32_t powers;
+  static __device__ __forceinline__ uint32_t data_at(int row, int part) { return row * (D / 2) + part * (D / 8); }
+  static __device__ __forceinline__ uint32_t power_at(int row, int part) {
+    return row * (D / 32) + (D == 64 ? part >> 1 : part * (D / 128));
+  }
+  __device__ __forceinline__ void load(const char* data, const char* power) {
+    if constexpr (D == 64) {
+      const u32x2 v = *(const u32x2*)data;
+      x[0] = v[0];
+      x[1] = v[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const u32x4 v = *(const u32x4*)(data + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
+      }
+    }
+    if constexpr (D == 256)
+      powers = *(const uint16_t*)power;
+    else
+      powers = *(const uint8_t*)power;
+  }
+  // word i's power
+  __device__ __forceinline__ float power(int i) const {
+    return power_of(D == 256 ? (powers >> (8 * (i / 4))) & 255 : powers);
+  }
+};
+
+template <int D, int G, int H, int S>
+struct FewShape {
+  static constexpr int kRows = 16 * G * H;
+  static constexpr int kThreads = 64 * H * S;
+  static constexpr int kTile = 64 * D;  // V of a tile in bf16; also 16 rows of sums
+  static constexpr int kLds = H * S * kTile;
+};
+
+// tiles of the chunk that a workgroup takes; none for a chunk past the last
+struct Chunk {
+  int first, stop, chunks;
+};
+__device__ __forceinline__ Chunk chunk_of(int count, int chunk, int per) {
+  Chunk c;
+  c.chunks = count > per ? (count + per - 1) / per : 1;
+  c.first = (int)((int64_t)count * chunk / c.chunks);
+  c.stop = (int)((int64_t)count * (chunk + 1) / c.chunks);
+  return c;
+}
+
+template <int D, int G, int H, int S>
+__global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 : 1)) void attend_few_kernel(AttendArgs a, int chunks, int per) {
+  using T = KeyTile<D>;
+  using C = FewShape<D, G, H, S>;
+  constexpr int DT = D / 16, KC = D / 32, W = H * S;
+  extern __shared__ __align__(1024) unsigned char s_tiles[];
+  __shared__ float s_m[W][16 * G], s_l[W][16 * G], s_f[W][16];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 15, q = lane >> 4;
+  const int half = w % H, stream = w / H;
+  const int b = blockIdx.y, h = blockIdx.x % a.kv_heads, chunk = blockIdx.x / a.kv_heads;
+  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  const int rows = req.n * a.group;
+  if (rows == 0) return;
+  const KeySpan span = uniform(key_span<32>(req, 0, req.n - 1, a.window, a.sinks));
+  const Chunk range = chunk_of(span.count, chunk, per);
+  if (chunk >= range.chunks) return;
+
+  // this wave's rows
+  const int w0 = half * 16 * G;
+  int pos[G];
+  v8s Q[G][KC];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int row = min(w0 + 16 * g + n, rows - 1), tok = row / a.group;
+    pos[g] = req.kv - req.n + tok;
+    const bf16_t* qp = (const bf16_t*)a.q + (req.q0 + tok) * a.q_tok + (h * a.group + row - tok * a.group) * a.q_head + q * (D / 4);
+#pragma unroll
+    for (int c = 0; c < KC; ++c) Q[g][c] = load_frag_bf16(qp + 8 * c);
+  }
+  KeySpan seen = span;
+  seen.pmin = uniform(req.kv - req.n + min(w0, rows - 1) / a.group);
+  seen.pmax = uniform(req.kv - req.n + min(w0 + 16 * G - 1, rows - 1) / a.group);
+
+  v4f o[G][DT];
+  float m[G], l[G];
+  uint32_t note[G];  // blocks of a row's output that are NaN
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    m[g] = -INFINITY;
+    l[g] = 0.f;
+    note[g] = 0;
+#pragma unroll
+    for (int x = 0; x < DT; ++x) o[g][x] = zero4();
+  }
+  bool bad = req.bad;
+
+  const_i32* const table = (const_i32*)(a.table + b * a.table_stride);
+  const uint64_t head = (uint64_t)h * (uint64_t)a.head, page_bytes = (uint64_t)a.page;
+  const int page_mask = (1 << a.page_shift) - 1;
+  lds_byte* const tile = (lds_byte*)s_tiles + w * C::kTile;
+  // V: rows that meet in different banks when they are written
+  const int v_row = (lane >> 2 & 3) * 4 + (lane >> 4), v_part = lane & 3;
+  const uint32_t k_data = Quarter<D>::data_at(n, q), k_power = Quarter<D>::power_at(n, q);
+  const uint32_t v_data = Quarter<D>::data_at(v_row, v_part), v_power = Quarter<D>::power_at(v_row, v_part);
+
+  Quarter<D> K[2], V[2];
+  int page[2] = {0, 0}, key = 0;
+  auto look_up = [&](int i) {
+    key = tile_of(span, i) * 32;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int k = key + 16 * t;
+      const bool any = k < span.hi && (k + 15 >= span.lo || k < a.sinks);
+      page[t] = table[(any ? k : key + 16 * (1 - t)) >> a.page_shift];
+    }
+  };
+  auto load = [&]() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int p = page[t];
+      if ((uint32_t)p >= (uint32_t)a.num_pages) {
+        bad = true;
+        p = 0;
+      }
+      const uint32_t row = (uint32_t)(key + 16 * t) & page_mask;
+      const uint64_t at = (uint32_t)p * page_bytes + head, data = at + row * (D / 2);
+      const uint64_t power = at + ((uint64_t)(D / 2) << a.page_shift) + row * (D / 32);
+      K[t].load((const char*)a.k + data + k_data, (const char*)a.k + power + k_power);
+      V[t].load((const char*)a.v + data + v_data, (const char*)a.v + power + v_power);
+    }
+  };
+  int i = range.first + stream;
+  if (i < range.stop) {
+    look_up(i);
+    load();
+  }
+#pragma unroll 1
+  for (; i < range.stop; i += S) {
+    const int at = key;  // of this tile
+    if (i + S < range.stop) look_up(i + S);
+    const bool whole = all_visible(seen, at, 32, a.window, a.sinks);
+    // scores, and V on its way through LDS
+    v4f s[G][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) s[g][t] = zero4();
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const v8s k = from_fp4(K[t].x[c], K[t].power(c));
+#pragma unroll
+        for (int g = 0; g < G; ++g) s[g][t] = mfma_16x16(k, Q[g][c], s[g][t]);
+      }
+    }
+    if (!whole) {
+      // Blocks of V that are not finite: a product would spoil rows that do not see them.
+      // They are noted for the rows that do, and become zeros.
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int e = 0; e < (D == 256 ? 2 : 1); ++e) {
+          const bool nan = (V[t].powers >> (8 * e) & 255) >= 253;  // the others hold infinities
+          uint64_t hit = __ballot(nan);
+          while (hit) {
+            const int from = __builtin_ctzll(hit);
+            hit &= hit - 1;
+            const int k = at + 16 * t + (from >> 2 & 3) * 4 + (from >> 4);
+            const int block = D == 64 ? (from & 3) >> 1 : D == 128 ? from & 3 : 2 * (from & 3) + e;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              if (visible(k, pos[g], a.window, a.sinks)) note[g] |= 1u << block;
+          }
+          if (nan) {
+            V[t].powers &= ~(255u << (8 * e));
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+              if (D < 256 || x / 4 == e) V[t].x[x] = 0;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+        *(__attribute__((address_space(3))) v8s*)(tile + (16 * t + v_row) * T::kRow + (((v_part * (D / 32) + x) ^ T::swizzle(v_row)) << 4)) =
+            from_fp4(V[t].x[x], V[t].power(x));
+    if (i + S < range.stop) load();
+    if (!whole) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!visible(at + 16 * t + 4 * q + j, pos[g], a.window, a.sinks)) s[g][t][j] = -INFINITY;
+    }
+    // weights, as the sum of two bf16 numbers
+    v8s p[G], rest[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float top = fmaxf(fmaxf(fmaxf(s[g][0][0], s[g][0][1]), fmaxf(s[g][0][2], s[g][0][3])),
+                        fmaxf(fmaxf(s[g][1][0], s[g][1][1]), fmaxf(s[g][1][2], s[g][1][3])));
+      top = max_quarters(top);
+      if (__any(top * a.scale_log2 > m[g] * a.scale_log2 + kSlack)) {
+        const float mn = fmaxf(m[g], top);
+        const float alpha = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[g] - mn) * a.scale_log2);
+        l[g] *= alpha;
+#pragma unroll
+        for (int x = 0; x < DT; ++x) o[g][x] *= alpha;
+        m[g] = mn;
+      }
+      const float ref = m[g] == -INFINITY ? 0.f : m[g] * a.scale_log2;
+      float e[8], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g][j >> 2][j & 3], a.scale_log2, -ref));
+        sum += e[j];
+      }
+      l[g] += sum;
+      u32x4 hi, lo;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = __float_as_uint(e[2 * j]) & 0xFFFF0000u, y = __float_as_uint(e[2 * j + 1]) & 0xFFFF0000u;
+        hi[j] = x >> 16 | y;
+        lo[j] = pack_bf16(e[2 * j] - __uint_as_float(x), e[2 * j + 1] - __uint_as_float(y));
+      }
+      p[g] = __builtin_bit_cast(v8s, hi);
+      rest[g] = __builtin_bit_cast(v8s, lo);
+    }
+    // O^T += V^T P^T: lane j of a quarter points at row j / 4 of four, elements
+    // 4 (j % 4), and gets element j of the four rows
+    const int j4 = lane & 15;
+#pragma unroll
+    for (int x = 0; x < DT; ++x) {
+      v4s f[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 4 * q + (j4 >> 2), piece = 2 * x + ((j4 & 3) >> 1);
+        f[t] = lds_read_tr(tile + (16 * t + row) * T::kRow + ((piece ^ T::swizzle(row)) << 4) + ((j4 & 1) << 3));
+      }
+      const v8s v = __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        o[g][x] = mfma_16x16(v, p[g], o[g][x]);
+        o[g][x] = mfma_16x16(v, rest[g], o[g][x]);
+      }
+    }
+  }
+
+  // join the streams, 16 rows of each half at a time, over the tiles
+  if (tid == 0) s_bad = 0;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float sum = sum_quarters(l[g]);
+    if (q == 0) {
+      s_m[w][16 * g + n] = m[g];
+      s_l[w][16 * g + n] = sum;
+    }
+  }
+  const bool alone = range.chunks == 1;
+  const int64_t part = ((int64_t)b * a.kv_heads + h) * chunks + chunk;
+  float* const sums = (float*)s_tiles;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    __syncthreads();
+    if (g == 0 && bad) s_bad = 1;
+#pragma unroll
+    for (int x = 0; x < DT; ++x) {
+      float4 y = make_float4(o[g][x][0], o[g][x][1], o[g][x][2], o[g][x][3]);
+      if (note[g] >> (x / 2) & 1) y = make_float4(NAN, NAN, NAN, NAN);
+      *(float4*)(sums + (w * 16 + n) * D + (((4 * x + q) ^ (n & (D / 4 - 1))) << 2)) = y;
+    }
+    // a row's factors for its streams, the division by the sum in them where the row is complete
+    float top = -INFINITY, den = 0.f;
+    const int r_ = tid & 15, half_ = tid >> 4, row_ = half_ * 16 * G + 16 * g + r_;
+    const bool joins = tid < 16 * H;
+    if (joins) {
+#pragma unroll
+      for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[x * H + half_][16 * g + r_]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float f[S];
+#pragma unroll
+      for (int x = 0; x < S; ++x) {
+        f[x] = __builtin_amdgcn_exp2f((s_m[x * H + half_][16 * g + r_] - ref) * a.scale_log2);
+        den += f[x] * s_l[x * H + half_][16 * g + r_];
+      }
+      const float inv = !alone ? 1.f : den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+      for (int x = 0; x < S; ++x) s_f[x * H + half_][r_] = f[x] * inv;
+    }
+    __syncthreads();
+    const bool spoilt = s_bad != 0;
+    if (joins && row_ < rows) {
+      if (spoilt) den = NAN;
+      if (alone) {
+        const int tok = row_ / a.group, hq = h * a.group + row_ - tok * a.group;
+        if (a.lse)
+          a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
+      } else {
+        *(float2*)(a.part_ml + (part * C::kRows + row_) * 2) = make_float2(top, den);
+      }
+    }
+#pragma unroll 2
+    for (int i = tid; i < H * 16 * (D / 4); i += C::kThreads) {
+      const int piece = i % (D / 4), r = i / (D / 4) % 16, hf = i / (D / 4) / 16;
+      const int row = hf * 16 * G + 16 * g + r;
+      if (row >= rows) continue;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < S; ++x) {
+        const float f = s_f[x * H + hf][r];
+        const float4 z = *(const float4*)(sums + ((x * H + hf) * 16 + r) * D + ((piece ^ (r & (D / 4 - 1))) << 2));
+        y.x += f * z.x;
+        y.y += f * z.y;
+        y.z += f * z.z;
+        y.w += f * z.w;
+      }
+      if (alone) {
+        if (spoilt) y = make_float4(NAN, NAN, NAN, NAN);
+        const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+        *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
+            u32x2{pack_bf16(y.x, y.y), pack_bf16(y.z, y.w)};
+      } else {
+        *(float4*)(a.part_o + (part * C::kRows + row) * D + 4 * piece) = y;
+      }
+    }
+  }
+}
+
+// Joins the chunks of a request and key head, 1024 / D rows to a workgroup.
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, int chunks, int per) {
+  constexpr int PER = 1024 / D;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  const int rows = req.n * a.group, row = blockIdx.x * PER + threadIdx.x / (D / 4), piece = threadIdx.x % (D / 4);
+  if (row >= rows) return;
+  const KeySpan span = key_span<32>(req, 0, req.n - 1, a.window, a.sinks);
+  const int parts = chunk_of(span.count, 0, per).chunks;
+  if (parts == 1) return;
+  const int64_t first = ((int64_t)b * a.kv_heads + h) * chunks;
+  float top = -INFINITY, den = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int g = 0; g < parts; ++g) {
+    const float2 ml = *(const float2*)(a.part_ml + ((first + g) * ROWS + row) * 2);
+    const float4 y = *(const float4*)(a.part_o + ((first + g) * ROWS + row) * D + 4 * piece);
+    const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+    const float fo = __builtin_amdgcn_exp2f((top - ref) * a.scale_log2);
+    const float fn = __builtin_amdgcn_exp2f((ml.x - ref) * a.scale_log2);
+    den = den * fo + ml.y * fn;
+    o.x = o.x * fo + y.x * fn;
+    o.y = o.y * fo + y.y * fn;
+    o.z = o.z * fo + y.z * fn;
+    o.w = o.w * fo + y.w * fn;
+    top = mn;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+  *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
+      u32x2{pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)};
+  if (piece == 0 && a.lse)
+    a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
+}
+
+constexpr int kFewTarget = 8;  // workgroups to a CU
+constexpr int kFewTiles = 2;   // fewer to a wave would be all start and end
+
+template <int D, int G, int H, int S>
+hipError_t allow_few() {
+  return hipFuncSetAttribute((const void*)attend_few_kernel<D, G, H, S>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             FewShape<D, G, H, S>::kLds);
+}
+
+// rows of the workspace that parts may take: as attend_split_floats
+constexpr int few_rows(int head_dim, int cus) { return 2 * cus * (head_dim == 256 ? 128 : 256); }
+
+template <int D, int G, int H, int S>
+void launch_few(const AttendArgs& a, int cus, hipStream_t st) {
+  using C = FewShape<D, G, H, S>;
+  constexpr int PER = 1024 / D;
+  const int64_t segments = (int64_t)a.requests * a.kv_heads;
+  int64_t keys = a.max_kv;  // the most that a request's rows see
+  if (a.window && (int64_t)a.window + C::kRows + a.sinks + 65 < keys) keys = (int64_t)a.window + C::kRows + a.sinks + 65;
+  const int64_t tiles = (keys + 31) / 32 + 2;
+  int64_t chunks = kFewTarget * cus / segments;
+  if (chunks > (tiles + S * kFewTiles - 1) / (S * kFewTiles)) chunks = (tiles + S * kFewTiles - 1) / (S * kFewTiles);
+  if (chunks * segments > few_rows(D, cus) / C::kRows) chunks = few_rows(D, cus) / C::kRows / segments;
+  if (chunks < 1) chunks = 1;
+  const int per = chunks == 1 ? 0x7FFFFFFF : (int)((tiles + chunks - 1) / chunks);
+  hipLaunchKernelGGL((attend_few_kernel<D, G, H, S>), dim3((unsigned)(a.kv_heads * chunks), a.requests), dim3(C::kThreads),
+                     C::kLds, st, a, (int)chunks, per);
+  if (chunks == 1 || hipPeekAtLastError() != hipSuccess) return;  // the join would follow the parts of an earlier call
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  hipLaunchKernelGGL((join_few_kernel<D, C::kRows>), dim3((unsigned)((rows + PER - 1) / PER), a.kv_heads, a.requests),
+                     dim3(256), 0, st, a, (int)chunks, per);
+}
+
+}  // namespace

@@ -1,11 +1,47 @@
 // bf16 attention over a cache in 4 bits, the append that fills it and the read
 // that gives back what stands there.
+#include "attention_few.h"
 #include "attention_split.h"
 
-hipError_t attend_fp4_prepare(int head_dim) { return prepare<true>(head_dim); }
+template <int D>
+static hipError_t prepare_fp4() {
+  hipError_t e = allow_few<D, 1, 1, 4>();
+  if (e == hipSuccess) e = allow_few<D, 2, 1, 4>();
+  if constexpr (D < 256) {
+    if (e == hipSuccess) e = allow_few<D, 2, 2, 4>();
+    if (e == hipSuccess) e = allow_lds<D, 8, true>();
+  }
+  if (e == hipSuccess) e = allow_lds<D, 4, true>();
+  return e;
+}
+
+// The fewest rows to a workgroup that hold a request's, so that its keys are read
+// once; beyond 128 rows the largest.
+template <int D>
+static void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  if (rows <= 16) return launch_few<D, 1, 1, 4>(a, cus, st);
+  if (rows <= 32) return launch_few<D, 2, 1, 4>(a, cus, st);
+  if constexpr (D == 256) {
+    launch<D, 4, true>(a, cus, st);
+  } else {
+    if (rows <= 64) return launch_few<D, 2, 2, 4>(a, cus, st);
+    if (rows <= 128) return launch<D, 4, true>(a, cus, st);
+    launch<D, 8, true>(a, cus, st);
+  }
+}
+
+hipError_t attend_fp4_prepare(int head_dim) {
+  return head_dim == 64 ? prepare_fp4<64>() : head_dim == 128 ? prepare_fp4<128>() : prepare_fp4<256>();
+}
 
 void launch_attend_fp4(int head_dim, const AttendArgs& a, int cus, hipStream_t st) {
-  launch_dim<true>(head_dim, a, cus, st);
+  if (head_dim == 64)
+    launch_fp4<64>(a, cus, st);
+  else if (head_dim == 128)
+    launch_fp4<128>(a, cus, st);
+  else
+    launch_fp4<256>(a, cus, st);
 }
 
 namespace {

@@ -777,17 +777,6 @@ hipError_t allow_lds() {
   }
   return hipSuccess;
 }
-template <int D, bool F4>
-hipError_t allow_lds_d() {
-  hipError_t e = allow_lds<D, 1, F4>();
-  if (e == hipSuccess) e = allow_lds<D, 4, F4>();
-  if constexpr (D < 256) {
-    if (e == hipSuccess) e = allow_lds<D, 2, F4>();
-    if (e == hipSuccess) e = allow_lds<D, 8, F4>();
-  }
-  return e;
-}
-
 template <int D, int R, bool F4>
 void launch(AttendArgs a, int cus, hipStream_t st) {
   using C = Shape<D, R, F4>;
@@ -820,37 +809,6 @@ void launch(AttendArgs a, int cus, hipStream_t st) {
   const int groups = (int)(((rows < ROWS ? rows : ROWS) + PER - 1) / PER);
   hipLaunchKernelGGL((attend_join_kernel<D, R, F4>), dim3((unsigned)row_tiles, a.kv_heads * groups, a.requests),
                      dim3(256), 0, st, a, workers, groups);
-}
-
-// The fewest rows to a workgroup that hold a request's, so that its keys are
-// read once; beyond 128 rows the largest.  A wave costs the same whether its
-// rows are there or not.
-template <int D, bool F4>
-void launch_d(const AttendArgs& a, int cus, hipStream_t st) {
-  const int64_t rows = (int64_t)a.max_new * a.group;
-  if (rows <= 32) return launch<D, 1, F4>(a, cus, st);
-  if constexpr (D == 256) {
-    launch<D, 4, F4>(a, cus, st);
-  } else {
-    if (rows <= 64) return launch<D, 2, F4>(a, cus, st);
-    if (rows <= 128) return launch<D, 4, F4>(a, cus, st);
-    launch<D, 8, F4>(a, cus, st);
-  }
-}
-
-template <bool F4>
-hipError_t prepare(int head_dim) {
-  return head_dim == 64 ? allow_lds_d<64, F4>() : head_dim == 128 ? allow_lds_d<128, F4>() : allow_lds_d<256, F4>();
-}
-
-template <bool F4>
-void launch_dim(int head_dim, const AttendArgs& a, int cus, hipStream_t st) {
-  if (head_dim == 64)
-    launch_d<64, F4>(a, cus, st);
-  else if (head_dim == 128)
-    launch_d<128, F4>(a, cus, st);
-  else
-    launch_d<256, F4>(a, cus, st);
 }
 
 }  // namespace
