@@ -114,6 +114,20 @@ __device__ __forceinline__ float sum_halves(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ __forceinline__ int scan_lanes(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ Request of_lane(const Request& r, int lane) {
+  return Request{__builtin_amdgcn_readlane(r.q0, lane), __builtin_amdgcn_readlane(r.n, lane),
+                 __builtin_amdgcn_readlane(r.kv, lane), (bool)__builtin_amdgcn_readlane((int)r.bad, lane)};
+}
+
 // One row tile's state in a wave: 32 rows, lane n = l % 32 holds row n in both
 // halves (m in both, l as each half's part).  m is what the exponents are taken
 // against: a score the row has met, at most kSlack (in powers of two) below its

@@ -1,9 +1,9 @@
 // Attention of few rows over a cache in 4 bits: up to 64 rows of a request and
 // key head (a token of many heads, a draft block).
 //
-// Each wave works alone: it takes every S-th tile of 32 keys of its workgroup's
-// run of them, reads K and V straight into registers, a tile ahead of their
-// use, and keeps the sums of 16 G rows.  Products are 16 x 16 x 32, with both
+// A workgroup takes 16 G rows and a run of tiles of 32 keys; each of its S waves
+// works alone on every S-th of them, reads K and V straight into registers, a tile
+// ahead of their use, and keeps its own sums.  Products are 16 x 16 x 32, with both
 // results transposed: S^T = K Q^T (keys x rows) and O^T = V^T P^T.  Lane l (n = l % 16,
 // q = l / 16) holds row n, of S the keys 4 q .. 4 q + 3 of both halves of the
 // tile, which are its slots of the second product's operand, and of O the elements
@@ -12,7 +12,11 @@
 //      are, with the queries' elements dealt alike.
 //   V: bf16 rows go through 64 D bytes of LDS of the wave's own for the transposing
 //      read, swizzled as in KeyTile.
-// For more than 32 rows H = 2 waves take the same keys for 32 rows each.
+//
+// Units.  A unit is a (request, key head, run of its tiles).  Where the requests
+// fill the chip by themselves a run is all of a request's tiles, otherwise each request is
+// cut into as many equal runs as workgroups allow and a second launch joins
+// them.  Every workgroup finds the division by itself, a lane to each request.
 #pragma once
 #include "fp4.h"
 
@@ -36,13 +40,16 @@ __device__ __forceinline__ float sum_quarters(float x) {
 template <int D>
 struct Quarter {
   static constexpr int kWords = D / 32;
+  static constexpr int kPowers = D == 256 ? 2 : 1;
   uint32_t x[kWords];
+  // The four bytes among which the powers are: a byte alone would be widened
+  // where it lands, a wait for memory in every tile.
   uint32_t powers;
   static __device__ __forceinline__ uint32_t data_at(int row, int part) { return row * (D / 2) + part * (D / 8); }
-  static __device__ __forceinline__ uint32_t power_at(int row, int part) {
-    return row * (D / 32) + (D == 64 ? part >> 1 : part * (D / 128));
-  }
+  static __device__ __forceinline__ int block_of(int part) { return D == 64 ? part >> 1 : part * (D / 128); }
+  static __device__ __forceinline__ uint32_t power_at(int row, int part) { return row * (D / 32) + block_of(part); }
   __device__ __forceinline__ void load(const char* data, const char* power) {
+    powers = *(const uint32_t*)power;
     if constexpr (D == 64) {
       const u32x2 v = *(const u32x2*)data;
       x[0] = v[0];
@@ -55,57 +62,117 @@ struct Quarter {
         for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
       }
     }
-    if constexpr (D == 256)
-      powers = *(const uint16_t*)power;
-    else
-      powers = *(const uint8_t*)power;
   }
-  // word i's power
-  __device__ __forceinline__ float power(int i) const {
-    return power_of(D == 256 ? (powers >> (8 * (i / 4))) & 255 : powers);
+  // power e, the first `shift` bits up
+  __device__ __forceinline__ uint32_t byte(int e, uint32_t shift) const {
+    return __builtin_amdgcn_ubfe(powers, shift + 8 * e, 8);
   }
+  // that of word i
+  __device__ __forceinline__ float power(int i, uint32_t shift) const { return power_of(byte(D == 256 ? i / 4 : 0, shift)); }
 };
 
-template <int D, int G, int H, int S>
+template <int D, int G, int S>
 struct FewShape {
-  static constexpr int kRows = 16 * G * H;
-  static constexpr int kThreads = 64 * H * S;
+  static constexpr int kRows = 16 * G;
+  static constexpr int kThreads = 64 * S;
   static constexpr int kTile = 64 * D;  // V of a tile in bf16; also 16 rows of sums
-  static constexpr int kLds = H * S * kTile;
+  static constexpr int kLds = S * kTile;
 };
 
-// tiles of the chunk that a workgroup takes; none for a chunk past the last
-struct Chunk {
-  int first, stop, chunks;
+// What a workgroup does: tiles [first, stop) of request b and key head h, which
+// is cut into `runs`.
+struct Unit {
+  int b, h, first, stop, runs;
 };
-__device__ __forceinline__ Chunk chunk_of(int count, int chunk, int per) {
-  Chunk c;
-  c.chunks = count > per ? (count + per - 1) / per : 1;
-  c.first = (int)((int64_t)count * chunk / c.chunks);
-  c.stop = (int)((int64_t)count * (chunk + 1) / c.chunks);
-  return c;
+
+__device__ __forceinline__ int quotient_up(int x, int y, float inv) {  // about x / y, at least 1
+  const int q = (int)((float)(x + y - 1) * inv);
+  return q < 1 ? 1 : q;
 }
 
-template <int D, int G, int H, int S>
-__global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 : 1)) void attend_few_kernel(AttendArgs a, int chunks, int per) {
+struct FewArgs {
+  int32_t units;     // workgroups there are for units; 0: a run is all of a request's tiles
+  int32_t per, most; // beyond 64 requests: tiles to a run, and runs to a request, of the longest one
+  int32_t least;     // tiles of a run that are worth a workgroup
+};
+
+__device__ __forceinline__ int few_tiles(const AttendArgs& a, const Request& r) {
+  return r.n > 0 ? key_span<32>(r, 0, r.n - 1, a.window, a.sinks).count : -1;
+}
+
+// Runs of each request, by a wave: a lane to each, 0 for requests without rows.
+__device__ __forceinline__ int few_runs(const AttendArgs& a, const FewArgs& f, int tiles, int lane) {
+  int all = tiles < 0 ? 0 : tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
+  // The shortest run for which there are workgroups, each lane trying one
+  // between an even share and twice that.
+  int even = (int)(((int64_t)all * a.kv_heads + f.units - 1) / f.units);
+  if (even < f.least) even = f.least;
+  const int size = even + (int)((int64_t)even * lane / 63);
+  const float inv = 1.f / (float)size;
+  int need = 0;
+#pragma unroll 1
+  for (int i = 0; i < a.requests; ++i) {
+    const int t = __builtin_amdgcn_readlane(tiles, i);
+    if (t >= 0) need += quotient_up(t, size, inv);
+  }
+  const uint64_t fits = __ballot((int64_t)need * a.kv_heads <= f.units);
+  const int pick = fits ? __builtin_ctzll(fits) : 63;
+  return tiles < 0 ? 0 : quotient_up(tiles, __builtin_amdgcn_readlane(size, pick), __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), pick)));
+}
+
+template <int D, int G, int S>
+__global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : D * G <= 256 ? 2 : 1)) void attend_few_kernel(AttendArgs a, FewArgs f) {
   using T = KeyTile<D>;
-  using C = FewShape<D, G, H, S>;
-  constexpr int DT = D / 16, KC = D / 32, W = H * S;
+  using C = FewShape<D, G, S>;
+  constexpr int DT = D / 16, KC = D / 32;
   extern __shared__ __align__(1024) unsigned char s_tiles[];
-  __shared__ float s_m[W][16 * G], s_l[W][16 * G], s_f[W][16];
+  __shared__ float s_m[S][16 * G], s_l[S][16 * G], s_f[S][16];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 15, q = lane >> 4;
-  const int half = w % H, stream = w / H;
-  const int b = blockIdx.y, h = blockIdx.x % a.kv_heads, chunk = blockIdx.x / a.kv_heads;
-  const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
-  const int rows = req.n * a.group;
-  if (rows == 0) return;
-  const KeySpan span = uniform(key_span<32>(req, 0, req.n - 1, a.window, a.sinks));
-  const Chunk range = chunk_of(span.count, chunk, per);
-  if (chunk >= range.chunks) return;
+  const int unit = blockIdx.x;
 
-  // this wave's rows
-  const int w0 = half * 16 * G;
+  int b, h, run, runs;
+  Request req;
+  if (f.units == 0) {
+    b = unit / a.kv_heads;
+    h = unit - b * a.kv_heads;
+    run = 0;
+    runs = 1;
+    req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+  } else if (a.requests > 64) {
+    const int x = unit / a.kv_heads;
+    h = unit - x * a.kv_heads;
+    b = x / f.most;
+    run = x - b * f.most;
+    req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
+    runs = quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per);
+    if (run >= runs) return;
+  } else {
+    Request mine{0, 0, 0, false};
+    if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
+    const int own = few_runs(a, f, lane < a.requests ? few_tiles(a, mine) : -1, lane);
+    const int upto = scan_lanes(own, lane) * a.kv_heads;
+    if (unit == 0 && blockIdx.y == 0 && w == 0) {  // for the join
+      if (lane == 0) a.plan[0] = 0;
+      a.plan[lane + 1] = upto;
+    }
+    const uint64_t past = __ballot(upto > unit);
+    if (!past) return;
+    b = __builtin_ctzll(past);
+    const int off = unit - (b ? __builtin_amdgcn_readlane(upto, b - 1) : 0);
+    runs = __builtin_amdgcn_readlane(own, b);
+    run = off / a.kv_heads;
+    h = off - run * a.kv_heads;
+    req = of_lane(mine, b);
+  }
+  req = Request{uniform(req.q0), uniform(req.n), uniform(req.kv), (bool)uniform(req.bad)};
+  const int rows = req.n * a.group, w0 = blockIdx.y * C::kRows;
+  if (w0 >= rows) return;
+  const KeySpan span = uniform(key_span<32>(req, 0, req.n - 1, a.window, a.sinks));
+  const int first = uniform((int)((int64_t)span.count * run / runs)), stop = uniform((int)((int64_t)span.count * (run + 1) / runs));
+
   int pos[G];
   v8s Q[G][KC];
 #pragma unroll
@@ -139,10 +206,12 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
   lds_byte* const tile = (lds_byte*)s_tiles + w * C::kTile;
   // V: rows that meet in different banks when they are written
   const int v_row = (lane >> 2 & 3) * 4 + (lane >> 4), v_part = lane & 3;
-  const uint32_t k_data = Quarter<D>::data_at(n, q), k_power = Quarter<D>::power_at(n, q);
-  const uint32_t v_data = Quarter<D>::data_at(v_row, v_part), v_power = Quarter<D>::power_at(v_row, v_part);
+  using Q4 = Quarter<D>;
+  const uint32_t k_data = Q4::data_at(n, q), k_power = Q4::power_at(n, q) & ~3u, k_shift = 8 * (Q4::power_at(n, q) & 3);
+  const uint32_t v_data = Q4::data_at(v_row, v_part), v_power = Q4::power_at(v_row, v_part) & ~3u;
+  const uint32_t v_shift = 8 * (Q4::power_at(v_row, v_part) & 3);
 
-  Quarter<D> K[2], V[2];
+  Q4 K[2], V[2];
   int page[2] = {0, 0}, key = 0;
   auto look_up = [&](int i) {
     key = tile_of(span, i) * 32;
@@ -168,15 +237,15 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
       V[t].load((const char*)a.v + data + v_data, (const char*)a.v + power + v_power);
     }
   };
-  int i = range.first + stream;
-  if (i < range.stop) {
+  int i = first + w;
+  if (i < stop) {
     look_up(i);
     load();
   }
 #pragma unroll 1
-  for (; i < range.stop; i += S) {
+  for (; i < stop; i += S) {
     const int at = key;  // of this tile
-    if (i + S < range.stop) look_up(i + S);
+    if (i + S < stop) look_up(i + S);
     const bool whole = all_visible(seen, at, 32, a.window, a.sinks);
     // scores, and V on its way through LDS
     v4f s[G][2];
@@ -186,45 +255,44 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
       for (int g = 0; g < G; ++g) s[g][t] = zero4();
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        const v8s k = from_fp4(K[t].x[c], K[t].power(c));
+        const v8s k = from_fp4(K[t].x[c], K[t].power(c, k_shift));
 #pragma unroll
         for (int g = 0; g < G; ++g) s[g][t] = mfma_16x16(k, Q[g][c], s[g][t]);
       }
     }
     if (!whole) {
-      // Blocks of V that are not finite: a product would spoil rows that do not see them.
-      // They are noted for the rows that do, and become zeros.
+      // Blocks of V that are not finite (or nearly: their elements may not be): a
+      // product would spoil rows that do not see them.  They become zeros, and
+      // the rows that do see them get NaN at the end.
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < (D == 256 ? 2 : 1); ++e) {
-          const bool nan = (V[t].powers >> (8 * e) & 255) >= 253;  // the others hold infinities
-          uint64_t hit = __ballot(nan);
+        for (int e = 0; e < Q4::kPowers; ++e) {
+          const bool odd = V[t].byte(e, v_shift) >= 253;
+          uint64_t hit = __ballot(odd);
           while (hit) {
             const int from = __builtin_ctzll(hit);
             hit &= hit - 1;
             const int k = at + 16 * t + (from >> 2 & 3) * 4 + (from >> 4);
-            const int block = D == 64 ? (from & 3) >> 1 : D == 128 ? from & 3 : 2 * (from & 3) + e;
 #pragma unroll
             for (int g = 0; g < G; ++g)
-              if (visible(k, pos[g], a.window, a.sinks)) note[g] |= 1u << block;
+              if (visible(k, pos[g], a.window, a.sinks)) note[g] |= 1u << (Q4::block_of(from & 3) + e);
           }
-          if (nan) {
-            V[t].powers &= ~(255u << (8 * e));
+          if (odd) {
+            V[t].powers &= ~(255u << (v_shift + 8 * e));
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x)
-              if (D < 256 || x / 4 == e) V[t].x[x] = 0;
+            for (int x = 0; x < Q4::kWords; ++x)
+              if (Q4::kPowers == 1 || x / 4 == e) V[t].x[x] = 0;
           }
         }
-      }
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
         *(__attribute__((address_space(3))) v8s*)(tile + (16 * t + v_row) * T::kRow + (((v_part * (D / 32) + x) ^ T::swizzle(v_row)) << 4)) =
-            from_fp4(V[t].x[x], V[t].power(x));
-    if (i + S < range.stop) load();
+            from_fp4(V[t].x[x], V[t].power(x, v_shift));
+    if (i + S < stop) load();
     if (!whole) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -297,8 +365,8 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
       s_l[w][16 * g + n] = sum;
     }
   }
-  const bool alone = range.chunks == 1;
-  const int64_t part = ((int64_t)b * a.kv_heads + h) * chunks + chunk;
+  const bool alone = runs == 1;
+  const int64_t part = ((int64_t)unit * gridDim.y + blockIdx.y) * C::kRows;  // rows
   float* const sums = (float*)s_tiles;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -312,21 +380,17 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
     }
     // a row's factors for its streams, the division by the sum in them where the row is complete
     float top = -INFINITY, den = 0.f;
-    const int r_ = tid & 15, half_ = tid >> 4, row_ = half_ * 16 * G + 16 * g + r_;
-    const bool joins = tid < 16 * H;
+    const int row_ = w0 + 16 * g + (tid & 15);
+    const bool joins = tid < 16;
     if (joins) {
 #pragma unroll
-      for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[x * H + half_][16 * g + r_]);
+      for (int x = 0; x < S; ++x) top = fmaxf(top, s_m[x][16 * g + tid]);
       const float ref = top == -INFINITY ? 0.f : top;
-      float f[S];
 #pragma unroll
-      for (int x = 0; x < S; ++x) {
-        f[x] = __builtin_amdgcn_exp2f((s_m[x * H + half_][16 * g + r_] - ref) * a.scale_log2);
-        den += f[x] * s_l[x * H + half_][16 * g + r_];
-      }
+      for (int x = 0; x < S; ++x) den += __builtin_amdgcn_exp2f((s_m[x][16 * g + tid] - ref) * a.scale_log2) * s_l[x][16 * g + tid];
       const float inv = !alone ? 1.f : den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-      for (int x = 0; x < S; ++x) s_f[x * H + half_][r_] = f[x] * inv;
+      for (int x = 0; x < S; ++x) s_f[x][tid] = __builtin_amdgcn_exp2f((s_m[x][16 * g + tid] - ref) * a.scale_log2) * inv;
     }
     __syncthreads();
     const bool spoilt = s_bad != 0;
@@ -337,19 +401,18 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
         if (a.lse)
           a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
       } else {
-        *(float2*)(a.part_ml + (part * C::kRows + row_) * 2) = make_float2(top, den);
+        *(float2*)(a.part_ml + (part + 16 * g + tid) * 2) = make_float2(top, den);
       }
     }
-#pragma unroll 2
-    for (int i = tid; i < H * 16 * (D / 4); i += C::kThreads) {
-      const int piece = i % (D / 4), r = i / (D / 4) % 16, hf = i / (D / 4) / 16;
-      const int row = hf * 16 * G + 16 * g + r;
+#pragma unroll 1
+    for (int i = tid; i < 16 * (D / 4); i += C::kThreads) {
+      const int piece = i % (D / 4), r = i / (D / 4), row = w0 + 16 * g + r;
       if (row >= rows) continue;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < S; ++x) {
-        const float f = s_f[x * H + hf][r];
-        const float4 z = *(const float4*)(sums + ((x * H + hf) * 16 + r) * D + ((piece ^ (r & (D / 4 - 1))) << 2));
+        const float f = s_f[x][r];
+        const float4 z = *(const float4*)(sums + (x * 16 + r) * D + ((piece ^ (r & (D / 4 - 1))) << 2));
         y.x += f * z.x;
         y.y += f * z.y;
         y.z += f * z.z;
@@ -361,30 +424,37 @@ __global__ __launch_bounds__((FewShape<D, G, H, S>::kThreads), (D * G < 512 ? 2 
         *(u32x2*)((bf16_t*)a.out + (req.q0 + tok) * a.o_tok + hq * a.o_head + 4 * piece) =
             u32x2{pack_bf16(y.x, y.y), pack_bf16(y.z, y.w)};
       } else {
-        *(float4*)(a.part_o + (part * C::kRows + row) * D + 4 * piece) = y;
+        *(float4*)(a.part_o + (part + 16 * g + r) * D + 4 * piece) = y;
       }
     }
   }
 }
 
-// Joins the chunks of a request and key head, 1024 / D rows to a workgroup.
+// Joins the runs of a request and key head, 1024 / D rows to a workgroup.
 template <int D, int ROWS>
-__global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, int chunks, int per) {
+__global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, FewArgs f, int row_tiles) {
   constexpr int PER = 1024 / D;
   const int b = blockIdx.z, h = blockIdx.y;
   const Request req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
   const int rows = req.n * a.group, row = blockIdx.x * PER + threadIdx.x / (D / 4), piece = threadIdx.x % (D / 4);
   if (row >= rows) return;
-  const KeySpan span = key_span<32>(req, 0, req.n - 1, a.window, a.sinks);
-  const int parts = chunk_of(span.count, 0, per).chunks;
-  if (parts == 1) return;
-  const int64_t first = ((int64_t)b * a.kv_heads + h) * chunks;
+  int runs;
+  int64_t first;
+  if (a.requests > 64) {
+    runs = quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per);
+    first = (int64_t)b * f.most * a.kv_heads + h;
+  } else {
+    first = a.plan[b] + h;
+    runs = (a.plan[b + 1] - a.plan[b]) / a.kv_heads;
+  }
+  if (runs == 1) return;
   float top = -INFINITY, den = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int g = 0; g < parts; ++g) {
-    const float2 ml = *(const float2*)(a.part_ml + ((first + g) * ROWS + row) * 2);
-    const float4 y = *(const float4*)(a.part_o + ((first + g) * ROWS + row) * D + 4 * piece);
+  for (int g = 0; g < runs; ++g) {
+    const int64_t at = (first + (int64_t)g * a.kv_heads) * row_tiles * ROWS + row;
+    const float2 ml = *(const float2*)(a.part_ml + at * 2);
+    const float4 y = *(const float4*)(a.part_o + at * D + 4 * piece);
     const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
     const float fo = __builtin_amdgcn_exp2f((top - ref) * a.scale_log2);
     const float fn = __builtin_amdgcn_exp2f((ml.x - ref) * a.scale_log2);
@@ -403,37 +473,47 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, int chunks,
     a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
 }
 
-constexpr int kFewTarget = 8;  // workgroups to a CU
-constexpr int kFewTiles = 2;   // fewer to a wave would be all start and end
-
-template <int D, int G, int H, int S>
+template <int D, int G, int S>
 hipError_t allow_few() {
-  return hipFuncSetAttribute((const void*)attend_few_kernel<D, G, H, S>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                             FewShape<D, G, H, S>::kLds);
+  return hipFuncSetAttribute((const void*)attend_few_kernel<D, G, S>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                             FewShape<D, G, S>::kLds);
 }
 
 // rows of the workspace that parts may take: as attend_split_floats
 constexpr int few_rows(int head_dim, int cus) { return 2 * cus * (head_dim == 256 ? 128 : 256); }
 
-template <int D, int G, int H, int S>
-void launch_few(const AttendArgs& a, int cus, hipStream_t st) {
-  using C = FewShape<D, G, H, S>;
+// `units`: workgroups that the chip holds at once, divided among the row tiles
+template <int D, int G, int S>
+void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
+  using C = FewShape<D, G, S>;
   constexpr int PER = 1024 / D;
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  const int row_tiles = (int)((rows + C::kRows - 1) / C::kRows);
   const int64_t segments = (int64_t)a.requests * a.kv_heads;
   int64_t keys = a.max_kv;  // the most that a request's rows see
-  if (a.window && (int64_t)a.window + C::kRows + a.sinks + 65 < keys) keys = (int64_t)a.window + C::kRows + a.sinks + 65;
+  if (a.window && (int64_t)a.window + rows + a.sinks + 65 < keys) keys = (int64_t)a.window + rows + a.sinks + 65;
   const int64_t tiles = (keys + 31) / 32 + 2;
-  int64_t chunks = kFewTarget * cus / segments;
-  if (chunks > (tiles + S * kFewTiles - 1) / (S * kFewTiles)) chunks = (tiles + S * kFewTiles - 1) / (S * kFewTiles);
-  if (chunks * segments > few_rows(D, cus) / C::kRows) chunks = few_rows(D, cus) / C::kRows / segments;
-  if (chunks < 1) chunks = 1;
-  const int per = chunks == 1 ? 0x7FFFFFFF : (int)((tiles + chunks - 1) / chunks);
-  hipLaunchKernelGGL((attend_few_kernel<D, G, H, S>), dim3((unsigned)(a.kv_heads * chunks), a.requests), dim3(C::kThreads),
-                     C::kLds, st, a, (int)chunks, per);
-  if (chunks == 1 || hipPeekAtLastError() != hipSuccess) return;  // the join would follow the parts of an earlier call
-  const int64_t rows = (int64_t)a.max_new * a.group;
+  FewArgs f{};
+  f.least = S < 8 ? S : 8;
+  units /= row_tiles;
+  const int64_t room = few_rows(D, cus) / (C::kRows * row_tiles);
+  if (units > room) units = (int)room;
+  if (2 * segments <= units && tiles > f.least && a.requests * tiles < (int64_t)1 << 30) {
+    f.units = units;
+    if (a.requests > 64) {
+      f.most = (int)(units / segments);
+      f.per = (int)((tiles + f.most - 1) / f.most);
+      f.units = (int)(segments * f.most);
+    } else if (f.units > segments * ((tiles + f.least - 1) / f.least)) {
+      f.units = (int)(segments * ((tiles + f.least - 1) / f.least));
+    }
+  }
+  // row tiles of a unit meet in one XCD's cache
+  const int64_t grid = f.units ? f.units : segments;
+  hipLaunchKernelGGL((attend_few_kernel<D, G, S>), dim3((unsigned)grid, row_tiles), dim3(C::kThreads), C::kLds, st, a, f);
+  if (!f.units || hipPeekAtLastError() != hipSuccess) return;  // the join would follow the parts of an earlier call
   hipLaunchKernelGGL((join_few_kernel<D, C::kRows>), dim3((unsigned)((rows + PER - 1) / PER), a.kv_heads, a.requests),
-                     dim3(256), 0, st, a, (int)chunks, per);
+                     dim3(256), 0, st, a, f, row_tiles);
 }
 
 }  // namespace

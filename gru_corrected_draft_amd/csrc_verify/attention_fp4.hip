@@ -3,33 +3,42 @@
 #include "attention_few.h"
 #include "attention_split.h"
 
+namespace {
+
+// Row tiles of 32 rows save conversions over 16 where there are so many; for
+// heads of 256 their sums do not fit in registers.
 template <int D>
-static hipError_t prepare_fp4() {
-  hipError_t e = allow_few<D, 1, 1, 4>();
-  if (e == hipSuccess) e = allow_few<D, 2, 1, 4>();
+constexpr int kRowGroups = D == 256 ? 1 : 2;
+template <int D>
+constexpr int kManyWaves = D == 256 ? 8 : 16;  // what a CU holds
+
+template <int D>
+hipError_t prepare_fp4() {
+  hipError_t e = allow_few<D, 1, 4>();
+  if (e == hipSuccess) e = allow_few<D, 1, kManyWaves<D>>();
+  if (D < 256 && e == hipSuccess) e = allow_few<D, kRowGroups<D>, 4>();
   if constexpr (D < 256) {
-    if (e == hipSuccess) e = allow_few<D, 2, 2, 4>();
     if (e == hipSuccess) e = allow_lds<D, 8, true>();
   }
   if (e == hipSuccess) e = allow_lds<D, 4, true>();
   return e;
 }
 
-// The fewest rows to a workgroup that hold a request's, so that its keys are read
-// once; beyond 128 rows the largest.
 template <int D>
-static void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
+void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
-  if (rows <= 16) return launch_few<D, 1, 1, 4>(a, cus, st);
-  if (rows <= 32) return launch_few<D, 2, 1, 4>(a, cus, st);
-  if constexpr (D == 256) {
-    launch<D, 4, true>(a, cus, st);
-  } else {
-    if (rows <= 64) return launch_few<D, 2, 2, 4>(a, cus, st);
-    if (rows <= 128) return launch<D, 4, true>(a, cus, st);
-    launch<D, 8, true>(a, cus, st);
+  if (rows <= 64 || (rows <= 128 && a.max_kv <= 4096)) {
+    if ((rows + 15) / 16 * a.requests * a.kv_heads <= cus) return launch_few<D, 1, kManyWaves<D>>(a, cus, cus, st);
+    if (rows <= 16) return launch_few<D, 1, 4>(a, 2 * cus, cus, st);
+    return launch_few<D, kRowGroups<D>, 4>(a, 2 * cus, cus, st);
   }
+  if constexpr (D < 256) {
+    if (rows > 128) return launch<D, 8, true>(a, cus, st);
+  }
+  launch<D, 4, true>(a, cus, st);
 }
+
+}  // namespace
 
 hipError_t attend_fp4_prepare(int head_dim) {
   return head_dim == 64 ? prepare_fp4<64>() : head_dim == 128 ? prepare_fp4<128>() : prepare_fp4<256>();

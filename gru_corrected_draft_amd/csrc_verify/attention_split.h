@@ -107,15 +107,6 @@ __device__ __forceinline__ int request_steps(const AttendArgs& a, const Request&
   return n * a.kv_heads;
 }
 
-__device__ __forceinline__ int scan_lanes(int x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
-  }
-  return x;
-}
-
 // Row tile of step `off` of a request's, which becomes the step among the row
 // tile's, by a wave for one request: a lane to each row tile.  A prompt of 2048 tokens has 32 row
 // tiles, and gone through one by one they were a third of its time.
@@ -141,11 +132,6 @@ __device__ __forceinline__ int steps_before(const AttendArgs& a, const Request& 
   for (int x = 0; x < rt; x += 64)
     n += __builtin_amdgcn_readlane(scan_lanes(x + lane < rt ? tile_steps<ROWS, STEP>(a, r, x + lane) : 0, lane), 63);
   return n * a.kv_heads;
-}
-
-__device__ __forceinline__ Request of_lane(const Request& r, int lane) {
-  return Request{__builtin_amdgcn_readlane(r.q0, lane), __builtin_amdgcn_readlane(r.n, lane),
-                 __builtin_amdgcn_readlane(r.kv, lane), (bool)__builtin_amdgcn_readlane((int)r.bad, lane)};
 }
 
 template <int D, int R, bool WHOLE, bool F4>

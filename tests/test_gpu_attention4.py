@@ -148,6 +148,10 @@ def test_against_64_bits(case):
 @pytest.mark.parametrize("heads,dim,new,kv", [
     ((8, 2), 128, [1] * 70, [5 + 37 * (i % 9) for i in range(70)]),
     ((8, 2), 128, [1] * 3, [4000, 1, 2500]),
+    ((4, 1), 64, [1] * 70, [3 + 101 * (i % 9) for i in range(70)]),
+    ((4, 1), 128, [2, 0, 1] * 27, [900, 0, 350] * 27),
+    ((16, 8), 128, [1] * 40, [40 + 90 * (i % 7) for i in range(40)]),
+    ((16, 8), 128, [4] * 40, [40 + 90 * (i % 7) for i in range(40)]),
     ((8, 1), 64, [16] * 3, [3000, 16, 900]),
     ((16, 4), 128, [16, 7], [2500, 700]),
     ((8, 2), 256, [16, 9], [1500, 30]),
