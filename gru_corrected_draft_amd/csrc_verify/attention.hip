@@ -7,6 +7,7 @@
 #include "attention_bf16.h"
 #include "fp4.h"
 #include "handle.h"
+#include "parts.h"
 
 // ---------------------------------------------------------------- append
 // A copy: one 16-byte piece per thread, keys in the first half of the grid's
@@ -66,34 +67,6 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // element 16 c + 4 q + i, and output row m of accumulator (blk, j) is element
 // 64 blk + 4 m + j.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-
-// Parts of an output pass between workgroups of one launch on any XCD: written
-// through to and read from where all see them, 8 bytes at a time.  A fence in
-// their place writes a whole L2 back (27.5 us for those 10.8).
-__device__ __forceinline__ void share2(float* p, float x, float y) {
-  const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
-  __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 shared2(const float* p) {
-  const uint64_t v = __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ float4 shared4(const float* p) {
-  const float2 a = shared2(p), b = shared2(p + 2);
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-// Called by all threads of a workgroup after they shared a part of a segment:
-// whether it was the last of `parts`, in which case all of them can be read.
-__device__ __forceinline__ bool last_of(int32_t* arrived, int parts, int* s_last) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's are where all see them
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    *s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
-    if (*s_last) __hip_atomic_store(arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  return *s_last;
-}
 
 template <int D>
 __global__ __launch_bounds__(256) void attend_f32_kernel(AttendArgs a, int splits) {

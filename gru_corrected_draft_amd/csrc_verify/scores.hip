@@ -6,26 +6,30 @@
 // Both terms of the entropy are of one sign, so nothing cancels, and a row with
 // one candidate yields exactly 0 for both.
 //
-// Two launches.  The first reads the logits once: a workgroup takes a part of a
-// row, each wave keeps m, l and t (rescaled when its maximum grows, about
-// ln(vectors) times a row), and for the likeliest ids every 32 logits leave their
-// largest.  The second takes a row to a workgroup: it joins the parts, and since
-// n of the groups of 32 whose maxima are the n largest hold the n largest logits,
-// it goes back for those alone.
+// A workgroup takes a row, or a part of one where there are few: it reads the
+// logits once, each wave keeps m, l and t (rescaled when its maximum grows, about
+// ln(vectors) times a row), and for the likeliest ids every 128 logits leave their
+// largest.  Then the row's last workgroup joins the parts, and since the n groups
+// with the largest maxima hold n logits as large as any other group's, it goes back
+// for the few groups that reach them.
 #include <cmath>
 #include <new>
 
 #include "../../include/domino_verify.h"
 #include "common.h"
 #include "handle.h"
+#include "parts.h"
 #include "vocab.h"
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = kThreads * 8;  // logits of a step of a workgroup
-constexpr int kGroup = 32;            // logits that leave one maximum
-constexpr int kMaxTop = 64;
+constexpr int kVectors = 4;           // of 8 logits, in flight to a lane
+constexpr int kSpan = kThreads * 8;   // logits that a workgroup reads at once
+constexpr int kChunk = kVectors * kSpan;  // logits of a step of a workgroup
+// Four lanes' logits of a step leave one maximum: kVectors runs of 32, kSpan apart.
+constexpr int kGroups = kThreads / 4;  // of a step
+constexpr int kMaxTop = 64, kFewTop = 24;
 constexpr int kMaxParts = 128;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -34,8 +38,9 @@ struct ScoreArgs {
   int64_t row_stride;
   int32_t rows, vocab, range, parts, top;
   const int32_t* tokens;
-  float* part;    // [rows][parts][3]: m, l, t in powers of two
-  float* maxima;  // [rows][groups]
+  float* part;       // [rows][parts][4]: m, l, t in powers of two
+  float* maxima;     // [rows][groups]
+  int32_t* arrived;  // [rows] parts there are, 0 between calls
   int32_t groups;
   float* logprob;
   float* entropy;
@@ -77,59 +82,6 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   return r;
 }
 
-template <typename T, bool TOP>
-__global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
-  __shared__ Sums s_sums[kThreads / 64];
-  const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x;
-  const int lo = part * a.range, hi = min(lo + a.range, a.vocab);
-  const T* const p = (const T*)a.logits + row * a.row_stride;
-  float m = -INFINITY, l = 0.f, t = 0.f;  // m is the wave's
-  for (int v = lo + tid * 8; v - tid * 8 < hi; v += kChunk) {
-    float x[8];
-    load_logits<T>(p + v, hi - v, x);
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-    if (__any(top > m)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = tame(x[j]);
-      top = tame(top);
-      const float mn = fmaxf(m, wave_max(top));
-      if (m != -INFINITY) {
-        const float d = fmaxf((m - mn) * kLog2e, -200.f), f = exp2_fast(d);
-        t = f * (t + d * l);
-        l *= f;
-      }
-      m = mn;
-    }
-    if constexpr (TOP) {
-      float g = fmaxf(top, __uint_as_float(other<0>(__float_as_uint(top))));
-      g = fmaxf(g, __uint_as_float(other<1>(__float_as_uint(g))));
-      if ((tid & 3) == 0 && v < hi) a.maxima[(int64_t)row * a.groups + v / kGroup] = tame(g);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // -inf and NaN end at 2^-200, which is 0
-      const float y = fmaxf((x[j] - m) * kLog2e, -200.f), e = exp2_fast(y);
-      l += e;
-      t = __builtin_fmaf(e, y, t);
-    }
-  }
-  l = wave_sum(l);
-  t = wave_sum(t);
-  if ((tid & 63) == 0) s_sums[tid >> 6] = Sums{m, l, t};
-  __syncthreads();
-  if (tid == 0) {
-    Sums s = s_sums[0];
-#pragma unroll
-    for (int i = 1; i < kThreads / 64; ++i) s = join(s, s_sums[i]);
-    float* out = a.part + ((int64_t)row * a.parts + part) * 3;
-    out[0] = s.m;
-    out[1] = s.l;
-    out[2] = s.t;
-  }
-}
-
 // counts over a workgroup
 __device__ __forceinline__ int count_all(int n, int* s_count) {
   __syncthreads();
@@ -144,7 +96,7 @@ __device__ __forceinline__ int count_all(int n, int* s_count) {
 // f(logit, id) for each logit of the row above -inf
 template <typename T, typename F>
 __device__ __forceinline__ void each_logit(const T* p, int vocab, F f) {
-  for (int v = threadIdx.x * 8; v < vocab; v += kChunk) {
+  for (int v = threadIdx.x * 8; v < vocab; v += kSpan) {
     float x[8];
     load_logits<T>(p + v, vocab - v, x);
 #pragma unroll
@@ -156,73 +108,203 @@ __device__ __forceinline__ void each_logit(const T* p, int vocab, F f) {
 }
 
 template <typename T, bool TOP>
-__global__ __launch_bounds__(kThreads) void score_join_kernel(ScoreArgs a) {
-  constexpr int kGroups = 256, kKeys = 1024;  // what a row's lists hold
-  __shared__ Sums s_sums;
-  __shared__ float s_max[kThreads];
-  __shared__ float s_bar;
-  __shared__ int s_groups[kGroups], s_count, s_keys_n;
-  __shared__ uint64_t s_keys[kKeys];
-  const int row = blockIdx.x, tid = threadIdx.x;
+__global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
+  constexpr int kList = 256, kKeys = 1024;  // what a row's lists hold
+  constexpr int kKept = 8;                  // maxima of a thread in registers
+  __shared__ Sums s_sums[kThreads / 64];
+  __shared__ int s_last;
+  __shared__ __align__(16) union {
+    float maxima[kKept * kThreads];
+    uint64_t keys[kKeys];
+  } s_row;
+  float* const s_maxima = s_row.maxima;
+  const bool local = a.parts == 1 && a.groups <= kKept * kThreads;  // the maxima need not leave the workgroup
+  const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x;
+  const int lo = part * a.range, hi = min(lo + a.range, a.vocab);
   const T* const p = (const T*)a.logits + row * a.row_stride;
-
-  if (tid < 64) {  // the parts, a lane to each
-    Sums s{-INFINITY, 0.f, 0.f};
-    for (int i = tid; i < a.parts; i += 64) {
-      const float* in = a.part + ((int64_t)row * a.parts + i) * 3;
-      s = join(s, Sums{in[0], in[1], in[2]});
-    }
-    const float m = wave_max(s.m);
-    const float d = s.m == -INFINITY ? -200.f : fmaxf((s.m - m) * kLog2e, -200.f), f = exp2_fast(d);
-    const float t = wave_sum(f * (s.t + d * s.l)), l = wave_sum(f * s.l);
-    if (tid == 0) {
-      const float norm = logf(l);
-      if (a.entropy) a.entropy[row] = m == -INFINITY ? 0.f : norm - kLn2 * t / l;
-      if (a.logprob) {
-        const int token = a.tokens[row];
-        const float x = token >= 0 && token < a.vocab ? load_tame(p + token) : -INFINITY;
-        a.logprob[row] = x == -INFINITY ? -INFINITY : (x - m) - norm;
+  float m = -INFINITY, l = 0.f, t = 0.f;  // m is the wave's
+  float* const maxima = TOP ? a.maxima + (int64_t)row * a.groups + tid / 4 : nullptr;
+  u32x4 raw[kVectors][8 / Elem<T>::kVec], next[kVectors][8 / Elem<T>::kVec];
+  auto load = [&](int at) {
+    const bool whole = at + kChunk <= hi;
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+      for (int i = 0; i < 8 / Elem<T>::kVec; ++i) {
+        const int v = at + u * kSpan + tid * 8 + i * Elem<T>::kVec;
+        if (whole)
+          __builtin_memcpy(&next[u][i], p + v, 16);
+        else
+          next[u][i] = load_raw<T>(p + v, hi - v);
       }
-      s_sums = Sums{m, norm, 0.f};
+  };
+  load(lo);
+  for (int at = lo; at < hi; at += kChunk) {
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u)
+#pragma unroll
+      for (int i = 0; i < 8 / Elem<T>::kVec; ++i) raw[u][i] = next[u][i];
+    if (at + kChunk < hi) load(at + kChunk);
+    float group = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8 / Elem<T>::kVec; ++i) unpack<T>(raw[u][i], x + i * Elem<T>::kVec);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __builtin_canonicalizef(x[j]);
+      float top = largest(x);
+      if (__any(top > m)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = tame(x[j]);
+        top = tame(top);
+        const float mn = fmaxf(m, wave_max(top));
+        if (m != -INFINITY) {
+          const float d = fmaxf((m - mn) * kLog2e, -200.f), f = exp2_fast(d);
+          t = f * (t + d * l);
+          l *= f;
+        }
+        m = mn;
+      }
+      if (TOP) group = max3(group, top, top);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // -inf and NaN end at 2^-200, which is 0
+        const float y = fmaxf((x[j] - m) * kLog2e, -200.f), e = exp2_fast(y);
+        l += e;
+        t = __builtin_fmaf(e, y, t);
+      }
+    }
+    if constexpr (TOP) {
+      group = fmaxf(group, __uint_as_float(other<0>(__float_as_uint(group))));
+      group = fmaxf(group, __uint_as_float(other<1>(__float_as_uint(group))));
+      group = tame(group);
+      if ((tid & 3) == 0) {
+        if (local)
+          s_maxima[at / kChunk * kGroups + tid / 4] = group;
+        else
+          __hip_atomic_store(maxima + at / kChunk * kGroups, group, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+  }
+  l = wave_sum(l);
+  t = wave_sum(t);
+  if ((tid & 63) == 0) s_sums[tid >> 6] = Sums{m, l, t};
+  __syncthreads();
+  if (tid < 64) {
+    Sums s = s_sums[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 64; ++i) s = join(s, s_sums[i]);
+    if (tid == 0) s_sums[0] = s;
+    if (a.parts > 1 && tid == 0) {
+      float* const out = a.part + ((int64_t)row * a.parts + part) * 4;
+      share2(out, s.m, s.l);
+      share2(out + 2, s.t, 0.f);
+    }
+  }
+  if (a.parts > 1) {
+    if (!last_of(a.arrived + row, a.parts, &s_last)) return;
+    if (tid < 64) {  // the parts, a lane to each
+      Sums s{-INFINITY, 0.f, 0.f};
+      for (int i = tid; i < a.parts; i += 64) {
+        const float* const in = a.part + ((int64_t)row * a.parts + i) * 4;
+        const float2 x = shared2(in), y = shared2(in + 2);
+        s = join(s, Sums{x.x, x.y, y.x});
+      }
+      const float top = wave_max(s.m);
+      const float d = s.m == -INFINITY ? -200.f : fmaxf((s.m - top) * kLog2e, -200.f), f = exp2_fast(d);
+      s.t = wave_sum(f * (s.t + d * s.l));
+      s.l = wave_sum(f * s.l);
+      s.m = top;
+      if (tid == 0) s_sums[0] = s;
+    }
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's maxima are where all see them
+  }
+  __syncthreads();
+  const Sums sums = s_sums[0];
+  const float norm = logf(sums.l);
+  m = sums.m;
+  if (tid == 0) {
+    if (a.entropy) a.entropy[row] = m == -INFINITY ? 0.f : norm - kLn2 * sums.t / sums.l;
+    if (a.logprob) {
+      const int token = a.tokens[row];
+      const float x = token >= 0 && token < a.vocab ? load_tame(p + token) : -INFINITY;
+      a.logprob[row] = x == -INFINITY ? -INFINITY : (x - m) - norm;
     }
   }
   if constexpr (TOP) {
+    __shared__ __align__(16) float s_max[kThreads];
+    __shared__ float s_bar[kThreads / 64];
+    __shared__ int s_groups[kList], s_count, s_keys_n;
+    uint64_t* const s_keys = s_row.keys;
     // A bar that at least `top` logits reach, where so many threads have met a
     // logit at all: the top-th largest of what the threads find largest.
-    const float* const maxima = a.maxima + (int64_t)row * a.groups;
-    float mine = -INFINITY;
-    for (int g = tid; g < a.groups; g += kThreads) mine = fmaxf(mine, maxima[g]);
-    s_max[tid] = mine;
+    const float* const all = a.maxima + (int64_t)row * a.groups;
+    auto maximum = [&](int g) { return __hip_atomic_load(all + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+    float kept[kKept], mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const int g = i * kThreads + tid;
+      kept[i] = g >= a.groups ? -INFINITY : local ? s_maxima[g] : maximum(g);
+    }
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) mine = fmaxf(mine, kept[i]);
+    for (int g = kKept * kThreads + tid; g < a.groups; g += kThreads) mine = fmaxf(mine, maximum(g));
     if (tid == 0) s_count = s_keys_n = 0;
-    __syncthreads();
-    int above = 0;
+    // The bar: a value that `top` threads' logits reach, where so many have met
+    // a logit at all.  The best of what each wave says for itself costs an eighth
+    // of ranking all threads together and lets about four times `top` groups pass.
+    float least;
+    if (a.top <= kFewTop) {
+      int above = 0;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), i)) > mine;
+      least = -wave_max(above < a.top ? -mine : -INFINITY);
+    } else {
+      s_max[tid] = mine;
+      __syncthreads();
+      int above = 0;
 #pragma unroll 8
-    for (int i = 0; i < kThreads; ++i) above += s_max[i] > mine || (s_max[i] == mine && i < tid);
-    if (above == a.top - 1) s_bar = mine;
+      for (int i = 0; i < kThreads; i += 4) {
+        const float4 x = *(const float4*)(s_max + i);
+        above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+      }
+      least = -wave_max(above < a.top ? -mine : -INFINITY);
+    }
+    if ((tid & 63) == 0) s_bar[tid >> 6] = least;
     __syncthreads();
-    const float bar = s_bar;
-    for (int g = tid; g < a.groups; g += kThreads) {
-      const float x = maxima[g];
+    const float bar = a.top <= kFewTop ? fmaxf(fmaxf(s_bar[0], s_bar[1]), fmaxf(s_bar[2], s_bar[3]))
+                                       : fminf(fminf(s_bar[0], s_bar[1]), fminf(s_bar[2], s_bar[3]));
+    auto list = [&](float x, int g) {
       if (x >= bar && x > -INFINITY) {
         const int at = atomicAdd(&s_count, 1);
-        if (at < kGroups) s_groups[at] = g;
+        if (at < kList) s_groups[at] = g;
       }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) list(kept[i], i * kThreads + tid);
+    for (int g = kKept * kThreads + tid; g < a.groups; g += kThreads) list(maximum(g), g);
     __syncthreads();
     const int groups = s_count;
-    if (groups <= kGroups) {
-      for (int i = tid; i < groups * kGroup; i += kThreads) {
-        const int id = s_groups[i / kGroup] * kGroup + i % kGroup;
-        if (id >= a.vocab) continue;
-        const float x = load_tame(p + id);
-        if (x >= bar && x > -INFINITY) {
-          const int at = atomicAdd(&s_keys_n, 1);
-          if (at < kKeys) s_keys[at] = pack_key(x, id);
+    if (groups <= kList) {
+      for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {  // 8 logits each
+        const int g = s_groups[i / (4 * kVectors)];
+        const int id = g / kGroups * kChunk + i / 4 % kVectors * kSpan + g % kGroups * 32 + i % 4 * 8;
+        float x[8];
+        load_logits<T>(p + id, a.vocab - id, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y = tame(x[j]);
+          if (y >= bar && y > -INFINITY) {
+            const int at = atomicAdd(&s_keys_n, 1);
+            if (at < kKeys) s_keys[at] = pack_key(y, id + j);
+          }
         }
       }
     }
     __syncthreads();
-    if (groups > kGroups || s_keys_n > kKeys) {
+    if (groups > kList || s_keys_n > kKeys) {
       // Many equal logits, or few ids left in few groups.  The bar is found bit
       // by bit, and among the logits equal to it the last id, each by a pass
       // over the row.
@@ -257,7 +339,6 @@ __global__ __launch_bounds__(kThreads) void score_join_kernel(ScoreArgs a) {
     }
     // each key to the place of its rank
     const int n = min(s_keys_n, kKeys);
-    const float m = s_sums.m, norm = s_sums.l;
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t key = s_keys[i];
       int rank = 0;
@@ -274,15 +355,7 @@ __global__ __launch_bounds__(kThreads) void score_join_kernel(ScoreArgs a) {
   }
 }
 
-int groups_of(int vocab) { return (int)(((int64_t)vocab + kGroup - 1) / kGroup); }
-
-// parts of a row: what gives each CU eight workgroups, of at least a step each
-int parts_of(int rows, int vocab, int cus) {
-  const int64_t most = ((int64_t)vocab + kChunk - 1) / kChunk;
-  int64_t n = ((int64_t)8 * cus + rows - 1) / rows;
-  if (n > most) n = most;
-  return (int)(n > kMaxParts ? kMaxParts : n);
-}
+int steps_of(int vocab) { return (vocab + kChunk - 1) / kChunk; }
 
 }  // namespace
 
@@ -291,6 +364,7 @@ struct domino_scores : HandleBase {
   int cus = 256;
   float* part = nullptr;
   float* maxima = nullptr;
+  int32_t* arrived = nullptr;
 };
 
 static thread_local char t_err[256] = "";
@@ -321,10 +395,13 @@ extern "C" domino_status_t domino_scores_create(const domino_scores_config_t* cf
     (void)hipGetLastError();
     h->cus = 256;
   }
-  h->part = (float*)h->take(((size_t)8 * h->cus + cfg->max_rows) * 3 * sizeof(float));
-  bool ok = h->part != nullptr;
+  const int most_parts = steps_of(cfg->vocab) < kMaxParts ? steps_of(cfg->vocab) : kMaxParts;
+  h->part = (float*)h->take((size_t)cfg->max_rows * most_parts * 4 * sizeof(float));
+  h->arrived = (int32_t*)h->take((size_t)cfg->max_rows * sizeof(int32_t));
+  bool ok = h->part && h->arrived &&
+            hipMemset(h->arrived, 0, (size_t)cfg->max_rows * sizeof(int32_t)) == hipSuccess;
   if (cfg->max_top) {
-    h->maxima = (float*)h->take((size_t)cfg->max_rows * groups_of(cfg->vocab) * sizeof(float));
+    h->maxima = (float*)h->take((size_t)cfg->max_rows * steps_of(cfg->vocab) * kGroups * sizeof(float));
     ok = ok && h->maxima;
   }
   if (!ok || hipDeviceSynchronize() != hipSuccess) {
@@ -346,19 +423,12 @@ extern "C" void domino_scores_destroy(domino_scores_t* h) {
 extern "C" const char* domino_scores_last_error(const domino_scores_t* h) { return h ? h->err : t_err; }
 
 template <typename T>
-static hipError_t launch_scores(const ScoreArgs& a, hipStream_t st) {
+static void launch_scores(const ScoreArgs& a, hipStream_t st) {
   const dim3 grid(a.parts, a.rows);
   if (a.top)
     hipLaunchKernelGGL((score_kernel<T, true>), grid, dim3(kThreads), 0, st, a);
   else
     hipLaunchKernelGGL((score_kernel<T, false>), grid, dim3(kThreads), 0, st, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;  // the join would follow the parts of an earlier call
-  if (a.top)
-    hipLaunchKernelGGL((score_join_kernel<T, true>), dim3(a.rows), dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((score_join_kernel<T, false>), dim3(a.rows), dim3(64), 0, st, a);
-  return hipGetLastError();
 }
 
 extern "C" domino_status_t domino_scores_run(domino_scores_t* h, const void* logits, int64_t row_stride, int32_t rows,
@@ -387,22 +457,34 @@ extern "C" domino_status_t domino_scores_run(domino_scores_t* h, const void* log
   a.row_stride = row_stride;
   a.rows = rows;
   a.vocab = f.vocab;
-  const int parts = parts_of(rows, f.vocab, h->cus);
-  a.range = ((f.vocab + parts - 1) / parts + kChunk - 1) / kChunk * kChunk;
+  // Parts of a row, of at least a step each: as many as give each CU eight
+  // workgroups (777 rows of 50257 in 3 parts 22 us, undivided 27).  For the
+  // likeliest ids four, and none from two rows to a CU on, where the maxima then
+  // stay in LDS (1024 rows of 151936 undivided 65 us, in 2 parts 74; 256 rows in 4
+  // parts and undivided 32).
+  const int steps = steps_of(f.vocab);
+  int parts = !top ? (8 * h->cus + rows - 1) / rows : rows >= 2 * h->cus ? 1 : (4 * h->cus + rows - 1) / rows;
+  if (parts > steps) parts = steps;
+  if (parts > kMaxParts) parts = kMaxParts;
+  a.range = (steps + parts - 1) / parts * kChunk;
   a.parts = (f.vocab + a.range - 1) / a.range;
+  a.groups = steps * kGroups;
   a.top = top;
   a.tokens = tokens;
   a.part = h->part;
   a.maxima = h->maxima;
-  a.groups = groups_of(f.vocab);
+  a.arrived = h->arrived;
   a.logprob = logprob;
   a.entropy = entropy;
   a.ids = top_ids;
   a.values = top_logprob;
   DeviceGuard dg(h->device);
   (void)hipGetLastError();
-  const hipError_t e = f.dtype == DOMINO_DTYPE_BF16 ? launch_scores<bf16_t>(a, (hipStream_t)stream)
-                                                    : launch_scores<float>(a, (hipStream_t)stream);
+  if (f.dtype == DOMINO_DTYPE_BF16)
+    launch_scores<bf16_t>(a, (hipStream_t)stream);
+  else
+    launch_scores<float>(a, (hipStream_t)stream);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess)
     return say(h->err, DOMINO_ERR_HIP, "run: kernel launch failed: %s", hipGetErrorString(e));
   h->err[0] = 0;

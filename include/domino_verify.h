@@ -315,7 +315,7 @@ typedef struct domino_scores domino_scores_t;
 
 /* Validates the configuration, checks that the current HIP device is gfx950
  * and allocates the workspace (statistics of parts of rows and, with max_top,
- * V / 8 bytes a row).  Synchronises the device. */
+ * V / 32 bytes a row).  Synchronises the device. */
 domino_status_t domino_scores_create(const domino_scores_config_t* cfg, domino_scores_t** out);
 
 /* Scores of rows of logits, row i at logits + i * row_stride (elements, >= 0).  With
