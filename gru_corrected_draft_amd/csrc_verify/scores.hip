@@ -29,7 +29,7 @@ constexpr int kSpan = kThreads * 8;   // logits that a workgroup reads at once
 constexpr int kChunk = kVectors * kSpan;  // logits of a step of a workgroup
 // Four lanes' logits of a step leave one maximum: kVectors runs of 32, kSpan apart.
 constexpr int kGroups = kThreads / 4;  // of a step
-constexpr int kMaxTop = 64, kFewTop = 24;
+constexpr int kMaxTop = 64;
 constexpr int kMaxParts = 128;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
   if constexpr (TOP) {
     __shared__ __align__(16) float s_max[kThreads];
     __shared__ float s_bar[kThreads / 64];
-    __shared__ int s_groups[kList], s_count, s_keys_n;
+    __shared__ int s_groups[kList], s_count, s_keys_n, s_best_n;
     uint64_t* const s_keys = s_row.keys;
     // A bar that at least `top` logits reach, where so many threads have met a
     // logit at all: the top-th largest of what the threads find largest.
@@ -251,31 +251,29 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
 #pragma unroll
     for (int i = 0; i < kKept; ++i) mine = fmaxf(mine, kept[i]);
     for (int g = kKept * kThreads + tid; g < a.groups; g += kThreads) mine = fmaxf(mine, maximum(g));
-    if (tid == 0) s_count = s_keys_n = 0;
-    // The bar: a value that `top` threads' logits reach, where so many have met
-    // a logit at all.  The best of what each wave says for itself costs an eighth
-    // of ranking all threads together and lets about four times `top` groups pass.
-    float least;
-    if (a.top <= kFewTop) {
-      int above = 0;
+    s_max[tid] = -INFINITY;
+    if (tid == 0) s_count = s_keys_n = s_best_n = 0;
+    __syncthreads();
+    // The bar: the top-th largest of what the threads find largest, which `top`
+    // logits reach, where so many threads have met one at all.  Ranked within
+    // each wave first: only its best can be among the best of all.
+    int above = 0;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), i)) > mine;
-      least = -wave_max(above < a.top ? -mine : -INFINITY);
-    } else {
-      s_max[tid] = mine;
-      __syncthreads();
-      int above = 0;
-#pragma unroll 8
-      for (int i = 0; i < kThreads; i += 4) {
-        const float4 x = *(const float4*)(s_max + i);
-        above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
-      }
-      least = -wave_max(above < a.top ? -mine : -INFINITY);
+    for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), i)) > mine;
+    const bool best = above < a.top && mine > -INFINITY;
+    if (best) s_max[atomicAdd(&s_best_n, 1)] = mine;
+    __syncthreads();
+    const int best_n = s_best_n;
+    above = 0;
+#pragma unroll 4
+    for (int i = 0; i < best_n; i += 4) {
+      const float4 x = *(const float4*)(s_max + i);
+      above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
     }
+    const float least = -wave_max(best && above < a.top ? -mine : -INFINITY);
     if ((tid & 63) == 0) s_bar[tid >> 6] = least;
     __syncthreads();
-    const float bar = a.top <= kFewTop ? fmaxf(fmaxf(s_bar[0], s_bar[1]), fmaxf(s_bar[2], s_bar[3]))
-                                       : fminf(fminf(s_bar[0], s_bar[1]), fminf(s_bar[2], s_bar[3]));
+    const float bar = best_n < a.top ? -INFINITY : fminf(fminf(s_bar[0], s_bar[1]), fminf(s_bar[2], s_bar[3]));
     auto list = [&](float x, int g) {
       if (x >= bar && x > -INFINITY) {
         const int at = atomicAdd(&s_count, 1);
@@ -288,6 +286,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     __syncthreads();
     const int groups = s_count;
     if (groups <= kList) {
+#pragma unroll 2
       for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {  // 8 logits each
         const int g = s_groups[i / (4 * kVectors)];
         const int id = g / kGroups * kChunk + i / 4 % kVectors * kSpan + g % kGroups * 32 + i % 4 * 8;
@@ -342,6 +341,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t key = s_keys[i];
       int rank = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) rank += s_keys[j] > key;
       if (rank < a.top) {
         a.ids[(int64_t)row * a.top + rank] = key_id(key);
