@@ -433,7 +433,17 @@ static RowsArgs4 rows_args(const domino_attention_t* h, const domino_cache_t* c,
   a.max_new = c->max_new;
   a.max_kv = clip_kv(c, f.page_size);
   a.kv_heads = f.kv_heads;
+  a.piece_shift = __builtin_ctz(f.head_dim / 8);
+  const uint32_t per_token = (uint32_t)f.kv_heads << a.piece_shift;
+  a.magic_shift = per_token > 1 ? 32 - __builtin_clz(per_token - 1) : 0;
+  a.magic = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.magic_shift) - per_token)) / per_token + 1);
   return a;
+}
+
+// pieces of a request's new tokens stay in 31 bits
+static bool rows_fit(const domino_attention_t* h, const domino_cache_t* c) {
+  const int most = c->max_new < c->tokens ? c->max_new : c->tokens;
+  return (int64_t)most * h->cfg.kv_heads * (h->cfg.head_dim / 8) < (int64_t)1 << 30;
 }
 
 extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const domino_cache_t* c,
@@ -452,6 +462,7 @@ extern "C" domino_status_t domino_attention_append(domino_attention_t* h, const 
     return say(h->err, DOMINO_ERR_INVALID_ARG,
                "append: k and v must be 16-byte aligned, their strides multiples of 16 bytes");
   if (h->fp4) {
+    if (!rows_fit(h, c)) return say(h->err, DOMINO_ERR_UNSUPPORTED, "append: too many rows for a request");
     const RowsArgs4 a = rows_args(h, c, (void*)k, k_token_stride, k_head_stride, (void*)v, v_token_stride, v_head_stride);
     DeviceGuard dg(h->device);
     (void)hipGetLastError();
@@ -507,6 +518,7 @@ extern "C" domino_status_t domino_attention_read(domino_attention_t* h, const do
   if ((c->tokens > 1 && (k_token_stride < dim || v_token_stride < dim)) ||
       (h->cfg.kv_heads > 1 && (k_head_stride < dim || v_head_stride < dim)))
     return say(h->err, DOMINO_ERR_INVALID_ARG, "read: rows of k or v overlap");
+  if (!rows_fit(h, c)) return say(h->err, DOMINO_ERR_UNSUPPORTED, "read: too many rows for a request");
   const RowsArgs4 a = rows_args(h, c, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride);
   DeviceGuard dg(h->device);
   (void)hipGetLastError();

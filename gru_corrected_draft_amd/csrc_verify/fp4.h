@@ -148,6 +148,9 @@ struct RowsArgs4 {
   const int32_t* kv_len;
   const int32_t* q_start;
   int32_t requests, tokens, max_new, max_kv, kv_heads;
+  int32_t piece_shift;  // 2^that pieces of 8 elements in a row
+  uint32_t magic;       // i / pieces of a token = (high half of magic i, + i) >> magic_shift, i < 2^31
+  int32_t magic_shift;
 };
 
 hipError_t attend_fp4_prepare(int head_dim);
