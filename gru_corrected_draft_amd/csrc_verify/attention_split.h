@@ -43,14 +43,13 @@
 // requests 42 us against 36, one prompt of 512 tokens over 4096 keys 73 against
 // 64).
 //
-// A cache in 4 bits (F4).  What is copied to LDS is the raw tile, a quarter of the
-// bytes; from there it becomes bf16, which holds the sixteen numbers times a power
-// of two exactly, so that all else is as above.
-//   R = 1: fragments of K are read raw and converted in registers; V goes through
-//          a tile in LDS for the transposing read.  Lane half h takes elements
-//          h D / 2 .. of a key and a query, a run of whole blocks of 32.
-//   R > 1: each wave converts what it copied, a step ahead of the products, into
-//          one of two bf16 tiles, so a step still has one barrier.
+// A cache in 4 bits (F4, R = 4 and 8).  What is copied to LDS is the raw tile, a
+// quarter of the bytes; each wave converts what it copied, a step ahead of the
+// products, into one of two bf16 tiles, so a step still has one barrier.  bf16
+// holds the sixteen numbers times a power of two exactly, so all else is as above.
+// 2 requests of up to 2048 tokens over up to 5120 keys take 250 us, 913 TFLOP/s,
+// against 235 over bf16: the conversions are vector instructions, of which there
+// were too many already.
 #pragma once
 #include "attention_bf16.h"
 #include "fp4.h"
@@ -61,6 +60,7 @@ constexpr int kMinShare = 2;  // steps: fewer to a workgroup would be all start 
 
 template <int D, int R, bool F4>
 struct Shape {
+  static_assert(!F4 || R >= 4, "fewer rows have kernels of their own");
   // R = 2: 4 streams with rings of 2 take as long as 2 with rings of 4 (36.1 and
   // 35.6 us, block of 8 requests)
   static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : R == 2 ? 2 : 8 / R);  // streams
@@ -73,7 +73,7 @@ struct Shape {
   static constexpr int kRaw = F4 ? (R == 8 ? 2 : 4) : kRing / N;  // steps in the ring
   static constexpr int kSlot = N * (F4 ? RawTile<D>::kBytes : KeyTile<D>::kBytes);
   // bf16 tiles of a stream besides the ring
-  static constexpr int kTiles = !F4 ? 0 : R == 1 ? KeyTile<D>::kHalf : 2 * N * KeyTile<D>::kBytes;
+  static constexpr int kTiles = F4 ? 2 * N * KeyTile<D>::kBytes : 0;
   static constexpr int kStream = kRaw * kSlot + kTiles;
   static constexpr int kLds = S * kStream;
   static constexpr int kJoin = kLds >= 32 * W * D * 4 ? 32 : kLds >= 16 * W * D * 4 ? 16 : 8;  // rows joined at a time
@@ -254,13 +254,9 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
   uint32_t src[T::kChunkLoads];
 #pragma unroll
   for (int j = 0; j < T::kChunkLoads; ++j) src[j] = T::source(j, lane, 2 * a.row);
-  uint32_t raw_src[2][RawTile<D>::kData];
+  uint32_t raw_src[RawTile<D>::kData];
 #pragma unroll
-  for (int j = 0; j < RawTile<D>::kData; ++j) {
-    raw_src[0][j] = R == 1 ? RawTile<D>::source_by_row(lane, j) : RawTile<D>::source(lane, j);
-    raw_src[1][j] = RawTile<D>::source(lane, j);
-  }
-  const uint32_t raw_k = RawTile<D>::k_first(lane), raw_k_power = RawTile<D>::k_power(lane);
+  for (int j = 0; j < RawTile<D>::kData; ++j) raw_src[j] = RawTile<D>::source(lane, j);
 
   while (at < end) {
     Request req;
@@ -374,7 +370,7 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
     auto copy_raw = [&](int c, int key, int page, const lds_byte* slot) {
       const char* from = (const char*)(c < 2 ? a.k : a.v) + chunk(key, page);
       const uint32_t row = key & page_mask;
-      RawTile<D>::copy(from + row * (D / 2), from + (D / 2 << a.page_shift) + row * (D / 32), raw_src[c >> 1], slot, c, lane);
+      RawTile<D>::copy(from + row * (D / 2), from + (D / 2 << a.page_shift) + row * (D / 32), raw_src, slot, c, lane);
     };
     // this wave's part of the stream's next tile, into the ring
     auto fetch = [&]() {
@@ -384,15 +380,8 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
       if (next < tiles) look_up();
       const lds_byte* dst = own + slot_in * C::kSlot;
       slot_in = slot_in + 1 == C::kRaw ? 0 : slot_in + 1;
-      if constexpr (F4 && R >= 4) {
+      if constexpr (F4) {
         copy_raw((rg & 2) | own_half, key + 16 * own_half, p0, dst + own_tile * RawTile<D>::kBytes);
-      } else if constexpr (F4) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (R == 1 || rg == x) {
-            copy_raw(2 * x, key, p0, dst);
-            copy_raw(2 * x + 1, key + 16, p1, dst);
-          }
       } else if constexpr (R >= 4) {  // 16 rows of K or of V
         const int x = rg / 2 % 2;
         copy(x ? a.v : a.k, chunk(key + 16 * own_half, p0),
@@ -421,8 +410,9 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
       else
         wait_copies<0>();
     };
-    // F4: waits for the oldest step in the ring, as the walk does below
-    auto take_raw = [&]() -> const lds_byte* {
+    // F4: this wave's part of the next step becomes bf16
+    int tile_in = 0;
+    auto convert = [&]() {
       if (next < tiles) {
         fetch();
         --ahead;
@@ -432,24 +422,9 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
       }
       const lds_byte* slot = own + slot_out * C::kSlot;
       slot_out = slot_out + 1 == C::kRaw ? 0 : slot_out + 1;
-      return slot;
-    };
-    // F4, R > 1: this wave's part of the next step becomes bf16
-    int tile_in = 0;
-    auto convert = [&]() {
-      const lds_byte* slot = take_raw();
-      lds_byte* const to = tiles16 + tile_in * (N * T::kBytes);
+      RawTile<D>::convert(slot + own_tile * RawTile<D>::kBytes, (rg & 2) | own_half,
+                          tiles16 + tile_in * (N * T::kBytes) + own_tile * T::kBytes, lane);
       tile_in ^= 1;
-      if constexpr (R >= 4) {
-        RawTile<D>::convert(slot + own_tile * RawTile<D>::kBytes, (rg & 2) | own_half, to + own_tile * T::kBytes, lane);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (rg == x) {
-            RawTile<D>::convert(slot, 2 * x, to, lane);
-            RawTile<D>::convert(slot, 2 * x + 1, to, lane);
-          }
-      }
     };
     // the ring's first copies leave before the queries are read, so that the
     // wait for the queries does not hold them up
@@ -465,9 +440,9 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
       const int row = min(w0 + n, last), tok = row / a.group;
       pos = req.kv - req.n + tok;
       const bf16_t* qp = (const bf16_t*)a.q + (req.q0 + tok) * a.q_tok +
-                         (h * a.group + row - tok * a.group) * a.q_head + (F4 && R == 1 ? D / 2 : 8) * h2;
+                         (h * a.group + row - tok * a.group) * a.q_head + 8 * h2;
 #pragma unroll
-      for (int kc = 0; kc < D / 16; ++kc) Q[kc] = load_frag_bf16(qp + (F4 && R == 1 ? 8 : 16) * kc);
+      for (int kc = 0; kc < D / 16; ++kc) Q[kc] = load_frag_bf16(qp + 16 * kc);
     }
     // the queries are waited for here, not in the walk, where the wait would
     // hold up the copies in flight
@@ -496,23 +471,14 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
       return true;
     };
 
-    if constexpr (F4 && R > 1) {
+    if constexpr (F4) {
       if (first * STEP + stream * N < tiles) convert();
     }
 
 #pragma unroll 1
     for (int i = first * STEP + stream * N; i - stream * N < tiles; i += STEP) {
-      lds_byte* const tile = !F4 ? own + slot_out * C::kSlot : R == 1 ? tiles16 - T::kHalf : tiles16 + (tile_in ^ 1) * (N * T::kBytes);
-      v8s raw_frags[D / 16];
-      if constexpr (F4 && R == 1) {
-        if (i >= tiles) break;
-        const lds_byte* slot = take_raw();
-        RawTile<D>::keys(slot, raw_k, raw_k_power, raw_frags);
-        RawTile<D>::convert(slot, 2, tile, lane);
-        RawTile<D>::convert(slot, 3, tile, lane);
-        if ((i < range.whole_lo || i >= range.whole_hi) && note(tile, tile_of(span, i) * 32))
-          clear_odd_values<D>(tile, 0, 1, lane);
-      } else if constexpr (R == 1) {
+      lds_byte* const tile = F4 ? tiles16 + (tile_in ^ 1) * (N * T::kBytes) : own + slot_out * C::kSlot;
+      if constexpr (R == 1) {
         if (i >= tiles) break;
         if (next < tiles) {
           fetch();
@@ -554,14 +520,14 @@ __global__ __launch_bounds__((Shape<D, R, F4>::kThreads), (D < 256 ? 2 : 1)) voi
         if (i >= tiles) continue;
       }
       if constexpr (!F4) slot_out = slot_out + 1 == C::kRaw ? 0 : slot_out + 1;
-      if constexpr (F4 && R > 1) {
+      if constexpr (F4) {
         if (i + STEP < tiles) convert();
       }
       if (R > 1 && (i >= mine_range.some_hi || (i + N <= mine_range.some_lo && i >= mine_range.sink_hi)))
         continue;  // none of this wave's rows sees it
       v16f s[N];
 #pragma unroll
-      for (int x = 0; x < N; ++x) s[x] = F4 && R == 1 ? scores<D>(raw_frags, Q) : scores<D>(tile + x * T::kBytes, k0_off, Q);
+      for (int x = 0; x < N; ++x) s[x] = scores<D>(tile + x * T::kBytes, k0_off, Q);
       ValueFrags v = read_values<D>(tile, v0_off, 0);
       __builtin_amdgcn_sched_barrier(0);
       if (i < mine_range.whole_lo || i + N > mine_range.whole_hi) {

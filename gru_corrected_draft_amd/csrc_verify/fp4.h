@@ -11,8 +11,6 @@
 #include "attention_bf16.h"
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
-typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
 // the scale operand of the conversions: a float whose exponent counts
 __device__ __forceinline__ float power_of(uint32_t byte) { return __uint_as_float(byte << 23); }
@@ -55,15 +53,6 @@ struct RawTile {
     return row_of(lane) * (D / 2) + block_of(lane, j) * 16;
   }
 
-  // Row after row instead, for fragments read raw (lanes at one block of 16
-  // rows), with the blocks of a row permuted so that these rows' pieces fall into
-  // different banks
-  static __device__ __forceinline__ int permuted(int row) { return row / (16 / kBlocks) % kBlocks; }
-  static __device__ __forceinline__ uint32_t source_by_row(int lane, int j) {
-    const int piece = j * 64 + lane, row = piece / kBlocks;
-    return row * (D / 2) + (((piece % kBlocks) ^ permuted(row & 15)) << 4);
-  }
-
   // chunk c of the tile at `slot`, from its elements and powers in the cache
   static __device__ __forceinline__ void copy(const char* data, const char* powers, const uint32_t (&src)[kData],
                                               const lds_byte* slot, int c, int lane) {
@@ -91,49 +80,7 @@ struct RawTile {
       }
     }
   }
-
-  // LDS bytes from the slot to this lane's first block of its key, and to its power
-  static __device__ __forceinline__ int key_of(int lane) {
-    const int m = lane & 31;
-    return 16 * (m >> 4) + 8 * ((m >> 2) & 1) + 4 * ((m >> 3) & 1) + (m & 3);
-  }
-  static __device__ __forceinline__ uint32_t k_first(int lane) {
-    const int key = key_of(lane), row = key & 15;
-    return (key >> 4) * kChunk + row * (D / 2) + (((lane >> 5) * (kBlocks / 2) ^ permuted(row)) << 4);
-  }
-  static __device__ __forceinline__ uint32_t k_power(int lane) {
-    const int key = key_of(lane);
-    return kPowers + (key >> 4) * (D / 2) + (key & 15) * kBlocks + (lane >> 5) * (kBlocks / 2);
-  }
-  // fragments of K: half h of the lanes holds the elements from h D / 2 on
-  static __device__ __forceinline__ void keys(const lds_byte* slot, uint32_t first, uint32_t power, v8s (&k)[D / 16]) {
-    uint32_t powers;
-    if constexpr (D == 64)
-      powers = slot[power];
-    else if constexpr (D == 128)
-      powers = *(const lds_u16*)(slot + power);
-    else
-      powers = *(const lds_u32*)(slot + power);
-#pragma unroll
-    for (int x = 0; x < kBlocks / 2; ++x) {
-      const u32x4 w = __builtin_bit_cast(u32x4, lds_read16(slot + (first ^ (x << 4))));
-      const float p = power_of(powers >> (8 * x) & 255);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) k[4 * x + q] = from_fp4(w[q], p);
-    }
-  }
 };
-
-// S^T = K Q^T from fragments of K in registers
-template <int D>
-__device__ __forceinline__ v16f scores(const v8s (&k)[D / 16], const v8s (&q)[D / 16]) {
-  v16f s;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) s = mfma_32x32(k[c], q[c], s);
-  return s;
-}
 
 // what is done to a row, 8 elements to a lane
 struct RowsArgs4 {
