@@ -122,7 +122,7 @@ __device__ __forceinline__ int few_runs(const AttendArgs& a, const FewArgs& f, i
   return tiles < 0 ? 0 : quotient_up(tiles, __builtin_amdgcn_readlane(size, pick), __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), pick)));
 }
 
-template <int D, int G, int S>
+template <int D, int G, int S, bool FINE>
 __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : D * G <= 256 ? 2 : 1)) void attend_few_kernel(AttendArgs a, FewArgs f) {
   using T = KeyTile<D>;
   using C = FewShape<D, G, S>;
@@ -132,6 +132,8 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_index(), n = lane & 15, q = lane >> 4;
   const int unit = blockIdx.x;
+  // the last row tiles see the most keys and go first
+  const int row_tiles = gridDim.y * gridDim.z, row_tile = row_tiles - 1 - (blockIdx.z * gridDim.y + blockIdx.y);
 
   int b, h, run, runs;
   Request req;
@@ -147,14 +149,14 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
     b = x / f.most;
     run = x - b * f.most;
     req = request_of(a.q_start, a.kv_len, b, a.tokens, a.max_new, a.max_kv);
-    runs = quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per);
+    runs = min(quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per), f.most);
     if (run >= runs) return;
   } else {
     Request mine{0, 0, 0, false};
     if (lane < a.requests) mine = request_of(a.q_start, a.kv_len, lane, a.tokens, a.max_new, a.max_kv);
     const int own = few_runs(a, f, lane < a.requests ? few_tiles(a, mine) : -1, lane);
     const int upto = scan_lanes(own, lane) * a.kv_heads;
-    if (unit == 0 && blockIdx.y == 0 && w == 0) {  // for the join
+    if (unit == 0 && row_tile == 0 && w == 0) {  // for the join
       if (lane == 0) a.plan[0] = 0;
       a.plan[lane + 1] = upto;
     }
@@ -168,9 +170,9 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
     req = of_lane(mine, b);
   }
   req = Request{uniform(req.q0), uniform(req.n), uniform(req.kv), (bool)uniform(req.bad)};
-  const int rows = req.n * a.group, w0 = blockIdx.y * C::kRows;
+  const int rows = req.n * a.group, w0 = row_tile * C::kRows;
   if (w0 >= rows) return;
-  const KeySpan span = uniform(key_span<32>(req, 0, req.n - 1, a.window, a.sinks));
+  const KeySpan span = uniform(key_span<32>(req, w0 / a.group, (min(w0 + C::kRows, rows) - 1) / a.group, a.window, a.sinks));
   const int first = uniform((int)((int64_t)span.count * run / runs)), stop = uniform((int)((int64_t)span.count * (run + 1) / runs));
 
   int pos[G];
@@ -183,9 +185,6 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
 #pragma unroll
     for (int c = 0; c < KC; ++c) Q[g][c] = load_frag_bf16(qp + 8 * c);
   }
-  KeySpan seen = span;
-  seen.pmin = uniform(req.kv - req.n + min(w0, rows - 1) / a.group);
-  seen.pmax = uniform(req.kv - req.n + min(w0 + 16 * G - 1, rows - 1) / a.group);
 
   v4f o[G][DT];
   float m[G], l[G];
@@ -246,7 +245,7 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
   for (; i < stop; i += S) {
     const int at = key;  // of this tile
     if (i + S < stop) look_up(i + S);
-    const bool whole = all_visible(seen, at, 32, a.window, a.sinks);
+    const bool whole = all_visible(span, at, 32, a.window, a.sinks);
     // scores, and V on its way through LDS
     v4f s[G][2];
 #pragma unroll
@@ -302,7 +301,7 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
           for (int j = 0; j < 4; ++j)
             if (!visible(at + 16 * t + 4 * q + j, pos[g], a.window, a.sinks)) s[g][t][j] = -INFINITY;
     }
-    // weights, as the sum of two bf16 numbers
+    // weights, FINE as the sum of two bf16 numbers
     v8s p[G], rest[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -328,12 +327,16 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
       u32x4 hi, lo;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        if constexpr (!FINE) {
+          hi[j] = pack_bf16(e[2 * j], e[2 * j + 1]);
+          continue;
+        }
         const uint32_t x = __float_as_uint(e[2 * j]) & 0xFFFF0000u, y = __float_as_uint(e[2 * j + 1]) & 0xFFFF0000u;
         hi[j] = x >> 16 | y;
         lo[j] = pack_bf16(e[2 * j] - __uint_as_float(x), e[2 * j + 1] - __uint_as_float(y));
       }
       p[g] = __builtin_bit_cast(v8s, hi);
-      rest[g] = __builtin_bit_cast(v8s, lo);
+      if constexpr (FINE) rest[g] = __builtin_bit_cast(v8s, lo);
     }
     // O^T += V^T P^T: lane j of a quarter points at row j / 4 of four, elements
     // 4 (j % 4), and gets element j of the four rows
@@ -350,7 +353,7 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         o[g][x] = mfma_16x16(v, p[g], o[g][x]);
-        o[g][x] = mfma_16x16(v, rest[g], o[g][x]);
+        if constexpr (FINE) o[g][x] = mfma_16x16(v, rest[g], o[g][x]);
       }
     }
   }
@@ -366,7 +369,7 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
     }
   }
   const bool alone = runs == 1;
-  const int64_t part = ((int64_t)unit * gridDim.y + blockIdx.y) * C::kRows;  // rows
+  const int64_t part = ((int64_t)unit * row_tiles + row_tile) * C::kRows;  // rows
   float* const sums = (float*)s_tiles;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -441,7 +444,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, FewArgs f, 
   int runs;
   int64_t first;
   if (a.requests > 64) {
-    runs = quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per);
+    runs = min(quotient_up(few_tiles(a, req), f.per, 1.f / (float)f.per), f.most);
     first = (int64_t)b * f.most * a.kv_heads + h;
   } else {
     first = a.plan[b] + h;
@@ -473,26 +476,32 @@ __global__ __launch_bounds__(256) void join_few_kernel(AttendArgs a, FewArgs f, 
     a.lse[(int64_t)(req.q0 + tok) * a.q_heads + hq] = den == 0.f ? -INFINITY : top * a.scale + logf(den);
 }
 
-template <int D, int G, int S>
+template <int D, int G, int S, bool FINE>
 hipError_t allow_few() {
-  return hipFuncSetAttribute((const void*)attend_few_kernel<D, G, S>, hipFuncAttributeMaxDynamicSharedMemorySize,
+  return hipFuncSetAttribute((const void*)attend_few_kernel<D, G, S, FINE>, hipFuncAttributeMaxDynamicSharedMemorySize,
                              FewShape<D, G, S>::kLds);
 }
+
+constexpr int kMostY = 1 << 15;  // below the limit of a grid's second dimension
 
 // rows of the workspace that parts may take: as attend_split_floats
 constexpr int few_rows(int head_dim, int cus) { return 2 * cus * (head_dim == 256 ? 128 : 256); }
 
+// the most keys that the rows of a request see
+inline int64_t few_keys(const AttendArgs& a) {
+  const int64_t seen = (int64_t)a.window + a.max_new + a.sinks + 65;
+  return a.window && seen < a.max_kv ? seen : a.max_kv;
+}
+
 // `units`: workgroups that the chip holds at once, divided among the row tiles
-template <int D, int G, int S>
+template <int D, int G, int S, bool FINE>
 void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
   using C = FewShape<D, G, S>;
   constexpr int PER = 1024 / D;
   const int64_t rows = (int64_t)a.max_new * a.group;
   const int row_tiles = (int)((rows + C::kRows - 1) / C::kRows);
   const int64_t segments = (int64_t)a.requests * a.kv_heads;
-  int64_t keys = a.max_kv;  // the most that a request's rows see
-  if (a.window && (int64_t)a.window + rows + a.sinks + 65 < keys) keys = (int64_t)a.window + rows + a.sinks + 65;
-  const int64_t tiles = (keys + 31) / 32 + 2;
+  const int64_t tiles = (few_keys(a) + 31) / 32 + 2;
   FewArgs f{};
   f.least = S < 8 ? S : 8;
   units /= row_tiles;
@@ -510,7 +519,8 @@ void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
   }
   // row tiles of a unit meet in one XCD's cache
   const int64_t grid = f.units ? f.units : segments;
-  hipLaunchKernelGGL((attend_few_kernel<D, G, S>), dim3((unsigned)grid, row_tiles), dim3(C::kThreads), C::kLds, st, a, f);
+  const int y = row_tiles < kMostY ? row_tiles : kMostY, z = (row_tiles + y - 1) / y;
+  hipLaunchKernelGGL((attend_few_kernel<D, G, S, FINE>), dim3((unsigned)grid, y, z), dim3(C::kThreads), C::kLds, st, a, f);
   if (!f.units || hipPeekAtLastError() != hipSuccess) return;  // the join would follow the parts of an earlier call
   hipLaunchKernelGGL((join_few_kernel<D, C::kRows>), dim3((unsigned)((rows + PER - 1) / PER), a.kv_heads, a.requests),
                      dim3(256), 0, st, a, f, row_tiles);

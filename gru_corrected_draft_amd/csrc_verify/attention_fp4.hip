@@ -12,30 +12,55 @@ constexpr int kRowGroups = D == 256 ? 1 : 2;
 template <int D>
 constexpr int kManyWaves = D == 256 ? 8 : 16;  // what a CU holds
 
+template <int D, bool FINE>
+hipError_t allow_few_d() {
+  hipError_t e = allow_few<D, 1, kManyWaves<D>, FINE>();
+  if (e == hipSuccess) e = allow_few<D, kRowGroups<D>, 4, FINE>();
+  return e;
+}
+
 template <int D>
 hipError_t prepare_fp4() {
-  hipError_t e = allow_few<D, 1, 4>();
-  if (e == hipSuccess) e = allow_few<D, 1, kManyWaves<D>>();
-  if (D < 256 && e == hipSuccess) e = allow_few<D, kRowGroups<D>, 4>();
+  hipError_t e = allow_few_d<D, true>();
+  if (e == hipSuccess) e = allow_few_d<D, false>();
   if constexpr (D < 256) {
+    if (e == hipSuccess) e = allow_few<D, 1, 4, true>();
+  }
+  if constexpr (D == 128) {
     if (e == hipSuccess) e = allow_lds<D, 8, true>();
   }
-  if (e == hipSuccess) e = allow_lds<D, 4, true>();
+  if constexpr (D > 64) {
+    if (e == hipSuccess) e = allow_lds<D, 4, true>();
+  }
   return e;
+}
+
+template <int D, bool FINE>
+void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
+  const int64_t rows = (int64_t)a.max_new * a.group;
+  if ((rows + 15) / 16 * a.requests * a.kv_heads <= cus) return launch_few<D, 1, kManyWaves<D>, FINE>(a, cus, cus, st);
+  if constexpr (FINE) {
+    if (rows <= 16) return launch_few<D, 1, 4, true>(a, 2 * cus, cus, st);
+  }
+  launch_few<D, kRowGroups<D>, 4, FINE>(a, 2 * cus, cus, st);
 }
 
 template <int D>
 void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
-  if (rows <= 64 || (rows <= 128 && a.max_kv <= 4096)) {
-    if ((rows + 15) / 16 * a.requests * a.kv_heads <= cus) return launch_few<D, 1, kManyWaves<D>>(a, cus, cus, st);
-    if (rows <= 16) return launch_few<D, 1, 4>(a, 2 * cus, cus, st);
-    return launch_few<D, kRowGroups<D>, 4>(a, 2 * cus, cus, st);
+  if (rows <= 32) return launch_few_d<D, true>(a, cus, st);
+  if constexpr (D > 64) {
+    // rows times keys for each CU
+    const double work = (double)a.requests * a.kv_heads * rows * few_keys(a) / cus;
+    const int most = D == 256 ? 1 << 16 : rows <= 128 ? 1 << 20 : 1 << 18;
+    if (rows > 64 && work > most) {
+      if constexpr (D == 128) {
+        if (rows > 128) return launch<D, 8, true>(a, cus, st);
+      }
+      return launch<D, 4, true>(a, cus, st);
+    }
   }
-  if constexpr (D < 256) {
-    if (rows > 128) return launch<D, 8, true>(a, cus, st);
-  }
-  launch<D, 4, true>(a, cus, st);
+  launch_few_d<D, false>(a, cus, st);
 }
 
 }  // namespace

@@ -60,7 +60,7 @@ constexpr int kMinShare = 2;  // steps: fewer to a workgroup would be all start 
 
 template <int D, int R, bool F4>
 struct Shape {
-  static_assert(!F4 || R >= 4, "fewer rows have kernels of their own");
+  static_assert(!F4 || (R >= 4 && D >= 128), "the others have kernels of their own");
   // R = 2: 4 streams with rings of 2 take as long as 2 with rings of 4 (36.1 and
   // 35.6 us, block of 8 requests)
   static constexpr int S = D == 256 ? (R == 1 ? 2 : 1) : (R == 1 ? 4 : R == 2 ? 2 : 8 / R);  // streams

@@ -25,7 +25,7 @@ __device__ __forceinline__ v8s from_fp4(uint32_t x, float power) {
   return __builtin_bit_cast(v8s, r);
 }
 
-// A tile of 32 keys as it lies in the cache: four chunks of 16 rows, two of K
+// A tile of 32 keys as it lies in the cache, for heads of 128 and 256: four chunks of 16 rows, two of K
 // and two of V, then their powers.  A piece is the 16 bytes of a block of 32
 // elements.
 template <int D>
@@ -34,21 +34,14 @@ struct RawTile {
   static constexpr int kChunk = 8 * D;         // bytes of 16 rows
   static constexpr int kPowers = 4 * kChunk;   // where the powers begin
   static constexpr int kBytes = kPowers + 2 * D;
-  static constexpr int kData = D <= 128 ? 1 : D / 128;  // copies of a chunk's elements
+  static constexpr int kData = D < 128 ? 1 : D / 128;   // copies of a chunk's elements
   static constexpr int kLoads = 4 * (kData + 1);        // copies of a tile
 
   // Row and block that a lane copies and converts in a chunk's copy j.  The 16
   // lanes that write to LDS together then write 16 different pieces of the
   // bf16 tile's 256 bytes of banks, whose swizzle goes by these bits of the row.
-  static __device__ __forceinline__ int row_of(int lane) {
-    if constexpr (D == 64)
-      return (lane >> 1 & 1) | (lane >> 4 & 1) << 1 | (lane >> 2 & 3) << 2;
-    else
-      return (lane >> 2 & 3) << 2 | lane >> 4;
-  }
-  static __device__ __forceinline__ int block_of(int lane, int j) {
-    return D == 64 ? lane & 1 : (lane & 3) + 4 * j;
-  }
+  static __device__ __forceinline__ int row_of(int lane) { return (lane >> 2 & 3) << 2 | lane >> 4; }
+  static __device__ __forceinline__ int block_of(int lane, int j) { return (lane & 3) + 4 * j; }
   static __device__ __forceinline__ uint32_t source(int lane, int j) {
     return row_of(lane) * (D / 2) + block_of(lane, j) * 16;
   }
@@ -56,28 +49,24 @@ struct RawTile {
   // chunk c of the tile at `slot`, from its elements and powers in the cache
   static __device__ __forceinline__ void copy(const char* data, const char* powers, const uint32_t (&src)[kData],
                                               const lds_byte* slot, int c, int lane) {
-    if (D >= 128 || lane < 32) {
 #pragma unroll
-      for (int j = 0; j < kData; ++j) copy_to_lds(data, src[j], slot + c * kChunk + j * 1024);
-    }
+    for (int j = 0; j < kData; ++j) copy_to_lds(data, src[j], slot + c * kChunk + j * 1024);
     if (lane < D / 32) copy_to_lds(powers, 16 * lane, slot + kPowers + c * (D / 2));
   }
 
   // chunk c, by the wave that copied it (as source says), into a bf16 tile
   static __device__ __forceinline__ void convert(const lds_byte* slot, int c, lds_byte* tile, int lane) {
     using T = KeyTile<D>;
-    if (D >= 128 || lane < 32) {
-      const int row = row_of(lane), swizzle = T::swizzle(row);
-      lds_byte* const to = tile + (c >> 1) * T::kHalf + ((c & 1) * 16 + row) * T::kRow;
+    const int row = row_of(lane), swizzle = T::swizzle(row);
+    lds_byte* const to = tile + (c >> 1) * T::kHalf + ((c & 1) * 16 + row) * T::kRow;
 #pragma unroll
-      for (int j = 0; j < kData; ++j) {
-        const int block = block_of(lane, j);
-        const u32x4 x = __builtin_bit_cast(u32x4, lds_read16(slot + c * kChunk + j * 1024 + lane * 16));
-        const float power = power_of(slot[kPowers + c * (D / 2) + row * kBlocks + block]);
+    for (int j = 0; j < kData; ++j) {
+      const int block = block_of(lane, j);
+      const u32x4 x = __builtin_bit_cast(u32x4, lds_read16(slot + c * kChunk + j * 1024 + lane * 16));
+      const float power = power_of(slot[kPowers + c * (D / 2) + row * kBlocks + block]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *(__attribute__((address_space(3))) v8s*)(to + (((4 * block + q) ^ swizzle) << 4)) = from_fp4(x[q], power);
-      }
+      for (int q = 0; q < 4; ++q)
+        *(__attribute__((address_space(3))) v8s*)(to + (((4 * block + q) ^ swizzle) << 4)) = from_fp4(x[q], power);
     }
   }
 };
