@@ -93,7 +93,7 @@ __device__ __forceinline__ int quotient_up(int x, int y, float inv) {  // about 
 struct FewArgs {
   int32_t units;     // workgroups there are for units; 0: a run is all of a request's tiles
   int32_t per, most; // beyond 64 requests: tiles to a run, and runs to a request, of the longest one
-  int32_t least;     // tiles of a run that are worth a workgroup
+  int32_t least;     // tiles of a run that are worth a workgroup: one to a wave
 };
 
 __device__ __forceinline__ int few_tiles(const AttendArgs& a, const Request& r) {
@@ -493,6 +493,14 @@ inline int64_t few_keys(const AttendArgs& a) {
   return a.window && seen < a.max_kv ? seen : a.max_kv;
 }
 
+// Tiles of the longest request beyond which it is worth cutting: the second launch
+// and the parts cost what several steps do.  One token over 1024 keys takes 11.0 us
+// whole and 13.5 in parts, over 3000 18.6 and 13.5; 8 tokens of 32 requests of 32 heads
+// of 128 over 1024 18.0 and 24.3, over 2048 29.6 and 32.2, 20 requests 27.9 and 25.3; of
+// heads of 256 one token over 600 11.9 and 13.5, over 1024 16.6 and 13.5.
+template <int D>
+constexpr int kWorth = D == 256 ? 32 : 64;
+
 // `units`: workgroups that the chip holds at once, divided among the row tiles
 template <int D, int G, int S, bool FINE>
 void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
@@ -503,11 +511,11 @@ void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
   const int64_t segments = (int64_t)a.requests * a.kv_heads;
   const int64_t tiles = (few_keys(a) + 31) / 32 + 2;
   FewArgs f{};
-  f.least = S < 8 ? S : 8;
+  f.least = S;
   units /= row_tiles;
   const int64_t room = few_rows(D, cus) / (C::kRows * row_tiles);
   if (units > room) units = (int)room;
-  if (2 * segments <= units && tiles > f.least && a.requests * tiles < (int64_t)1 << 30) {
+  if (2 * segments <= units && tiles > kWorth<D> && a.requests * tiles < (int64_t)1 << 30) {
     f.units = units;
     if (a.requests > 64) {
       f.most = (int)(units / segments);

@@ -38,10 +38,18 @@ CASES = [
     ((16, 2), 64, 64, [300, 0, 5], [1300, 4, 700], 0, 0, 0),
     ((16, 2), 64, 64, [300, 1], [1300, 700], 100, 33, 0),
     ((4, 1), 64, 16, [40] * 70, [60 + 9 * (i % 11) for i in range(70)], 0, 0, 0),
-    # beyond 64 requests, each cut into runs of equal length
-    ((4, 1), 64, 16, [2, 0, 1] * 24, [900, 0, 350] * 24, 300, 40, 0),
-    ((8, 2), 256, 32, [1] * 66, [5 + 137 * (i % 9) for i in range(66)], 0, 0, 0),
-    ((8, 2), 256, 32, [1] * 66, [5 + 137 * (i % 9) for i in range(66)], 200, 3, 0),
+    # requests cut into runs: up to 64 of them by their lengths, beyond that each into as many
+    ((8, 2), 128, 16, [1, 1, 0, 1, 1], [5, 800, 3, 32, 900], 0, 0, 4096),
+    ((8, 2), 128, 16, [1, 4, 2, 1], [500, 800, 31, 900], 300, 33, 4096),
+    ((16, 4), 64, 16, [16, 7, 30], [500, 800, 1031], 0, 0, 4096),
+    ((16, 4), 64, 16, [16, 7, 30], [500, 2800, 1031], 2200, 70, 4096),
+    ((8, 2), 256, 16, [9, 1, 20], [500, 800, 31], 0, 0, 4096),
+    ((16, 4), 128, 16, [9] * 20, [20 + 60 * i for i in range(20)], 0, 0, 4096),
+    ((4, 1), 64, 16, [2, 0, 1] * 24, [900, 0, 350] * 24, 0, 0, 8192),
+    ((4, 1), 128, 16, [5, 0, 1] * 24, [900, 4, 350] * 24, 0, 0, 8192),
+    ((4, 1), 128, 16, [5, 0, 1] * 24, [900, 4, 2350] * 24, 2100, 40, 8192),
+    ((8, 2), 256, 32, [1] * 66, [5 + 137 * (i % 9) for i in range(66)], 0, 0, 4096),
+    ((8, 2), 256, 32, [1] * 66, [5 + 137 * (i % 9) for i in range(66)], 1100, 3, 4096),
 ]
 
 
