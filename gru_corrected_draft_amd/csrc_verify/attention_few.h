@@ -1,22 +1,38 @@
-// Attention of few rows over a cache in 4 bits: up to 64 rows of a request and
-// key head (a token of many heads, a draft block).
+// Attention over a cache in 4 bits where a wave converts what it reads: tokens,
+// draft blocks, short prompts, and all calls with heads of 64.
 //
-// A workgroup takes 16 G rows and a run of tiles of 32 keys; each of its S waves
-// works alone on every S-th of them, reads K and V straight into registers, a tile
-// ahead of their use, and keeps its own sums.  Products are 16 x 16 x 32, with both
-// results transposed: S^T = K Q^T (keys x rows) and O^T = V^T P^T.  Lane l (n = l % 16,
-// q = l / 16) holds row n, of S the keys 4 q .. 4 q + 3 of both halves of the
-// tile, which are its slots of the second product's operand, and of O the elements
-// 16 x + 4 q .. + 3 of block x.
+// A workgroup takes 16 G rows (a row tile) of a request and key head and a run of
+// the tiles of 32 keys that they see; each of its S waves works alone on every S-th
+// of them, reads K and V straight into registers, a tile ahead of their use, and
+// keeps its own maximum, sum and output.  A wave waits for no other before the end:
+// with barriers and V shared by row tiles 8 blocks took 63 us for 45 without.
+// Products are 16 x 16 x 32, with both results transposed: S^T = K Q^T (keys x
+// rows) and O^T = V^T P^T.  Lane l (n = l % 16, q = l / 16) holds row n, of S the keys
+// 4 q .. 4 q + 3 of both halves of the tile, which are its slots of the second
+// product's operand, and of O the elements 16 x + 4 q .. + 3 of block x.
 //   K: lane l converts elements q D / 4 .. of key n of a half: fragments as they
 //      are, with the queries' elements dealt alike.
 //   V: bf16 rows go through 64 D bytes of LDS of the wave's own for the transposing
 //      read, swizzled as in KeyTile.
+// FINE keeps each weight as the sum of two bf16 numbers (15 bits), otherwise they
+// are rounded once, as over a bf16 cache by the same rule of rows: beyond 32 rows the
+// second product is no longer hidden (32 blocks over 8 to 16 thousand keys 232 us
+// against 200, 8 blocks over 2 to 4 thousand 24.6 against 22.8).
 //
 // Units.  A unit is a (request, key head, run of its tiles).  Where the requests
-// fill the chip by themselves a run is all of a request's tiles, otherwise each request is
-// cut into as many equal runs as workgroups allow and a second launch joins
-// them.  Every workgroup finds the division by itself, a lane to each request.
+// fill the chip by themselves or are short a run is all of a request's tiles,
+// otherwise each request is cut into as many equal runs as workgroups allow and a
+// second launch joins them.  Every workgroup finds the division by itself, a lane
+// to each request.
+//
+// What bounds it.  64 single tokens over 4 to 8 thousand keys take 90 us, 4.8 TB/s
+// of the cache's bytes (a large copy reaches 5.2, reads alone more).  8 blocks of 16
+// tokens over 2 to 4 thousand keys take 23 us for 5 us of bytes: start, queries and
+// the joining of streams take about 8, then a wave takes 2 us to a tile, of which
+// vector instructions (conversions a third of them) fill 60 % and products 20 %.
+// 32-row tiles share each conversion between two products; the scaled products
+// that take 4-bit keys as they are were left: their sums lose up to 1e-4 of the
+// magnitudes they add.
 #pragma once
 #include "fp4.h"
 
@@ -358,7 +374,7 @@ __global__ __launch_bounds__((FewShape<D, G, S>::kThreads), (D * G <= 128 ? 4 : 
     }
   }
 
-  // join the streams, 16 rows of each half at a time, over the tiles
+  // join the streams, 16 rows at a time, over the tiles
   if (tid == 0) s_bad = 0;
 #pragma unroll
   for (int g = 0; g < G; ++g) {

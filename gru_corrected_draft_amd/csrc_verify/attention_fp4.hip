@@ -5,8 +5,10 @@
 
 namespace {
 
-// Row tiles of 32 rows save conversions over 16 where there are so many; for
-// heads of 256 their sums do not fit in registers.
+// Row tiles of 32 rows save conversions over 16 where there are so many (32 blocks of 16
+// tokens over 8 to 16 thousand keys 232 us against 314); for heads of 256 their sums do
+// not fit in registers, and 64 rows of heads of 64 are no faster (16 prompts of 256
+// tokens over 4096 keys 374 against 327).
 template <int D>
 constexpr int kRowGroups = D == 256 ? 1 : 2;
 template <int D>
@@ -35,6 +37,10 @@ hipError_t prepare_fp4() {
   return e;
 }
 
+// Where row tiles of 16 do not fill the CUs, one workgroup of all the waves that a CU
+// holds to each: 32 single tokens over 2 to 4 thousand keys 28.6 us against 33.6 with
+// workgroups of 4 waves, 8 blocks 24 against 29.  Beyond that 4 waves, two workgroups
+// to a CU: they leave the wait at the end to others.
 template <int D, bool FINE>
 void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
@@ -45,6 +51,17 @@ void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
   launch_few<D, kRowGroups<D>, 4, FINE>(a, 2 * cus, cus, st);
 }
 
+// The kernels of attention_split.h convert a tile once for all rows of a
+// workgroup (128 or 256), but start, wait at barriers and join slowly.  They win from
+// some work for each CU on, rows x keys:
+//   heads of 64    never: 16 prompts of 512 tokens over up to 16384 keys 612 us
+//                  here and 800 there, one over 1024 13 and 24
+//   128, to 128 rows   at 2^20: 16 of 128 rows over 8192 keys (half of that) 106 and
+//                  115, over 16384 201 and 207, 32 over 16384 (twice) 360 and 325
+//   128, beyond    at 2^18: 256 tokens over 4096 keys (half) 43 and 52, over
+//                  16384 (twice) 118 and 105
+//   256            at 2^16: 32 tokens of 4 requests over 4096 keys 50 and 57, over
+//                  8192 91 and 80
 template <int D>
 void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;

@@ -482,9 +482,8 @@ class DraftVerifier(_Handle):
 class TokenScores(_Handle):
     """Log-probabilities of given tokens, entropies and the likeliest ids of rows of logits.
 
-    ``logits`` is [rows, vocab] in the handle's dtype, rows at any stride ([requests, rows, vocab] logits are
-    flattened).  ``max_top`` bounds the ids of a row that can be asked for (up to 64; with 0 the handle
-    needs no memory for them).
+    ``logits`` is [rows, vocab] in the handle's dtype, rows at any stride.  ``max_top`` bounds the ids
+    of a row that can be asked for (up to 64; with 0 the handle needs no memory for them).
     """
 
     def __init__(self, vocab, dtype=torch.bfloat16, max_rows=1024, max_top=64):

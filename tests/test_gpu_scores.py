@@ -211,3 +211,19 @@ def test_graph_replays_match_eager_runs():
         for a, b in zip(got, op.run(x, tokens, top=8)):
             assert torch.equal(a, b)
         check(got, x, tokens, 8)
+
+
+def test_many_rows_of_a_very_large_vocabulary():
+    """Rows enough for a workgroup each, with more groups than its memory holds maxima of."""
+    import torch
+    from gru_corrected_draft_amd import verify
+    rows, vocab, top = 521, 270001, 9
+    log(f"[gpu-test] scores of {rows} rows of {vocab}")
+    x, g = _logits(rows, vocab, "bf16", 12)
+    x[3] = float("-inf")
+    x[4, 100:] = float("-inf")
+    x[520, :] = 1.0
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda").to(torch.int32)
+    got = verify.TokenScores(vocab, torch.bfloat16, max_rows=rows).run(x, tokens, top=top)
+    pick = torch.tensor([0, 1, 3, 4, 100, 255, 256, 300, 511, 512, 519, 520], device="cuda")
+    check([y[pick] for y in got], x[pick], tokens[pick], top)
