@@ -12,6 +12,11 @@
 // largest.  Then the row's last workgroup joins the parts, and since the n groups
 // with the largest maxima hold n logits as large as any other group's, it goes back
 // for the few groups that reach them.
+//
+// 1024 rows of 151936 bf16 logits with 5 ids each take 65 us, 4.8 TB/s (a large copy
+// reaches 5.2; vector instructions are busy 75 % of the time), 777 rows of 50257 23.5, of
+// which 8 are start and join of workgroups that live for three steps, one fp32 row of
+// 151936 with 20 ids 11.4, near what the call takes on the host.
 #include <cmath>
 #include <new>
 
@@ -462,6 +467,8 @@ extern "C" domino_status_t domino_scores_run(domino_scores_t* h, const void* log
   // likeliest ids four, and none from two rows to a CU on, where the maxima then
   // stay in LDS (1024 rows of 151936 undivided 65 us, in 2 parts 74; 256 rows in 4
   // parts and undivided 32).
+  // Ranges are whole steps: those of a quarter of one balance better but run
+  // steps half empty (777 rows of 50257 27.9).
   const int steps = steps_of(f.vocab);
   int parts = !top ? (8 * h->cus + rows - 1) / rows : rows >= 2 * h->cus ? 1 : (4 * h->cus + rows - 1) / rows;
   if (parts > steps) parts = steps;
