@@ -87,15 +87,39 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   return r;
 }
 
-// counts over a workgroup
-__device__ __forceinline__ int count_all(int n, int* s_count) {
+// A digit of a selection by a workgroup, a bin to each thread: in the order of the
+// bins (UP: from 0, otherwise from 255) the bin that holds the `need`-th element,
+// and the elements of earlier bins, in *found.  The bins hold at least `need`.
+struct Found {
+  int bin, before, here;
+};
+template <bool UP>
+__device__ __forceinline__ void find_bin(const int* s_bins, int* s_waves, int need, Found* found) {
+  const int tid = threadIdx.x, lane = tid & 63, bin = UP ? tid : kThreads - 1 - tid;
   __syncthreads();
-  if (threadIdx.x == 0) *s_count = 0;
+  const int mine = s_bins[bin];
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int x = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += x;
+  }
+  if (lane == 63) s_waves[tid >> 6] = upto;
   __syncthreads();
-  n = (int)wave_reduce((uint32_t)n, [](uint32_t a, uint32_t b) { return a + b; });
-  if ((threadIdx.x & 63) == 0) atomicAdd(s_count, n);
+  for (int i = 0; i < tid >> 6; ++i) upto += s_waves[i];
+  if (upto >= need && upto - mine < need) *found = Found{bin, upto - mine, mine};
   __syncthreads();
-  return *s_count;
+}
+
+// One to a bin by each active lane; equal logits meet in one, so the lanes that
+// share the first lane's bin are counted for it.
+__device__ __forceinline__ void count_in(int* s_bins, int bin) {
+  const int first = __builtin_amdgcn_readfirstlane(bin);
+  const uint64_t same = __ballot(bin == first);
+  if (bin != first)
+    atomicAdd(s_bins + bin, 1);
+  else if ((threadIdx.x & 63) == __builtin_ctzll(same))
+    atomicAdd(s_bins + bin, __builtin_popcountll(same));
 }
 
 // f(logit, id) for each logit of the row above -inf
@@ -241,10 +265,9 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
   if constexpr (TOP) {
     __shared__ __align__(16) float s_max[kThreads];
     __shared__ float s_bar[kThreads / 64];
-    __shared__ int s_groups[kList], s_count, s_keys_n, s_best_n;
+    __shared__ int s_groups[kList], s_count, s_keys_n, s_best_n, s_bins[kThreads], s_waves[kThreads / 64];
+    __shared__ Found s_found;
     uint64_t* const s_keys = s_row.keys;
-    // A bar that at least `top` logits reach, where so many threads have met a
-    // logit at all: the top-th largest of what the threads find largest.
     const float* const all = a.maxima + (int64_t)row * a.groups;
     auto maximum = [&](int g) { return __hip_atomic_load(all + g, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
     float kept[kKept], mine = -INFINITY;
@@ -256,29 +279,34 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
 #pragma unroll
     for (int i = 0; i < kKept; ++i) mine = fmaxf(mine, kept[i]);
     for (int g = kKept * kThreads + tid; g < a.groups; g += kThreads) mine = fmaxf(mine, maximum(g));
-    s_max[tid] = -INFINITY;
-    if (tid == 0) s_count = s_keys_n = s_best_n = 0;
-    __syncthreads();
-    // The bar: the top-th largest of what the threads find largest, which `top`
-    // logits reach, where so many threads have met one at all.  Ranked within
-    // each wave first: only its best can be among the best of all.
-    int above = 0;
+    if (tid == 0) s_count = s_keys_n = 0;
+    // A bar that at least `top` logits reach: the top-th largest of what the threads
+    // find largest, -inf where fewer have met one at all.  Ranked within each wave
+    // first: only its best can be among the best of all.
+    auto bar_of = [&](float mine) {
+      __syncthreads();
+      s_max[tid] = -INFINITY;
+      if (tid == 0) s_best_n = 0;
+      __syncthreads();
+      int above = 0;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), i)) > mine;
-    const bool best = above < a.top && mine > -INFINITY;
-    if (best) s_max[atomicAdd(&s_best_n, 1)] = mine;
-    __syncthreads();
-    const int best_n = s_best_n;
-    above = 0;
+      for (int i = 0; i < 64; ++i) above += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), i)) > mine;
+      const bool best = above < a.top && mine > -INFINITY;
+      if (best) s_max[atomicAdd(&s_best_n, 1)] = mine;
+      __syncthreads();
+      const int best_n = s_best_n;
+      above = 0;
 #pragma unroll 4
-    for (int i = 0; i < best_n; i += 4) {
-      const float4 x = *(const float4*)(s_max + i);
-      above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
-    }
-    const float least = -wave_max(best && above < a.top ? -mine : -INFINITY);
-    if ((tid & 63) == 0) s_bar[tid >> 6] = least;
-    __syncthreads();
-    const float bar = best_n < a.top ? -INFINITY : fminf(fminf(s_bar[0], s_bar[1]), fminf(s_bar[2], s_bar[3]));
+      for (int i = 0; i < best_n; i += 4) {
+        const float4 x = *(const float4*)(s_max + i);
+        above += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+      }
+      const float least = -wave_max(best && above < a.top ? -mine : -INFINITY);
+      if ((tid & 63) == 0) s_bar[tid >> 6] = least;
+      __syncthreads();
+      return best_n < a.top ? -INFINITY : fminf(fminf(s_bar[0], s_bar[1]), fminf(s_bar[2], s_bar[3]));
+    };
+    float bar = bar_of(mine);
     auto list = [&](float x, int g) {
       if (x >= bar && x > -INFINITY) {
         const int at = atomicAdd(&s_count, 1);
@@ -290,11 +318,28 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     for (int g = kKept * kThreads + tid; g < a.groups; g += kThreads) list(maximum(g), g);
     __syncthreads();
     const int groups = s_count;
+    // the first id of piece i of the listed groups, 8 logits each
+    auto piece_at = [&](int i) {
+      const int g = s_groups[i / (4 * kVectors)];
+      return g / kGroups * kChunk + i / 4 % kVectors * kSpan + g % kGroups * 32 + i % 4 * 8;
+    };
+    if (bar == -INFINITY && groups <= kList) {
+      // Fewer groups than ids asked for (a small vocabulary, a mask that leaves ids
+      // in few places): a bar from their pieces (100 rows of 1500 with 64 ids
+      // 19.4 us, without it 59.5).
+      mine = -INFINITY;
+      for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {
+        const int id = piece_at(i);
+        float x[8];
+        load_logits<T>(p + id, a.vocab - id, x);
+        mine = fmaxf(mine, tame(largest(x)));
+      }
+      bar = bar_of(mine);
+    }
     if (groups <= kList) {
 #pragma unroll 2
-      for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {  // 8 logits each
-        const int g = s_groups[i / (4 * kVectors)];
-        const int id = g / kGroups * kChunk + i / 4 % kVectors * kSpan + g % kGroups * 32 + i % 4 * 8;
+      for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {
+        const int id = piece_at(i);
         float x[8];
         load_logits<T>(p + id, a.vocab - id, x);
 #pragma unroll
@@ -309,40 +354,88 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     }
     __syncthreads();
     if (groups > kList || s_keys_n > kKeys) {
-      // Many equal logits, or few ids left in few groups.  The bar is found bit
-      // by bit, and among the logits equal to it the last id, each by a pass
-      // over the row.
-      uint32_t at_least = 0;
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t next = at_least | 1u << bit;
-        int n = 0;
-        each_logit(p, a.vocab, [&](float x, int) { n += orderable(x) >= next; });
-        if (count_all(n, &s_count) >= a.top) at_least = next;
+      // Many equal logits, or ids in fewer groups than asked for.  The value of
+      // the top-th logit is found digit by digit, and among its equals the last id
+      // in the same way, each digit by a pass over the row (a row of 151936 ids of
+      // four values 640 us, 300 such rows 1260; bit by bit 2270 and 4250).
+      uint32_t value = 0;  // of the last logit to take, and its number among its equals
+      int left = a.top, equals = 0;
+      bool all = false;
+      for (int shift = 24; shift >= 0 && !all; shift -= 8) {
+        __syncthreads();
+        s_bins[tid] = 0;
+        __syncthreads();
+        int met = 0;
+        each_logit<T>(p, a.vocab, [&](float x, int) {
+          const uint32_t y = orderable(x);
+          if (shift == 24 || y >> (shift + 8) == value >> (shift + 8)) {
+            count_in(s_bins, y >> shift & 255);
+            ++met;
+          }
+        });
+        if (shift == 24) {
+          met = (int)wave_reduce((uint32_t)met, [](uint32_t x, uint32_t y) { return x + y; });
+          if ((tid & 63) == 0) s_waves[tid >> 6] = met;
+          __syncthreads();
+          all = s_waves[0] + s_waves[1] + s_waves[2] + s_waves[3] <= left;
+          if (all) break;
+        }
+        find_bin<false>(s_bins, s_waves, left, &s_found);
+        const Found f = s_found;
+        value |= (uint32_t)f.bin << shift;
+        left -= f.before;
+        equals = f.here;
       }
-      int n = 0;
-      each_logit(p, a.vocab, [&](float x, int) { n += orderable(x) > at_least; });
-      const int left = a.top - count_all(n, &s_count);
-      int ids = 0;  // the most of the lowest ids that hold fewer than `left` equal ones
-      for (int step = 1 << 30; step; step >>= 1) {
-        const int next = ids + step;
-        if (next >= a.vocab || next < 0) continue;
-        n = 0;
-        each_logit(p, a.vocab, [&](float x, int id) { n += orderable(x) == at_least && id < next; });
-        if (count_all(n, &s_count) < left) ids = next;
+      int last = 0;  // id of the last of the equals
+      if (!all && equals > left) {
+        for (int shift = 16; shift >= 0; shift -= 8) {
+          if ((a.vocab - 1) >> shift == 0) continue;
+          __syncthreads();
+          s_bins[tid] = 0;
+          __syncthreads();
+          each_logit<T>(p, a.vocab, [&](float x, int id) {
+            if (orderable(x) == value && id >> (shift + 8) == last >> (shift + 8)) count_in(s_bins, id >> shift & 255);
+          });
+          find_bin<true>(s_bins, s_waves, left, &s_found);
+          const Found f = s_found;
+          last |= f.bin << shift;
+          left -= f.before;
+        }
+      } else {
+        last = a.vocab;
       }
       __syncthreads();
       if (tid == 0) s_keys_n = 0;
       __syncthreads();
-      each_logit(p, a.vocab, [&](float x, int id) {
-        if (orderable(x) > at_least || (orderable(x) == at_least && id <= ids)) {
+      each_logit<T>(p, a.vocab, [&](float x, int id) {
+        if (all || orderable(x) > value || (orderable(x) == value && id <= last)) {
           const int at = atomicAdd(&s_keys_n, 1);
           if (at < kKeys) s_keys[at] = pack_key(x, id);
         }
       });
       __syncthreads();
     }
+    int n = min(s_keys_n, kKeys);
+    if (n > kThreads) {
+      // Many for the ranking, which takes n^2: a bar from the threads' own largest
+      // leaves few (500 rows of 5003 with masks and 64 ids 19.9 us, without it 49.8).
+      uint64_t mine_keys[kKeys / kThreads];
+      mine = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kKeys / kThreads; ++i) {
+        mine_keys[i] = i * kThreads + tid < n ? s_keys[i * kThreads + tid] : 0;
+        if (mine_keys[i]) mine = fmaxf(mine, key_value(mine_keys[i]));
+      }
+      bar = bar_of(mine);
+      if (tid == 0) s_keys_n = 0;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kKeys / kThreads; ++i)
+        if (mine_keys[i] && key_value(mine_keys[i]) >= bar) s_keys[atomicAdd(&s_keys_n, 1)] = mine_keys[i];
+      __syncthreads();
+      n = s_keys_n;
+    }
     // each key to the place of its rank
-    const int n = min(s_keys_n, kKeys);
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t key = s_keys[i];
       int rank = 0;
