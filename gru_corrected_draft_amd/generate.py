@@ -187,15 +187,16 @@ class Generator:
     def score(self, tokens, top=0):
         """What the target makes of ``tokens`` ([requests, up to 16]) as each text's continuation, without the
         rules: their log-probabilities and the entropy at each of them, both [requests, n], and the ``top``
-        likeliest ids in their places with log-probabilities, [requests, n, top] (None, None for 0).  The
-        texts stay."""
+        likeliest ids in their places with log-probabilities, [requests, n, top] (None, None for 0).  A token
+        outside the vocabulary (padding) gets -inf, and what follows it is read after the nearest id inside.
+        The texts stay."""
         b, n = tokens.shape
         if not 1 <= n <= BLOCK:
             raise ValueError(f"1 to {BLOCK} tokens can be scored at once")
         self._room(n - 1, "the texts have no room for these tokens")
         if self._scores is None:
             self._scores = TokenScores(self.target.vocab, self.target.dtype, max_rows=b * BLOCK)
-        tokens = tokens.to(torch.int32)
+        tokens = tokens.clamp(-1, self.target.vocab).to(torch.int32)  # before 64 bits become 32
         x = self.logits(torch.cat([self.last(), tokens[:, :-1]], 1))
         logprob, entropy, ids, values = self._scores.run(x.flatten(0, 1), tokens.flatten(), top)
         if top:

@@ -138,7 +138,9 @@ domino_status_t domino_attention_create(const domino_attention_config_t* cfg,
 /* Writes keys and values of the new tokens into the cache: token row i, head h
  * of k lies at k + i * k_token_stride + h * k_head_stride (elements, multiples
  * of 16 bytes), v alike.  Tokens of a malformed request, at a negative
- * position, or whose page id is outside [0, num_pages) are not written. */
+ * position, or whose page id is outside [0, num_pages) are not written.  Where
+ * two tokens of a call meet in one row (a page id stands twice), pieces of either
+ * remain. */
 domino_status_t domino_attention_append(domino_attention_t* h, const domino_cache_t* cache,
                                         const void* k, int64_t k_token_stride,
                                         int64_t k_head_stride, const void* v,

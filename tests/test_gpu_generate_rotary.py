@@ -145,6 +145,21 @@ def test_score_of_continuations(dtype, bits):
         gen.score(tokens)
 
 
+def test_scores_of_padded_continuations():
+    """Ids outside the vocabulary have no probability; those before them are what they would be."""
+    import torch
+    log("[gpu-test] scores of padded continuations")
+    gen = _generator("bf16", 4)
+    b = len(LENGTHS)
+    tokens = torch.randint(0, VOCAB, (b, 5), device="cuda")
+    want = gen.score(tokens)[0]
+    padded = tokens.clone()
+    padded[:, 3] = torch.tensor([-1, VOCAB, -2 ** 40, 2 ** 32], device="cuda")[torch.arange(b, device="cuda") % 4]
+    got, entropy = gen.score(padded)[:2]
+    assert torch.equal(got[:, :3], want[:, :3])
+    assert torch.isneginf(got[:, 3]).all() and torch.isfinite(got[:, 4]).all() and torch.isfinite(entropy).all()
+
+
 def test_the_cache_of_the_target():
     """Another cache, another answer; which targets can have one of 4 bits."""
     import torch
