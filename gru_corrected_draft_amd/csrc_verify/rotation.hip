@@ -38,19 +38,24 @@ struct RotateArgs {
   float eps, magnitude;
 };
 
-__device__ __forceinline__ void load8(const bf16_t* p, float (&x)[8]) {
-  const u32x4 v = *(const u32x4*)p;
+// eight elements as they lie in memory
+template <typename T>
+struct Raw {
+  u32x4 x[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(v[i] << 16);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) x[i] = *((const u32x4*)p + i);
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+  __device__ __forceinline__ void unpack(float (&y)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4)
+        y[i] = __uint_as_float(x[i / 4][i % 4]);
+      else
+        y[i] = __uint_as_float(i % 2 ? x[0][i / 2] & 0xFFFF0000u : x[0][i / 2] << 16);
+    }
+  }
+};
 __device__ __forceinline__ void store8(bf16_t* p, const float (&x)[8]) {
   typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
   v8bf v;
@@ -68,16 +73,9 @@ template <typename T, int D, bool PAIRS_NEXT>
 __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int tokens_each) {
   constexpr int LANES = D / 16;  // of a head
   __shared__ float2 s_turn[4][kMaxPairs];
+  __shared__ int s_written[4];
   const int half = a.rotary / 2, t0 = blockIdx.x * tokens_each, tid = threadIdx.x;
   const int here = min(tokens_each, a.tokens - t0);
-  for (int i = tid; i < here * half; i += 256) {
-    const int t = i / half, f = i - t * half;
-    const double turns = (double)a.positions[t0 + t] * a.turns[f];
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    s_turn[t][f] = make_float2(c * a.magnitude, s * a.magnitude);
-  }
-  __syncthreads();
   const int lane = tid % LANES, rot_lanes = a.rotary / 16;
   // first elements of the lane's two groups
   int e0, e1;
@@ -89,14 +87,41 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int tokens_ea
     e0 = 8 * lane;
     e1 = e0 + half;
   }
-  for (int item = tid / LANES; item < here * a.heads; item += 256 / LANES) {
-    const int t = item / a.heads, head = item - t * a.heads, which = head >= a.q_heads;
-    const int h = which ? head - a.q_heads : head;
-    if (a.positions[t0 + t] < 0) continue;
-    const T* x = (const T*)a.x[which] + (t0 + t) * a.x_tok[which] + h * a.x_head[which];
+  // A head ahead of its use, the first on its way while the angles are formed.
+  constexpr int STEP = 256 / LANES;
+  const int step_t = STEP / a.heads, step_h = STEP % a.heads;
+  int next_t = tid / LANES / a.heads, next_h = tid / LANES % a.heads;
+  Raw<T> next_u, next_v;
+  auto load = [&]() {
+    if (next_t >= here) return;
+    const int which = next_h >= a.q_heads, h = which ? next_h - a.q_heads : next_h;
+    const T* x = (const T*)a.x[which] + (t0 + next_t) * a.x_tok[which] + h * a.x_head[which];
+    next_u.load(x + e0);
+    next_v.load(x + e1);
+  };
+  load();
+  for (int i = tid; i < here * half; i += 256) {
+    const int t = i / half, f = i - t * half;
+    const double turns = (double)a.positions[t0 + t] * a.turns[f];
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    s_turn[t][f] = make_float2(c * a.magnitude, s * a.magnitude);
+  }
+  if (tid < here) s_written[tid] = a.positions[t0 + tid] >= 0;
+  __syncthreads();
+  while (next_t < here) {
+    const int t = next_t, which = next_h >= a.q_heads, h = which ? next_h - a.q_heads : next_h;
     float u[8], v[8];
-    load8(x + e0, u);
-    load8(x + e1, v);
+    next_u.unpack(u);
+    next_v.unpack(v);
+    next_t += step_t;
+    next_h += step_h;
+    if (next_h >= a.heads) {
+      next_h -= a.heads;
+      ++next_t;
+    }
+    load();
+    if (!s_written[t]) continue;
     if (a.w[0]) {
       float sum = 0.f;
 #pragma unroll
@@ -105,11 +130,14 @@ __global__ __launch_bounds__(256) void rotate_kernel(RotateArgs a, int tokens_ea
       for (int m = 1; m < LANES; m <<= 1) sum += __shfl_xor(sum, m, 64);
       const float r = 1.f / sqrtf(sum * (1.f / D) + a.eps);
       float w[8];
+      Raw<T> raw;
       const T* weight = (const T*)a.w[which];
-      load8(weight + e0, w);
+      raw.load(weight + e0);
+      raw.unpack(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = u[i] * r * w[i];
-      load8(weight + e1, w);
+      raw.load(weight + e1);
+      raw.unpack(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
     }
