@@ -13,9 +13,10 @@
 // is a 64-bit product of which the whole turns are taken off before it is
 // rounded to 32 bits, so far positions lose nothing.
 //
-// Bound by memory: 8192 tokens of 40 heads of 128 take 32 us on the GPU and 41.7 from
-// call to call, 4.8 TB/s (a large copy reaches 5.2); 64 blocks of 16 tokens 7.0 and
-// 9.9, one token 3.8 and 9.5, the call itself.
+// Bound by memory: 8191 tokens of 48 heads of 128 take 35 us from call to call, 5.8
+// TB/s (a large copy reaches 5.2); a head's elements are loaded one ahead, the
+// first before the angles are formed (41.5 without).  64 blocks of 16 tokens take 7 us
+// on the GPU and one token 4, less than the call on the host, 9.5.
 #include <cmath>
 #include <new>
 
@@ -244,12 +245,13 @@ extern "C" const char* domino_rotation_last_error(const domino_rotation_t* h) { 
 
 template <typename T, int D>
 static void launch_rotate(const domino_rotation* h, const RotateArgs& a, hipStream_t st) {
-  // Four tokens to a workgroup save starts where a token is little for 256 lanes and
-  // there are workgroups enough even so: 10 heads of 128 of 16000 tokens 22.4 us against
-  // 29.9, 40 heads of 64 of 8191 21.4 and 23.7, 48 of 128 of 8191 41.7 and 44.2, but
-  // 40 of 128 of 4096 23.7 and 22.3; 72 of 128 of 8191 61.8 and 62.5, of 4096 41 and 34.
+  // Several tokens to a workgroup save starts where a token is little for 256 lanes
+  // and there are workgroups enough even so, one, two or four: 40 heads of 128 of
+  // 2048 tokens 10.9, 11.3 and 12.4 us, of 4096 20.0, 18.1 and 18.4, of 8191 34.0, 30.5
+  // and 29.4; 10 heads of 128 of 16000 26.1, 20.6 and 19.7; but 72 of 128 of 16000
+  // 109, 113 and 120.
   const int size = a.heads * D;  // of a token
-  const int tokens_each = size <= 8192 && a.tokens >= (size <= 2560 ? 2048 : 6144) ? 4 : 1;
+  const int tokens_each = size > 8192 || a.tokens < 2560 ? 1 : a.tokens < 6000 ? 2 : 4;
   const dim3 grid((unsigned)((a.tokens + tokens_each - 1) / tokens_each));
   if (h->cfg.interleaved)
     hipLaunchKernelGGL((rotate_kernel<T, D, true>), grid, dim3(256), 0, st, a, tokens_each);
