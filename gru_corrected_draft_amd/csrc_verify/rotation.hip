@@ -13,9 +13,10 @@
 // is a 64-bit product of which the whole turns are taken off before it is
 // rounded to 32 bits, so far positions lose nothing.
 //
-// Bound by memory: 8191 tokens of 48 heads of 128 take 35 us from call to call, 5.8
-// TB/s (a large copy reaches 5.2); a head's elements are loaded one ahead, the
-// first before the angles are formed (41.5 without).  64 blocks of 16 tokens take 7 us
+// Bound by memory: 8191 tokens of 48 heads of 128 take 43 us from call to call, 4.7
+// TB/s (a large copy reaches 4.8 to 5.2), and 35 where the results fall into the same
+// memory each time; a head's elements are loaded one ahead, the first before the
+// angles are formed (46.5 and 41.5 without).  64 blocks of 16 tokens take 7 us
 // on the GPU and one token 4, less than the call on the host, 9.5.
 #include <cmath>
 #include <new>

@@ -1,22 +1,26 @@
 // Log-probabilities of given tokens, the entropy of each row of logits and its
 // likeliest ids.
 //
-// With m the row's largest logit, l = sum e^(x - m) and t = sum e^(x - m) (x - m):
+// With m the row's largest logit, n the logits equal to it, s = sum of e^(x - m) over
+// the others, l = n + s and t = sum e^(x - m) (x - m):
 //   log-probability of x = (x - m) - ln l;   entropy = ln l - t / l.
 // Both terms of the entropy are of one sign, so nothing cancels, and a row with
-// one candidate yields exactly 0 for both.
+// one candidate yields exactly 0 for both.  n is counted apart, since beside 1 a small s
+// would lose its digits, and with them the log-probability of a near certain token,
+// ln(1 + s): ln l = ln n + log1p(s / n).
 //
 // A workgroup takes a row, or a part of one where there are few: it reads the
-// logits once, each wave keeps m, l and t (rescaled when its maximum grows, about
+// logits once, each wave keeps m, n, s and t (rescaled when its maximum grows, about
 // ln(vectors) times a row), and for the likeliest ids every 128 logits leave their
 // largest.  Then the row's last workgroup joins the parts, and since the n groups
 // with the largest maxima hold n logits as large as any other group's, it goes back
 // for the few groups that reach them.
 //
 // 1024 rows of 151936 bf16 logits with 5 ids each take 65 us, 4.8 TB/s (a large copy
-// reaches 5.2; vector instructions are busy 75 % of the time), 777 rows of 50257 23.5, of
+// reaches 5.2; vector instructions are busy 75 % of the time), 777 rows of 50257 24.2, of
 // which 8 are start and join of workgroups that live for three steps, one fp32 row of
-// 151936 with 20 ids 11.4, near what the call takes on the host.
+// 151936 with 20 ids 11.7, near what the call takes on the host.  Counting n apart takes
+// 0.3 to 1.3 us of each.
 #include <cmath>
 #include <new>
 
@@ -43,7 +47,7 @@ struct ScoreArgs {
   int64_t row_stride;
   int32_t rows, vocab, range, parts, top;
   const int32_t* tokens;
-  float* part;       // [rows][parts][4]: m, l, t in powers of two
+  float* part;       // [rows][parts][4]: m, s, t in powers of two, n
   float* maxima;     // [rows][groups]
   int32_t* arrived;  // [rows] parts there are, 0 between calls
   int32_t groups;
@@ -69,22 +73,25 @@ __device__ __forceinline__ float load_tame(const T* p) {
 }
 
 struct Sums {
-  float m, l, t;
+  float m, s, t, n;
 };
-// to the reference of the larger maximum
+// to the reference of the larger maximum m
+__device__ __forceinline__ Sums refer(const Sums& a, float m) {
+  if (a.m == m || a.m == -INFINITY) return a;
+  const float d = fmaxf((a.m - m) * kLog2e, -200.f), f = exp2_fast(d), all = a.s + a.n;
+  return Sums{m, f * all, f * (a.t + d * all), 0.f};
+}
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return a;
-  Sums r{m, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const Sums& s = i ? b : a;
-    if (s.m == -INFINITY) continue;
-    const float d = fmaxf((s.m - m) * kLog2e, -200.f), f = exp2_fast(d);
-    r.l += f * s.l;
-    r.t += f * (s.t + d * s.l);
-  }
-  return r;
+  const Sums x = refer(a, m), y = refer(b, m);
+  return Sums{m, x.s + y.s, x.t + y.t, x.n + y.n};
+}
+
+// ln(n + s): with r = s / n and u = 1 + r rounded, ln(1 + r) = ln u + (r - (u - 1)) / u
+__device__ __forceinline__ float log_sum(float n, float s) {
+  const float r = n == 1.f ? s : s / n, u = 1.f + r;
+  const float x = logf(u) + (r - (u - 1.f)) * __builtin_amdgcn_rcpf(u);
+  return n == 1.f ? x : logf(n) + x;
 }
 
 // A digit of a selection by a workgroup, a bin to each thread: in the order of the
@@ -151,7 +158,8 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
   const int row = blockIdx.y, part = blockIdx.x, tid = threadIdx.x;
   const int lo = part * a.range, hi = min(lo + a.range, a.vocab);
   const T* const p = (const T*)a.logits + row * a.row_stride;
-  float m = -INFINITY, l = 0.f, t = 0.f;  // m is the wave's
+  float m = -INFINITY, s = 0.f, t = 0.f;  // m is the wave's
+  int n = 0;
   float* const maxima = TOP ? a.maxima + (int64_t)row * a.groups + tid / 4 : nullptr;
   u32x4 raw[kVectors][8 / Elem<T>::kVec], next[kVectors][8 / Elem<T>::kVec];
   auto load = [&](int at) {
@@ -183,24 +191,35 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __builtin_canonicalizef(x[j]);
       float top = largest(x);
-      if (__any(top > m)) {
+      if (__any(top >= m)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = tame(x[j]);
         top = tame(top);
         const float mn = fmaxf(m, wave_max(top));
-        if (m != -INFINITY) {
-          const float d = fmaxf((m - mn) * kLog2e, -200.f), f = exp2_fast(d);
-          t = f * (t + d * l);
-          l *= f;
+        if (mn > m) {
+          if (m > -INFINITY) {
+            const float d = fmaxf((m - mn) * kLog2e, -200.f), f = exp2_fast(d), all = s + (float)n;
+            t = f * (t + d * all);
+            s = f * all;
+            n = 0;
+          }
+          m = mn;
         }
-        m = mn;
+        if (m > -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool equal = x[j] == m;
+            n += equal;
+            x[j] = equal ? -INFINITY : x[j];
+          }
+        }
       }
       if (TOP) group = max3(group, top, top);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // -inf and NaN end at 2^-200, which is 0
         const float y = fmaxf((x[j] - m) * kLog2e, -200.f), e = exp2_fast(y);
-        l += e;
+        s += e;
         t = __builtin_fmaf(e, y, t);
       }
     }
@@ -216,9 +235,8 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
       }
     }
   }
-  l = wave_sum(l);
-  t = wave_sum(t);
-  if ((tid & 63) == 0) s_sums[tid >> 6] = Sums{m, l, t};
+  const Sums own{m, wave_sum(s), wave_sum(t), wave_sum((float)n)};
+  if ((tid & 63) == 0) s_sums[tid >> 6] = own;
   __syncthreads();
   if (tid < 64) {
     Sums s = s_sums[0];
@@ -227,24 +245,22 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     if (tid == 0) s_sums[0] = s;
     if (a.parts > 1 && tid == 0) {
       float* const out = a.part + ((int64_t)row * a.parts + part) * 4;
-      share2(out, s.m, s.l);
-      share2(out + 2, s.t, 0.f);
+      share2(out, s.m, s.s);
+      share2(out + 2, s.t, s.n);
     }
   }
   if (a.parts > 1) {
     if (!last_of(a.arrived + row, a.parts, &s_last)) return;
     if (tid < 64) {  // the parts, a lane to each
-      Sums s{-INFINITY, 0.f, 0.f};
+      Sums s{-INFINITY, 0.f, 0.f, 0.f};
       for (int i = tid; i < a.parts; i += 64) {
         const float* const in = a.part + ((int64_t)row * a.parts + i) * 4;
         const float2 x = shared2(in), y = shared2(in + 2);
-        s = join(s, Sums{x.x, x.y, y.x});
+        s = join(s, Sums{x.x, x.y, y.x, y.y});
       }
       const float top = wave_max(s.m);
-      const float d = s.m == -INFINITY ? -200.f : fmaxf((s.m - top) * kLog2e, -200.f), f = exp2_fast(d);
-      s.t = wave_sum(f * (s.t + d * s.l));
-      s.l = wave_sum(f * s.l);
-      s.m = top;
+      s = refer(s, top);
+      s = Sums{top, wave_sum(s.s), wave_sum(s.t), wave_sum(s.n)};
       if (tid == 0) s_sums[0] = s;
     }
   } else {
@@ -252,10 +268,10 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
   }
   __syncthreads();
   const Sums sums = s_sums[0];
-  const float norm = logf(sums.l);
   m = sums.m;
+  const float norm = log_sum(sums.n, sums.s);
   if (tid == 0) {
-    if (a.entropy) a.entropy[row] = m == -INFINITY ? 0.f : norm - kLn2 * sums.t / sums.l;
+    if (a.entropy) a.entropy[row] = m == -INFINITY ? 0.f : norm - kLn2 * sums.t / (sums.n + sums.s);
     if (a.logprob) {
       const int token = a.tokens[row];
       const float x = token >= 0 && token < a.vocab ? load_tame(p + token) : -INFINITY;

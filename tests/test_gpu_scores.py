@@ -227,3 +227,34 @@ def test_many_rows_of_a_very_large_vocabulary():
     got = verify.TokenScores(vocab, torch.bfloat16, max_rows=rows).run(x, tokens, top=top)
     pick = torch.tensor([0, 1, 3, 4, 100, 255, 256, 300, 511, 512, 519, 520], device="cuda")
     check([y[pick] for y in got], x[pick], tokens[pick], top)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(1, 151936, "fp32"), (24, 50257, "bf16"), (600, 5003, "fp32"), (3, 7, "bf16")])
+def test_near_certain_tokens_keep_their_digits(rows, vocab, dtype):
+    """With one id or two far ahead, ln(n + s) = ln n + ln(1 + s / n): the log-probability of such an id and
+    the entropy are as exact, relative to themselves, as s, whose terms are off by 2 U (Y + 1) of themselves, Y
+    the largest |y| that adds to it, and whose additions by U (n + 40) of it (the entropy's second sum by one U Y and
+    three roundings more); logarithm, quotient and sum take 8 U."""
+    import torch
+    from gru_corrected_draft_amd import verify
+    log(f"[gpu-test] scores of near certain tokens {rows} {vocab} {dtype}")
+    x, g = _logits(rows, vocab, dtype, 21, 1.0)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda").to(torch.int32)
+    ahead = torch.linspace(13, 24, rows, device="cuda").to(x.dtype)
+    x[torch.arange(rows, device="cuda"), tokens.long()] = ahead
+    tied = torch.arange(rows, device="cuda") % 3 == 2
+    x[tied, (tokens.long()[tied] + 1) % vocab] = ahead[tied]
+    logprob, entropy, ids, values = verify.TokenScores(vocab, _types()[dtype], max_rows=rows).run(x, tokens, top=1)
+    torch.cuda.synchronize()
+    z = x.double().cpu().numpy()
+    z -= z.max(1, keepdims=True)
+    e = np.exp(z)
+    n = (z == 0).sum(1)
+    s = np.where(z == 0, 0, e).sum(1)
+    want = -(np.log(n) + np.log1p(s / n))
+    h = -want - (e * z).sum(1) / (n + s)
+    tol = U * (2 * (-z.min(1) * LOG2E + 1) + 8 * -(-vocab // 2048) + 40 + 8)
+    assert np.all(np.abs(logprob.double().cpu().numpy() - want) <= tol * -want)
+    assert np.all(np.abs(values[:, 0].double().cpu().numpy() - want) <= tol * -want)
+    assert np.all(np.abs(entropy.double().cpu().numpy() - h) <= (tol + U * (-z.min(1) * LOG2E + 3)) * h)
+    assert -want.max() < 0.5
