@@ -73,9 +73,10 @@ domino_status_t domino_rotation_create(const domino_rotation_config_t* cfg, cons
  *   a' = magnitude * (a cos(p f_j) - b sin(p f_j))
  *   b' = magnitude * (b cos(p f_j) + a sin(p f_j))   for the pairs (a, b) of y, j < R / 2
  * and elements from R on are y.  The weights of q and k are given together or
- * not at all.  All of it is fp32 and rounded once; the angle is formed in 64
- * bits, so that any position is as good as the first.  Tokens with a negative
- * position are not written.  eps >= 0 and finite. */
+ * not at all.  All of it is fp32 and rounded once; the whole turns of an angle
+ * are taken off before it is rounded to fp32, so that any position is as good as
+ * the first at every frequency.  Tokens with a negative position are not written.
+ * eps >= 0 and finite. */
 domino_status_t domino_rotation_run(domino_rotation_t* h, const domino_heads_t* q, const domino_heads_t* k,
                                     const int32_t* positions, int32_t tokens, float eps, void* stream);
 
