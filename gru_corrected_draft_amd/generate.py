@@ -127,6 +127,7 @@ class Generator:
             self.attention = PagedAttention(q_heads, kv_heads, dim, page_size, target.dtype, max_requests=b)
             page, dtype = (page_size, dim), target.dtype
         self._scores = None
+        self.hidden = None  # of the last pass, [requests, tokens, hidden]
         self.verifier = DraftVerifier(target.vocab, target.dtype, max_requests=b, max_rows=BLOCK)
         self.caches = [tuple(torch.zeros(b * pages, kv_heads, *page, dtype=dtype, device=dev) for _ in range(2))
                        for _ in target.layers]
@@ -189,7 +190,8 @@ class Generator:
         rules: their log-probabilities and the entropy at each of them, both [requests, n], and the ``top``
         likeliest ids in their places with log-probabilities, [requests, n, top] (None, None for 0).  A token
         outside the vocabulary (padding) gets -inf, and what follows it is read after the nearest id inside.
-        The texts stay."""
+        The texts stay, and so does ``hidden``, from which the next proposals are made; before any other pass
+        it is the state at each text's last token, [requests, 1, hidden]."""
         b, n = tokens.shape
         if not 1 <= n <= BLOCK:
             raise ValueError(f"1 to {BLOCK} tokens can be scored at once")
@@ -197,7 +199,9 @@ class Generator:
         if self._scores is None:
             self._scores = TokenScores(self.target.vocab, self.target.dtype, max_rows=b * BLOCK)
         tokens = tokens.clamp(-1, self.target.vocab).to(torch.int32)  # before 64 bits become 32
+        hidden = self.hidden
         x = self.logits(torch.cat([self.last(), tokens[:, :-1]], 1))
+        self.hidden = self.hidden[:, :1] if hidden is None else hidden
         logprob, entropy, ids, values = self._scores.run(x.flatten(0, 1), tokens.flatten(), top)
         if top:
             ids, values = ids.view(b, n, top), values.view(b, n, top)
