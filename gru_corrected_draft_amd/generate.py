@@ -40,7 +40,7 @@ class Target:
     """A small decoder with random weights: embedding and position, layers of attention and a gated
     product, a head over the vocabulary.  Every second layer sees a window and four sinks.  With ``rotary``,
     the base of the frequencies (1e6 for instance), heads are normalised and rotated, and positions add
-    nothing to the embedding."""
+    nothing to the embedding: there is no table of them, and ``positions`` bounds no text."""
 
     def __init__(self, vocab, hidden, q_heads, kv_heads, head_dim, layers, positions, window=0,
                  dtype=torch.bfloat16, device="cuda", seed=0, rotary=None):
@@ -52,7 +52,9 @@ class Target:
         self.vocab, self.hidden, self.dtype, self.device = vocab, hidden, dtype, device
         self.heads, self.window = (q_heads, kv_heads, head_dim), window
         self.embed = torch.randn(vocab, hidden, generator=g).to(device, dtype)
-        self.position = torch.randn(positions, hidden, generator=g).to(device, dtype)
+        # drawn with ``rotary`` as well, so that a seed's weights are the same either way
+        position = torch.randn(positions, hidden, generator=g)
+        self.position = position.to(device, dtype) if rotary is None else None
         self.head = weight(vocab, hidden, 4.0)
         self.layers = [{"qkv": weight((q_heads + 2 * kv_heads) * head_dim, hidden),
                         "out": weight(hidden, q_heads * head_dim),
@@ -113,7 +115,7 @@ class Generator:
                 raise ValueError(f"a prompt's ids must be in [0, {target.vocab})")
         # a block may write up to 15 refused positions past the text
         self.max_kv = max(lens) + max_new + BLOCK
-        if self.max_kv > len(target.position):
+        if target.position is not None and self.max_kv > len(target.position):
             raise ValueError("the target has no positions for texts of this length")
         pages = -(-self.max_kv // page_size)
         if cache_bits not in (None, 4):
