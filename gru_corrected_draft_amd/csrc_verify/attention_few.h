@@ -509,13 +509,21 @@ inline int64_t few_keys(const AttendArgs& a) {
   return a.window && seen < a.max_kv ? seen : a.max_kv;
 }
 
-// Tiles of the longest request beyond which it is worth cutting: the second launch
-// and the parts cost what several steps do.  One token over 1024 keys takes 11.0 us
-// whole and 13.5 in parts, over 3000 18.6 and 13.5; 8 tokens of 32 requests of 32 heads
-// of 128 over 1024 18.0 and 24.3, over 2048 29.6 and 32.2, 20 requests 27.9 and 25.3; of
-// heads of 256 one token over 600 11.9 and 13.5, over 1024 16.6 and 13.5.
+// Cutting takes a second launch and the parts, on the host (one token over 1800 keys 13.1 us a
+// call whole and 14.2 in runs) and on the GPU, so requests have more tiles than kWorth and
+// lose more than kLess of them: a request can have units / segments runs, which leave it
+// about the share segments / units.  With 8 key heads, whole and cut, us on the GPU:
+//   heads of 128  one token of 1 request over 1024 keys 11 and 13, 2048 15 and 13; of 12 (3/8
+//                 left) over 2048 16 and 17, 4096 24 and 22; 8 tokens of 20 requests over 2048
+//                 28 and 26, of 32 (half left) over 2048 28 and 31, 2560 34 and 34, 4096 49 and 46
+//   64            one token of 1 over 1536 10 and 11, 2048 12 and 12, of 16 (half left) over
+//                 2560 14 and 15, 4096 18 and 19, 6144 24 and 22
+//   256           one token of 4 over 1024 19 and 15; 8 tokens of 16 (half left) over 1024 20
+//                 and 20, 1536 26 and 23
 template <int D>
 constexpr int kWorth = D == 256 ? 32 : 64;
+template <int D>
+constexpr int kLess = D == 256 ? 22 : D == 128 ? 44 : 60;
 
 // `units`: workgroups that the chip holds at once, divided among the row tiles
 template <int D, int G, int S, bool FINE>
@@ -531,7 +539,8 @@ void launch_few(const AttendArgs& a, int units, int cus, hipStream_t st) {
   units /= row_tiles;
   const int64_t room = few_rows(D, cus) / (C::kRows * row_tiles);
   if (units > room) units = (int)room;
-  if (2 * segments <= units && tiles > kWorth<D> && a.requests * tiles < (int64_t)1 << 30) {
+  if (2 * segments <= units && tiles > kWorth<D> && tiles * (units - segments) > (int64_t)kLess<D> * units &&
+      a.requests * tiles < (int64_t)1 << 30) {
     f.units = units;
     if (a.requests > 64) {
       f.most = (int)(units / segments);
