@@ -5,7 +5,7 @@
 // the tiles of 32 keys that they see; each of its S waves works alone on every S-th
 // of them, reads K and V straight into registers, a tile ahead of their use, and
 // keeps its own maximum, sum and output.  A wave waits for no other before the end:
-// with barriers and V shared by row tiles 8 blocks took 63 us for 45 without.
+// with barriers and V shared by row tiles 8 blocks took 1.4 times as long.
 // Products are 16 x 16 x 32, with both results transposed: S^T = K Q^T (keys x
 // rows) and O^T = V^T P^T.  Lane l (n = l % 16, q = l / 16) holds row n, of S the keys
 // 4 q .. 4 q + 3 of both halves of the tile, which are its slots of the second
@@ -16,8 +16,10 @@
 //      read, swizzled as in KeyTile.
 // FINE keeps each weight as the sum of two bf16 numbers (15 bits), otherwise they
 // are rounded once, as over a bf16 cache by the same rule of rows: beyond 32 rows the
-// second product is no longer hidden (32 blocks over 8 to 16 thousand keys 232 us
-// against 200, 8 blocks over 2 to 4 thousand 24.6 against 22.8).
+// second product is no longer hidden (32 blocks over 8 to 16 thousand keys 234 us
+// against 201, 8 blocks over 2 to 4 thousand 23.0 against 21.3, 16 prompts of 512 tokens of
+// 32 heads of 64 over 8 to 16 thousand 1505 against 1223; 0.0017 of the result in the root
+// mean square, most of it the result's own rounding, against 0.0023).
 //
 // Units.  A unit is a (request, key head, run of its tiles).  Where the requests
 // fill the chip by themselves or are short a run is all of a request's tiles,
@@ -25,9 +27,9 @@
 // second launch joins them.  Every workgroup finds the division by itself, a lane
 // to each request.
 //
-// What bounds it.  64 single tokens over 4 to 8 thousand keys take 90 us, 4.8 TB/s
+// What bounds it.  64 single tokens over 4 to 8 thousand keys take 88 us, 4.9 TB/s
 // of the cache's bytes (a large copy reaches 5.2, reads alone more).  8 blocks of 16
-// tokens over 2 to 4 thousand keys take 23 us for 5 us of bytes: start, queries and
+// tokens over 2 to 4 thousand keys take 21 us for 5 us of bytes: start, queries and
 // the joining of streams take about 8, then a wave takes 2 us to a tile, of which
 // vector instructions (conversions a third of them) fill 60 % and products 20 %.
 // 32-row tiles share each conversion between two products; the scaled products

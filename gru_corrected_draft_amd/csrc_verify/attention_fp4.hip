@@ -6,9 +6,9 @@
 namespace {
 
 // Row tiles of 32 rows save conversions over 16 where there are so many (32 blocks of 16
-// tokens over 8 to 16 thousand keys 232 us against 314); for heads of 256 their sums do
+// tokens over 8 to 16 thousand keys 201 us against 285); for heads of 256 their sums do
 // not fit in registers, and 64 rows of heads of 64 are no faster (16 prompts of 256
-// tokens over 4096 keys 374 against 327).
+// tokens over 4096 keys 200 against 174).
 template <int D>
 constexpr int kRowGroups = D == 256 ? 1 : 2;
 template <int D>
@@ -38,8 +38,8 @@ hipError_t prepare_fp4() {
 }
 
 // Where row tiles of 16 do not fill the CUs, one workgroup of all the waves that a CU
-// holds to each: 32 single tokens over 2 to 4 thousand keys 28.6 us against 33.6 with
-// workgroups of 4 waves, 8 blocks 24 against 29.  Beyond that 4 waves, two workgroups
+// holds to each: 32 single tokens over 2 to 4 thousand keys 27.3 us against 33.8 with
+// workgroups of 4 waves, 8 blocks 21.3 against 29.9.  Beyond that 4 waves, two workgroups
 // to a CU: they leave the wait at the end to others.
 template <int D, bool FINE>
 void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
@@ -54,13 +54,13 @@ void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
 // The kernels of attention_split.h convert a tile once for all rows of a
 // workgroup (128 or 256), but start, wait at barriers and join slowly.  They win from
 // some work for each CU on, rows x keys:
-//   heads of 64    never: 16 prompts of 512 tokens over up to 16384 keys 612 us
-//                  here and 800 there, one over 1024 13 and 24
-//   128, to 128 rows   at 2^20: 16 of 128 rows over 8192 keys (half of that) 106 and
-//                  115, over 16384 201 and 207, 32 over 16384 (twice) 360 and 325
-//   128, beyond    at 2^18: 256 tokens over 4096 keys (half) 43 and 52, over
-//                  16384 (twice) 118 and 105
-//   256            at 2^16: 32 tokens of 4 requests over 4096 keys 50 and 57, over
+//   heads of 64    never: 16 prompts of 512 tokens of 16 heads over up to 16384 keys
+//                  took 612 us here (589 since) and 800 there, one over 1024 13 and 24
+//   128, to 128 rows   at 2^20: 16 of 128 rows over 8192 keys (half of that) 105 and
+//                  114, over 16384 201 and 206, 32 over 16384 (twice) 360 and 324
+//   128, beyond    at 2^18: 256 tokens over 4096 keys (half) 40 and 47, over
+//                  16384 (twice) 111 and 95
+//   256            at 2^16: 32 tokens of 4 requests over 4096 keys 50 and 56, over
 //                  8192 91 and 80
 template <int D>
 void launch_fp4(const AttendArgs& a, int cus, hipStream_t st) {
@@ -99,9 +99,10 @@ namespace {
 
 // Append and read: 8 elements to a lane, four lanes to a block of 32, grid.y is
 // 2 x requests, keys and values.  Both are bound by the chain from the lengths over
-// the page table to memory (prompts of 8 requests up to 1024 tokens, one piece to a
-// lane: 12.1 and 11.4 us), so a lane takes kPieces at a time, their loads on
-// their way together.
+// the page table to memory, so a lane takes kPieces at a time, their loads on their
+// way together (prompts of 8 requests up to 1024 tokens, both after one another: 19.2 us,
+// with one piece 19.9; 64 requests of 64 tokens 14.7 and 14.8, but one prompt of 512, whose
+// lanes have a piece each either way, 7.2 and 6.1).
 constexpr int kPieces = 4;
 
 // where a piece lies, or nowhere
@@ -200,9 +201,7 @@ __global__ __launch_bounds__(256) void read_fp4_kernel(RowsArgs4 a) {
   }
 }
 
-// A piece to a lane up to 1024 workgroups, then up to kPieces: 64 requests of 64
-// tokens take 7.3 us with four to a lane and 10.1 with one, prompts of 8 requests
-// 10.4 and 14.5; one prompt of 512 tokens 5.1 and 4.3.
+// A piece to a lane up to 1024 workgroups, then up to kPieces.
 dim3 rows_grid(const RowsArgs4& a) {
   const int most = a.max_new < a.tokens ? a.max_new : a.tokens;
   const int64_t all = ((int64_t)most * a.kv_heads * (a.head_dim / 8) + 255) / 256;

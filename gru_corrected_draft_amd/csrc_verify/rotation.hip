@@ -19,8 +19,9 @@
 // Bound by memory: 8191 tokens of 48 heads of 128 take 43 us from call to call, 4.7
 // TB/s (a large copy reaches 4.8 to 5.2), and 35 where the results fall into the same
 // memory each time; a head's elements are loaded one ahead, the first before the
-// angles are formed (46.5 and 41.5 without).  64 blocks of 16 tokens take 7 us
-// on the GPU and one token 4, less than the call on the host, 9.5.
+// angles are formed (46.5 and 41.5 without).  64 blocks of 16 tokens take 6.7 us
+// on the GPU and one token 4.1, less than the call on the host, 9.5.  fp32: 4096 tokens
+// of 48 heads 37 us for 39 of bytes (results in the same memory), 1024 of 40 heads 10.6 for 8.1.
 #include <cmath>
 #include <new>
 
@@ -256,9 +257,9 @@ template <typename T, int D>
 static void launch_rotate(const domino_rotation* h, const RotateArgs& a, hipStream_t st) {
   // Several tokens to a workgroup save starts where a token is little for 256 lanes
   // and there are workgroups enough even so, one, two or four: 40 heads of 128 of
-  // 2048 tokens 10.9, 11.3 and 12.4 us, of 4096 20.0, 18.1 and 18.4, of 8191 34.0, 30.5
-  // and 29.4; 10 heads of 128 of 16000 26.1, 20.6 and 19.7; but 72 of 128 of 16000
-  // 109, 113 and 120.
+  // 2048 tokens 10.2, 10.1 and 10.2 us, of 4096 17.2, 14.9 and 15.0, of 8191 31.8, 30.1
+  // and 28.9; 10 heads of 128 of 16000 21.8, 17.8 and 17.1; but 72 of 128 of 4096 27.6, 26.7
+  // and 28.4, of 16000 109, 113 and 120.
   const int size = a.heads * D;  // of a token
   const int tokens_each = size > 8192 || a.tokens < 2560 ? 1 : a.tokens < 6000 ? 2 : 4;
   const dim3 grid((unsigned)((a.tokens + tokens_each - 1) / tokens_each));

@@ -17,10 +17,12 @@
 // for the few groups that reach them.
 //
 // 1024 rows of 151936 bf16 logits with 5 ids each take 65 us, 4.8 TB/s (a large copy
-// reaches 5.2; vector instructions are busy 75 % of the time), 777 rows of 50257 24.2, of
-// which 8 are start and join of workgroups that live for three steps, one fp32 row of
-// 151936 with 20 ids 11.7, near what the call takes on the host.  Counting n apart takes
-// 0.3 to 1.3 us of each.
+// reaches 5.2; vector instructions are busy 75 % of the time).  777 rows of 50257 take 22.3 for
+// 15.1 of bytes: a row is seven steps in parts of three, three and one, so a third of the
+// workgroups start and join for a step that is mostly past the row's end.  One fp32 row
+// of 151936 with 20 ids takes 11.5, near what the call takes on the host: 19 workgroups
+// of a step each, then the last of them ranks maxima, goes back for the groups and
+// ranks again.  Counting n apart takes 0.3 to 1.3 us of each.
 #include <cmath>
 #include <new>
 
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     if (bar == -INFINITY && groups <= kList) {
       // Fewer groups than ids asked for (a small vocabulary, a mask that leaves ids
       // in few places): a bar from their pieces (100 rows of 1500 with 64 ids
-      // 19.4 us, without it 59.5).
+      // 19.8 us, without it 25.4).
       mine = -INFINITY;
       for (int i = tid; i < groups * 4 * kVectors; i += kThreads) {
         const int id = piece_at(i);
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
       // Many equal logits, or ids in fewer groups than asked for.  The value of
       // the top-th logit is found digit by digit, and among its equals the last id
       // in the same way, each digit by a pass over the row (a row of 151936 ids of
-      // four values 640 us, 300 such rows 1260; bit by bit 2270 and 4250).
+      // four values 648 us, 300 such rows 1268; bit by bit 2270 and 4250).
       uint32_t value = 0;  // of the last logit to take, and its number among its equals
       int left = a.top, equals = 0;
       bool all = false;
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a) {
     int n = min(s_keys_n, kKeys);
     if (n > kThreads) {
       // Many for the ranking, which takes n^2: a bar from the threads' own largest
-      // leaves few (500 rows of 5003 with masks and 64 ids 19.9 us, without it 49.8).
+      // leaves few (500 rows of 5003 with masks and 64 ids 19.9 us, without it 42.8).
       uint64_t mine_keys[kKeys / kThreads];
       mine = -INFINITY;
 #pragma unroll
@@ -572,10 +574,10 @@ extern "C" domino_status_t domino_scores_run(domino_scores_t* h, const void* log
   a.rows = rows;
   a.vocab = f.vocab;
   // Parts of a row, of at least a step each: as many as give each CU eight
-  // workgroups (777 rows of 50257 in 3 parts 22 us, undivided 27).  For the
+  // workgroups (777 rows of 50257 in 3 parts 22.3 us, in 2 25.2, undivided 23.7).  For the
   // likeliest ids four, and none from two rows to a CU on, where the maxima then
-  // stay in LDS (1024 rows of 151936 undivided 65 us, in 2 parts 74; 256 rows in 4
-  // parts and undivided 32).
+  // stay in LDS (1024 rows of 151936 undivided 65.5 us, in 2 parts 78; 256 rows in 4
+  // parts 26.0, undivided 26.8; one fp32 row in 19 11.5, undivided 28).
   // Ranges are whole steps: those of a quarter of one balance better but run
   // steps half empty (777 rows of 50257 27.9).
   const int steps = steps_of(f.vocab);

@@ -191,8 +191,10 @@ domino_status_t domino_attention_run(domino_attention_t* h, const domino_cache_t
  * 6 x 2^e are off by at most half a step of the numbers around them, others by
  * at most 2^e (the largest bf16 numbers, from 7 x 2^125 on, become 6 x 2^125).  Run
  * computes its formula over the numbers that the cache stands for, which bf16
- * holds exactly; blocks of NaN and unseen keys have the effects stated there.  Powers of 2^-126
- * and less may count as zero, blocks of 2^126 and more as NaN. */
+ * holds exactly; blocks of NaN and unseen keys have the effects stated there.
+ * Powers of 2^-126 and less may count as zero, blocks of 2^126 and more as NaN.
+ * In append and read a request's new tokens, by the bounds, times kv_heads and
+ * head_dim stay below 2^33. */
 domino_status_t domino_attention_create_fp4(const domino_attention_config_t* cfg,
                                             domino_attention_t** out);
 
