@@ -39,8 +39,12 @@ hipError_t prepare_fp4() {
 
 // Where row tiles of 16 do not fill the CUs, one workgroup of all the waves that a CU
 // holds to each: 32 single tokens over 2 to 4 thousand keys 27.3 us against 33.8 with
-// workgroups of 4 waves, 8 blocks 21.3 against 29.9.  Beyond that 4 waves, two workgroups
-// to a CU: they leave the wait at the end to others.
+// workgroups of 4 waves, 8 blocks 21.3 against 29.9.  A block's four row tiles convert
+// the same keys each, but fewer of more rows with the keys cut into runs instead are
+// slower: 8 blocks 25.3 us in tiles of 32 rows with 8 waves and two runs, 25.7 with 4
+// waves, 31.6 in tiles of 64.  Beyond that 4 waves, two workgroups to a CU: they leave the
+// wait at the end to others (32 blocks over 8 to 16 thousand keys 201 us, with 8 waves 212;
+// 12 over 2 to 4 thousand 31.0 and 32.0, but 16 of them 38.9 and 32.1).
 template <int D, bool FINE>
 void launch_few_d(const AttendArgs& a, int cus, hipStream_t st) {
   const int64_t rows = (int64_t)a.max_new * a.group;
